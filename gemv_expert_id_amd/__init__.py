@@ -23,11 +23,14 @@ MM_F32, MM_F16, MM_BF16 = 0, 1, 2
 MM_ROUTE_GEMV, MM_ROUTE_GEMM, MM_ROUTE_ID_DIRECT = 0, 1, 2
 MM_ROUTE_ID_MAP, MM_ROUTE_ID_GROUPED, MM_ROUTE_ID_PREFILL = 3, 4, 5
 MM_ROUTE_GEMV_WIDE = 6
+MM_ROUTE_TOPK, MM_ROUTE_SORT, MM_ROUTE_COMBINE, MM_ROUTE_Q4 = 7, 8, 9, 10
 # mm_kernel: kernel family reported in receipts
 (MM_KERNEL_GEMV_ROWS, MM_KERNEL_GEMV_ROWS_ELEM, MM_KERNEL_GEMV_COLS, MM_KERNEL_GEMM_TILED,
  MM_KERNEL_GEMM_LARGE, MM_KERNEL_GEMM_F32, MM_KERNEL_ID_DIRECT_FAST, MM_KERNEL_ID_DIRECT,
  MM_KERNEL_ID_MAP, MM_KERNEL_ID_GROUPED_MFMA, MM_KERNEL_ID_GROUPED_FMA,
- MM_KERNEL_GEMV_WIDE, MM_KERNEL_GEMM_F32_SMALL, MM_KERNEL_GEMM_PANEL) = range(14)
+ MM_KERNEL_GEMV_WIDE, MM_KERNEL_GEMM_F32_SMALL, MM_KERNEL_GEMM_PANEL, MM_KERNEL_TOPK,
+ MM_KERNEL_TOPK_GRAD, MM_KERNEL_SORT_PLAN, MM_KERNEL_SORT_GATHER, MM_KERNEL_COMBINE,
+ MM_KERNEL_COMBINE_GRAD, MM_KERNEL_Q4) = range(21)
 MM_ID_SCHEMA_VERSION = 5
 MM_ID_GROUPED_MAX_EXPERTS = 1024
 
@@ -43,7 +46,10 @@ EXPORTS = [
     "mm_id_grouped",
     "mm_id", "mm_capabilities", "mm_status_string", "mm_last_error",
     "mm_test_inject_resolve_failure", "mm_test_launch_count", "mm_id_prefill_noalloc",
+    "mm_topk", "mm_topk_grad", "mm_id_sort", "mm_id_sort_grad", "mm_id_combine",
+    "mm_id_combine_grad", "mm_q4_gemv", "mm_q4_id_direct", "mm_q4_id_sorted",
 ]
+MM_TOPK_MAX_EXPERTS, MM_TOPK_MAX_SLOTS = 1024, 64
 MM_ID_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -87,6 +93,27 @@ class IdCapability(ctypes.Structure):
                 ("weight_bytes", ctypes.c_uint64), ("input_bytes", ctypes.c_uint64),
                 ("ids_bytes", ctypes.c_uint64), ("output_bytes", ctypes.c_uint64),
                 ("counts_bytes", ctypes.c_uint64), ("routed_rows_bytes", ctypes.c_uint64)]
+
+
+class TopkParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("m", ctypes.c_uint32), ("n_experts", ctypes.c_uint32),
+                ("top_k", ctypes.c_uint32), ("renormalize", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("ld", ctypes.c_int64)]
+
+
+class SortParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("m", ctypes.c_uint32), ("top_k", ctypes.c_uint32),
+                ("n_experts", ctypes.c_uint32), ("width", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("ld_tokens", ctypes.c_int64),
+                ("ld_rows", ctypes.c_int64)]
+
+
+class Q4Params(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("scale_dtype", ctypes.c_int), ("m", ctypes.c_uint32),
+                ("top_k", ctypes.c_uint32), ("n_experts", ctypes.c_uint32),
+                ("n", ctypes.c_uint32), ("k", ctypes.c_uint32), ("group", ctypes.c_uint32),
+                ("gated", ctypes.c_uint32), ("input_layout", ctypes.c_uint32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 class DeviceCaps(ctypes.Structure):
@@ -140,6 +167,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mm_id_prefill_noalloc.argtypes = [P(IdParams), ctypes.c_int, Buf, Buf, Buf, Buf, vp,
                                           P(Receipt)]
     lib.mm_id_prefill_noalloc.restype = st
+    for name, params, n_bufs in (("mm_topk", TopkParams, 3), ("mm_topk_grad", TopkParams, 4),
+                                 ("mm_id_sort", SortParams, 6), ("mm_id_sort_grad", SortParams, 4),
+                                 ("mm_id_combine", SortParams, 6),
+                                 ("mm_id_combine_grad", SortParams, 7),
+                                 ("mm_q4_gemv", Q4Params, 5), ("mm_q4_id_direct", Q4Params, 6),
+                                 ("mm_q4_id_sorted", Q4Params, 6)):
+        fn = getattr(lib, name)
+        fn.argtypes = [P(params)] + [Buf] * n_bufs + [vp, P(Receipt)]
+        fn.restype = st
     lib.mm_capabilities.argtypes = [ctypes.c_int, P(DeviceCaps)]
     lib.mm_capabilities.restype = st
     lib.mm_status_string.argtypes = [ctypes.c_int]
@@ -272,6 +308,96 @@ def mm_id_prefill_noalloc(params: IdParams, weight_dtype: int, weights: Buf, inp
     r = Receipt()
     _raise(load().mm_id_prefill_noalloc(ctypes.byref(params), weight_dtype, weights, inp, ids,
                                         out, _stream(stream), ctypes.byref(r)))
+    return r
+
+
+def topk_params(dtype: int, m: int, n_experts: int, top_k: int, *, renormalize: int = 0,
+                ld: int = 0) -> TopkParams:
+    return TopkParams(dtype, m, n_experts, top_k, int(renormalize), 0, ld)
+
+
+def sort_params(dtype: int, m: int, top_k: int, n_experts: int, width: int, *, ld_tokens: int = 0,
+                ld_rows: int = 0) -> SortParams:
+    return SortParams(dtype, m, top_k, n_experts, width, 0, ld_tokens, ld_rows)
+
+
+def q4_params(dtype: int, scale_dtype: int, m: int, n: int, k: int, group: int, *,
+              n_experts: int = 1, top_k: int = 1, gated: int = 0, input_layout: int = 0,
+              ldx: int = 0, ldy: int = 0) -> Q4Params:
+    return Q4Params(dtype, scale_dtype, m, top_k, n_experts, n, k, group, int(gated), input_layout,
+                    ldx, ldy)
+
+
+def mm_topk(params: TopkParams, logits: Buf, ids: Buf, weights: Buf, stream=None) -> Receipt:
+    """Router: expert ids and weights of each token from its logits."""
+    r = Receipt()
+    _raise(load().mm_topk(params, logits, ids, weights, _stream(stream), r))
+    return r
+
+
+def mm_topk_grad(params: TopkParams, logits: Buf, ids: Buf, dweights: Buf, dlogits: Buf,
+                 stream=None) -> Receipt:
+    r = Receipt()
+    _raise(load().mm_topk_grad(params, logits, ids, dweights, dlogits, _stream(stream), r))
+    return r
+
+
+def mm_id_sort(params: SortParams, x: Buf, ids: Buf, xs: Buf, offsets: Buf, order: Buf,
+               position: Buf, stream=None) -> Receipt:
+    """Token rows in expert order, with the segments' offsets and both permutations."""
+    r = Receipt()
+    _raise(load().mm_id_sort(params, x, ids, xs, offsets, order, position, _stream(stream), r))
+    return r
+
+
+def mm_id_sort_grad(params: SortParams, dxs: Buf, offsets: Buf, position: Buf, dx: Buf,
+                    stream=None) -> Receipt:
+    r = Receipt()
+    _raise(load().mm_id_sort_grad(params, dxs, offsets, position, dx, _stream(stream), r))
+    return r
+
+
+def mm_id_combine(params: SortParams, y: Buf, offsets: Optional[Buf], position: Optional[Buf],
+                  weights: Buf, residual: Optional[Buf], out: Buf, stream=None) -> Receipt:
+    """Weighted expert rows back to tokens; without offsets and position, rows as mm_id writes them."""
+    r = Receipt()
+    none = Buf(None, 0)
+    _raise(load().mm_id_combine(params, y, offsets or none, position or none, weights,
+                                residual or none, out, _stream(stream), r))
+    return r
+
+
+def mm_id_combine_grad(params: SortParams, dout: Buf, y: Buf, offsets: Optional[Buf],
+                       position: Optional[Buf], weights: Buf, dy: Buf, dweights: Buf,
+                       stream=None) -> Receipt:
+    r = Receipt()
+    none = Buf(None, 0)
+    _raise(load().mm_id_combine_grad(params, dout, y, offsets or none, position or none, weights,
+                                     dy, dweights, _stream(stream), r))
+    return r
+
+
+def mm_q4_gemv(params: Q4Params, codes: Buf, scales: Buf, biases: Buf, x: Buf, y: Buf,
+               stream=None) -> Receipt:
+    """Rows of x through one matrix of 4-bit weights."""
+    r = Receipt()
+    _raise(load().mm_q4_gemv(params, codes, scales, biases, x, y, _stream(stream), r))
+    return r
+
+
+def mm_q4_id_direct(params: Q4Params, codes: Buf, scales: Buf, biases: Buf, x: Buf, ids: Buf,
+                    y: Buf, stream=None) -> Receipt:
+    """Each routed row through the expert its id names, 4-bit weights."""
+    r = Receipt()
+    _raise(load().mm_q4_id_direct(params, codes, scales, biases, x, ids, y, _stream(stream), r))
+    return r
+
+
+def mm_q4_id_sorted(params: Q4Params, codes: Buf, scales: Buf, biases: Buf, x: Buf, offsets: Buf,
+                    y: Buf, stream=None) -> Receipt:
+    """Rows sorted by expert (mm_id_sort) through 4-bit weights."""
+    r = Receipt()
+    _raise(load().mm_q4_id_sorted(params, codes, scales, biases, x, offsets, y, _stream(stream), r))
     return r
 
 

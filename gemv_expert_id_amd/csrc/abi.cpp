@@ -530,6 +530,188 @@ mm_status route_hint(mm_dtype weight_dtype, const mm_id_params* params, uint32_t
     return ok();
 }
 
+// ---------------------------------------------------------------------------
+// Mixture-of-experts layer: router, sorted rows, 4-bit products
+// ---------------------------------------------------------------------------
+// Bytes of a [rows, width] tensor with row pitch ld (0 = tight, written back).
+mm_status rows_extent(const char* what, uint64_t rows, uint64_t width, int64_t* ld, uint64_t es,
+                      uint64_t* bytes) {
+    if (*ld == 0) *ld = (int64_t)width;
+    if (*ld < (int64_t)width)
+        return fail(MM_ERR_INVALID_ARGUMENT, "%s: row pitch %lld is below the row length %llu", what,
+                    (long long)*ld, (unsigned long long)width);
+    uint64_t t;
+    if (!mul_ok(rows - 1, (uint64_t)*ld, &t) || !add_ok(t, width, &t) || !mul_ok(t, es, bytes) ||
+        *bytes > (uint64_t)INT64_MAX)
+        return fail(MM_ERR_INVALID_ARGUMENT, "%s: byte extent overflows", what);
+    return MM_OK;
+}
+
+// A buffer of a call: what it must hold, and where it lies once checked.
+struct Operand {
+    const char* label;
+    mm_buf buf;
+    uint64_t bytes, align;
+    bool out;
+    Range range{0, 0};
+};
+
+// Every operand in bounds and aligned; no output meets another operand.
+template <size_t N>
+mm_status check_operands(Operand (&ops)[N]) {
+    mm_status st;
+    for (Operand& o : ops)
+        if (o.label && (st = check_buf(o.label, o.buf, 0, o.bytes, o.align, &o.range)) != MM_OK) return st;
+    for (size_t i = 0; i < N; ++i)
+        for (size_t j = 0; j < N; ++j)
+            if (i != j && ops[i].label && ops[j].label && ops[i].out && overlap(ops[i].range, ops[j].range))
+                return fail(MM_ERR_OVERLAP, "%s must not overlap %s", ops[i].label, ops[j].label);
+    return MM_OK;
+}
+
+// One resolved launch, its error and its receipt.
+template <class F>
+mm_status run_one(const char* family, mm_route route, int dtype, void* stream, mm_receipt* receipt,
+                  F&& launch) {
+    mm_status st = resolve(family);
+    if (st != MM_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    ++g_launches;
+    mmk::Launched L;
+    if ((st = finish(launch(s, &L), s, family)) != MM_OK) return st;
+    set_receipt(receipt, route, (uint32_t)dtype, 1, L);
+    return ok();
+}
+
+mm_status topk_plan(const mm_topk_params* p, mmk::TopkArgs* a, uint64_t* row_bytes) {
+    if (!p) return fail(MM_ERR_INVALID_ARGUMENT, "topk: null params");
+    if (!valid_dtype(p->dtype))
+        return fail(MM_ERR_UNSUPPORTED, "topk: dtype %d is not f32, f16 or bf16", (int)p->dtype);
+    if (!p->m || !p->n_experts || !p->top_k)
+        return fail(MM_ERR_INVALID_ARGUMENT, "topk: m, n_experts and top_k must be nonzero");
+    if (p->renormalize > 1 || p->reserved)
+        return fail(MM_ERR_INVALID_ARGUMENT, "topk: renormalize must be 0 or 1 and reserved 0");
+    if (p->n_experts > MM_TOPK_MAX_EXPERTS || p->top_k > MM_TOPK_MAX_SLOTS)
+        return fail(MM_ERR_UNSUPPORTED, "topk: at most %u experts and %u slots (got %u, %u)",
+                    MM_TOPK_MAX_EXPERTS, MM_TOPK_MAX_SLOTS, p->n_experts, p->top_k);
+    if (p->top_k > p->n_experts)
+        return fail(MM_ERR_INVALID_ARGUMENT, "topk: top_k %u exceeds n_experts %u", p->top_k, p->n_experts);
+    *a = mmk::TopkArgs{};
+    a->ld = p->ld;
+    a->m = p->m;
+    a->n_experts = p->n_experts;
+    a->top_k = p->top_k;
+    a->renormalize = p->renormalize;
+    a->dtype = (int)p->dtype;
+    return rows_extent("topk logits", p->m, p->n_experts, &a->ld, elt_size(p->dtype), row_bytes);
+}
+
+// Extents of the sorted-row calls.
+struct SortSizes {
+    uint64_t es, tokens, rows, offsets, slots;  // bytes
+};
+mm_status sort_plan(const mm_sort_params* p, mmk::SortArgs* a, SortSizes* z) {
+    if (!p) return fail(MM_ERR_INVALID_ARGUMENT, "sorted rows: null params");
+    if (!valid_dtype(p->dtype))
+        return fail(MM_ERR_UNSUPPORTED, "sorted rows: dtype %d is not f32, f16 or bf16", (int)p->dtype);
+    if (!p->m || !p->top_k || !p->n_experts || !p->width)
+        return fail(MM_ERR_INVALID_ARGUMENT, "sorted rows: m, top_k, n_experts and width must be nonzero");
+    if (p->reserved) return fail(MM_ERR_INVALID_ARGUMENT, "sorted rows: reserved must be 0");
+    if (p->n_experts > MM_TOPK_MAX_EXPERTS)
+        return fail(MM_ERR_UNSUPPORTED, "sorted rows: at most %u experts (got %u)", MM_TOPK_MAX_EXPERTS,
+                    p->n_experts);
+    const uint64_t R = (uint64_t)p->m * p->top_k;
+    if (R >= (1ull << 31) || p->width > (1u << 24))
+        return fail(MM_ERR_INVALID_ARGUMENT, "sorted rows: m*top_k must be below 2^31 and width at most 2^24");
+    *a = mmk::SortArgs{};
+    a->m = p->m;
+    a->top_k = p->top_k;
+    a->n_experts = p->n_experts;
+    a->width = p->width;
+    a->dtype = (int)p->dtype;
+    a->ld_tokens = p->ld_tokens;
+    a->ld_rows = p->ld_rows;
+    z->es = elt_size(p->dtype);
+    z->offsets = ((uint64_t)p->n_experts + 1) * 4;
+    z->slots = R * 4;
+    mm_status st = rows_extent("sorted rows: token rows", p->m, p->width, &a->ld_tokens, z->es, &z->tokens);
+    if (st != MM_OK) return st;
+    return rows_extent("sorted rows: expert rows", R, p->width, &a->ld_rows, z->es, &z->rows);
+}
+
+// position and offsets: both, or neither where the call allows that.
+mm_status positions(const char* what, mm_buf offsets, mm_buf position, bool* has) {
+    *has = position.ptr != nullptr;
+    if (*has != (offsets.ptr != nullptr))
+        return fail(MM_ERR_INVALID_ARGUMENT, "%s: position and offsets go together", what);
+    return MM_OK;
+}
+
+mm_status run_q4(mmk::Q4Mode mode, const mm_q4_params* p, mm_buf codes, mm_buf scales, mm_buf biases,
+                 mm_buf x, mm_buf route, mm_buf y, void* stream, mm_receipt* receipt) {
+    if (!p) return fail(MM_ERR_INVALID_ARGUMENT, "q4: null params");
+    if (!valid_dtype(p->dtype))
+        return fail(MM_ERR_UNSUPPORTED, "q4: dtype %d is not f32, f16 or bf16", (int)p->dtype);
+    if (p->scale_dtype != MM_F16 && p->scale_dtype != MM_BF16)
+        return fail(MM_ERR_UNSUPPORTED, "q4: scale dtype %d is not f16 or bf16", (int)p->scale_dtype);
+    if (!p->m || !p->top_k || !p->n_experts || !p->n || !p->k)
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: m, top_k, n_experts, n and k must be nonzero");
+    if (p->group != 32 && p->group != 64 && p->group != 128)
+        return fail(MM_ERR_UNSUPPORTED, "q4: group %u is not 32, 64 or 128", p->group);
+    if (p->k % p->group)
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: k %u is not a multiple of the group %u", p->k, p->group);
+    if (p->gated > 1 || p->input_layout > 1)
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: gated and input_layout must be 0 or 1");
+    if (mode == mmk::Q4_DENSE && (p->n_experts != 1 || p->top_k != 1))
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: the dense product has n_experts = top_k = 1");
+    if (mode != mmk::Q4_IDS && p->input_layout)
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: input_layout is for routed rows by id");
+    if (mode == mmk::Q4_SORTED && p->n_experts > MM_TOPK_MAX_EXPERTS)
+        return fail(MM_ERR_UNSUPPORTED, "q4: sorted rows take at most %u experts (got %u)",
+                    MM_TOPK_MAX_EXPERTS, p->n_experts);
+    const uint64_t R = (uint64_t)p->m * p->top_k;
+    if (R >= (1ull << 31) || p->n > (1u << 24) || p->k > (1u << 24))
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: m*top_k must be below 2^31, n and k at most 2^24");
+    const uint64_t N = (uint64_t)p->n * (1 + p->gated), es = elt_size(p->dtype);
+    uint64_t cells, cbytes, sbytes, xbytes, ybytes;
+    if (!mul_ok(N * p->n_experts, p->k, &cells) || cells > (uint64_t)INT64_MAX)
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4: weight extent overflows");
+    cbytes = cells / 2;
+    sbytes = cells / p->group * 2;
+    mmk::Q4Args a{};
+    a.ldx = p->ldx;
+    a.ldy = p->ldy;
+    const bool shared_x = mode == mmk::Q4_IDS && p->input_layout == 0;
+    mm_status st;
+    if ((st = rows_extent("q4 x", shared_x ? p->m : R, p->k, &a.ldx, es, &xbytes)) != MM_OK) return st;
+    if ((st = rows_extent("q4 y", R, p->n, &a.ldy, es, &ybytes)) != MM_OK) return st;
+    const char* route_label = mode == mmk::Q4_IDS ? "q4 ids" : mode == mmk::Q4_SORTED ? "q4 offsets" : nullptr;
+    const uint64_t route_bytes = mode == mmk::Q4_IDS ? R * 4 : ((uint64_t)p->n_experts + 1) * 4;
+    Operand ops[] = {{"q4 codes", codes, cbytes, 16, false},  {"q4 scales", scales, sbytes, 2, false},
+                     {"q4 biases", biases, sbytes, 2, false}, {"q4 x", x, xbytes, es, false},
+                     {route_label, route, route_bytes, 4, false}, {"q4 y", y, ybytes, es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.codes = static_cast<const uint8_t*>(codes.ptr);
+    a.scales = static_cast<const uint16_t*>(scales.ptr);
+    a.biases = static_cast<const uint16_t*>(biases.ptr);
+    a.x = x.ptr;
+    a.ids = static_cast<const uint32_t*>(route.ptr);
+    a.offsets = static_cast<const uint32_t*>(route.ptr);
+    a.y = y.ptr;
+    a.rows = (uint32_t)R;
+    a.x_div = shared_x ? p->top_k : 1;
+    a.n = p->n;
+    a.k = p->k;
+    a.group = p->group;
+    a.gated = p->gated;
+    a.n_experts = p->n_experts;
+    a.dtype = (int)p->dtype;
+    a.scale_dtype = (int)p->scale_dtype;
+    a.mode = mode;
+    return run_one("q4", MM_ROUTE_Q4, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_q4(a, s, L); });
+}
+
 }  // namespace
 
 extern "C" {
@@ -712,6 +894,168 @@ mm_status mm_id_prefill_noalloc(const mm_id_params* params, mm_dtype weight_dtyp
     if ((st = finish(mmk::launch_id_grouped(a, s, &L), s, "id_grouped")) != MM_OK) return st;
     set_receipt(receipt, MM_ROUTE_ID_PREFILL, (uint32_t)weight_dtype, 2, L);
     return ok();
+}
+
+mm_status mm_topk(const mm_topk_params* params, mm_buf logits, mm_buf ids, mm_buf weights,
+                  void* stream, mm_receipt* receipt) {
+    mmk::TopkArgs a;
+    uint64_t lbytes;
+    mm_status st = topk_plan(params, &a, &lbytes);
+    if (st != MM_OK) return st;
+    const uint64_t slots = (uint64_t)a.m * a.top_k * 4;
+    Operand ops[] = {{"topk logits", logits, lbytes, elt_size(a.dtype), false},
+                     {"topk ids", ids, slots, 4, true},
+                     {"topk weights", weights, slots, 4, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.logits = logits.ptr;
+    a.ids_w = static_cast<uint32_t*>(ids.ptr);
+    a.weights_w = static_cast<float*>(weights.ptr);
+    return run_one("topk", MM_ROUTE_TOPK, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_topk(a, false, s, L); });
+}
+
+mm_status mm_topk_grad(const mm_topk_params* params, mm_buf logits, mm_buf ids, mm_buf dweights,
+                       mm_buf dlogits, void* stream, mm_receipt* receipt) {
+    mmk::TopkArgs a;
+    uint64_t lbytes;
+    mm_status st = topk_plan(params, &a, &lbytes);
+    if (st != MM_OK) return st;
+    const uint64_t slots = (uint64_t)a.m * a.top_k * 4, es = elt_size(a.dtype);
+    Operand ops[] = {{"topk gradient logits", logits, lbytes, es, false},
+                     {"topk gradient ids", ids, slots, 4, false},
+                     {"topk gradient dweights", dweights, slots, 4, false},
+                     {"topk gradient dlogits", dlogits, lbytes, es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.logits = logits.ptr;
+    a.ids = static_cast<const uint32_t*>(ids.ptr);
+    a.dweights = static_cast<const float*>(dweights.ptr);
+    a.dlogits = dlogits.ptr;
+    return run_one("topk_grad", MM_ROUTE_TOPK, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_topk(a, true, s, L); });
+}
+
+mm_status mm_id_sort(const mm_sort_params* params, mm_buf x, mm_buf ids, mm_buf xs, mm_buf offsets,
+                     mm_buf order, mm_buf position, void* stream, mm_receipt* receipt) {
+    mmk::SortArgs a;
+    SortSizes z;
+    mm_status st = sort_plan(params, &a, &z);
+    if (st != MM_OK) return st;
+    Operand ops[] = {{"sort x", x, z.tokens, z.es, false},
+                     {"sort ids", ids, z.slots, 4, false},
+                     {"sort xs", xs, z.rows, z.es, true},
+                     {"sort offsets", offsets, z.offsets, 4, true},
+                     {"sort order", order, z.slots, 4, true},
+                     {"sort position", position, z.slots, 4, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.tokens = x.ptr;
+    a.rows_w = xs.ptr;
+    a.ids = static_cast<const uint32_t*>(ids.ptr);
+    a.offsets = a.offsets_w = static_cast<uint32_t*>(offsets.ptr);
+    a.order = a.order_w = static_cast<uint32_t*>(order.ptr);
+    a.position_w = static_cast<uint32_t*>(position.ptr);
+    if ((st = resolve("sort")) != MM_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    mmk::Launched L;
+    ++g_launches;
+    if ((st = finish(mmk::launch_sort_plan(a, s, &L), s, "sort")) != MM_OK) return st;
+    ++g_launches;
+    if ((st = finish(mmk::launch_sort_gather(a, s, &L), s, "sort")) != MM_OK) return st;
+    set_receipt(receipt, MM_ROUTE_SORT, (uint32_t)a.dtype, 2, L);
+    return ok();
+}
+
+mm_status mm_id_sort_grad(const mm_sort_params* params, mm_buf dxs, mm_buf offsets, mm_buf position,
+                          mm_buf dx, void* stream, mm_receipt* receipt) {
+    mmk::SortArgs a;
+    SortSizes z;
+    mm_status st = sort_plan(params, &a, &z);
+    if (st != MM_OK) return st;
+    Operand ops[] = {{"sort gradient dxs", dxs, z.rows, z.es, false},
+                     {"sort gradient offsets", offsets, z.offsets, 4, false},
+                     {"sort gradient position", position, z.slots, 4, false},
+                     {"sort gradient dx", dx, z.tokens, z.es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.rows = dxs.ptr;
+    a.offsets = static_cast<const uint32_t*>(offsets.ptr);
+    a.position = static_cast<const uint32_t*>(position.ptr);
+    a.tokens_w = dx.ptr;
+    return run_one("sort", MM_ROUTE_SORT, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_combine(a, s, L); });
+}
+
+mm_status mm_id_combine(const mm_sort_params* params, mm_buf y, mm_buf offsets, mm_buf position,
+                        mm_buf weights, mm_buf residual, mm_buf out, void* stream,
+                        mm_receipt* receipt) {
+    mmk::SortArgs a;
+    SortSizes z;
+    mm_status st = sort_plan(params, &a, &z);
+    if (st != MM_OK) return st;
+    bool sorted;
+    if ((st = positions("combine", offsets, position, &sorted)) != MM_OK) return st;
+    // The residual may be the output itself: each element is read, then written, by one lane.
+    const bool in_place = residual.ptr != nullptr && residual.ptr == out.ptr;
+    Operand ops[] = {{"combine y", y, z.rows, z.es, false},
+                     {sorted ? "combine offsets" : nullptr, offsets, z.offsets, 4, false},
+                     {sorted ? "combine position" : nullptr, position, z.slots, 4, false},
+                     {"combine weights", weights, z.slots, 4, false},
+                     {residual.ptr && !in_place ? "combine residual" : nullptr, residual, z.tokens, z.es, false},
+                     {"combine out", out, z.tokens, z.es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    if (in_place) {
+        Range same;
+        if ((st = check_buf("combine residual", residual, 0, z.tokens, z.es, &same)) != MM_OK) return st;
+    }
+    a.rows = y.ptr;
+    a.offsets = static_cast<const uint32_t*>(offsets.ptr);
+    a.position = static_cast<const uint32_t*>(position.ptr);
+    a.weights = static_cast<const float*>(weights.ptr);
+    a.residual = residual.ptr;
+    a.tokens_w = out.ptr;
+    return run_one("combine", MM_ROUTE_COMBINE, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_combine(a, s, L); });
+}
+
+mm_status mm_id_combine_grad(const mm_sort_params* params, mm_buf dout, mm_buf y, mm_buf offsets,
+                             mm_buf position, mm_buf weights, mm_buf dy, mm_buf dweights,
+                             void* stream, mm_receipt* receipt) {
+    mmk::SortArgs a;
+    SortSizes z;
+    mm_status st = sort_plan(params, &a, &z);
+    if (st != MM_OK) return st;
+    bool sorted;
+    if ((st = positions("combine gradient", offsets, position, &sorted)) != MM_OK) return st;
+    Operand ops[] = {{"combine gradient dout", dout, z.tokens, z.es, false},
+                     {"combine gradient y", y, z.rows, z.es, false},
+                     {sorted ? "combine gradient offsets" : nullptr, offsets, z.offsets, 4, false},
+                     {sorted ? "combine gradient position" : nullptr, position, z.slots, 4, false},
+                     {"combine gradient weights", weights, z.slots, 4, false},
+                     {"combine gradient dy", dy, z.rows, z.es, true},
+                     {"combine gradient dweights", dweights, z.slots, 4, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.tokens = dout.ptr;
+    a.rows = y.ptr;
+    a.offsets = static_cast<const uint32_t*>(offsets.ptr);
+    a.position = static_cast<const uint32_t*>(position.ptr);
+    a.weights = static_cast<const float*>(weights.ptr);
+    a.rows_w = dy.ptr;
+    a.dweights_w = static_cast<float*>(dweights.ptr);
+    return run_one("combine_grad", MM_ROUTE_COMBINE, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_combine_grad(a, s, L); });
+}
+
+mm_status mm_q4_gemv(const mm_q4_params* params, mm_buf codes, mm_buf scales, mm_buf biases, mm_buf x,
+                     mm_buf y, void* stream, mm_receipt* receipt) {
+    return run_q4(mmk::Q4_DENSE, params, codes, scales, biases, x, mm_buf{nullptr, 0}, y, stream, receipt);
+}
+
+mm_status mm_q4_id_direct(const mm_q4_params* params, mm_buf codes, mm_buf scales, mm_buf biases,
+                          mm_buf x, mm_buf ids, mm_buf y, void* stream, mm_receipt* receipt) {
+    return run_q4(mmk::Q4_IDS, params, codes, scales, biases, x, ids, y, stream, receipt);
+}
+
+mm_status mm_q4_id_sorted(const mm_q4_params* params, mm_buf codes, mm_buf scales, mm_buf biases,
+                          mm_buf x, mm_buf offsets, mm_buf y, void* stream, mm_receipt* receipt) {
+    return run_q4(mmk::Q4_SORTED, params, codes, scales, biases, x, offsets, y, stream, receipt);
 }
 
 mm_status mm_capabilities(int device, mm_device_caps* out) {

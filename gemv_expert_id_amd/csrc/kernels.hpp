@@ -92,6 +92,66 @@ hipError_t launch_id_direct(const IdArgs& a, hipStream_t s, Launched* L);
 hipError_t launch_id_map(const IdArgs& a, hipStream_t s, Launched* L);
 hipError_t launch_id_grouped(const IdArgs& a, hipStream_t s, Launched* L);
 
+// Router (logits -> ids, weights) and its gradient (logits, ids, dweights ->
+// dlogits).
+struct TopkArgs {
+    const void* logits;
+    const uint32_t* ids;
+    const float* dweights;
+    uint32_t* ids_w;
+    float* weights_w;
+    void* dlogits;
+    int64_t ld;
+    uint32_t m, n_experts, top_k, renormalize;
+    int32_t dtype;
+};
+hipError_t launch_topk(const TopkArgs& a, bool grad, hipStream_t s, Launched* L);
+
+// Sorted rows, their combination and the gradients; each launcher reads the
+// fields it needs. position == nullptr: rows in routed-row order, all live.
+struct SortArgs {
+    const void* tokens;      // [m, width]
+    const void* rows;        // [m * top_k, width]
+    void* tokens_w;
+    void* rows_w;
+    const void* residual;    // [m, width] or null
+    const uint32_t* ids;
+    const uint32_t* offsets;
+    const uint32_t* order;
+    const uint32_t* position;
+    uint32_t* offsets_w;
+    uint32_t* order_w;
+    uint32_t* position_w;
+    const float* weights;
+    float* dweights_w;
+    int64_t ld_tokens, ld_rows;
+    uint32_t m, top_k, n_experts, width;  // m * top_k < 2^31
+    int32_t dtype;
+};
+hipError_t launch_sort_plan(const SortArgs& a, hipStream_t s, Launched* L);
+hipError_t launch_sort_gather(const SortArgs& a, hipStream_t s, Launched* L);
+hipError_t launch_combine(const SortArgs& a, hipStream_t s, Launched* L);
+hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s, Launched* L);
+
+// Products with 4-bit weights; `mode` says where a block's rows come from.
+enum Q4Mode { Q4_DENSE = 0, Q4_IDS = 1, Q4_SORTED = 2 };
+struct Q4Args {
+    const uint8_t* codes;
+    const uint16_t* scales;
+    const uint16_t* biases;
+    const void* x;
+    const uint32_t* ids;      // Q4_IDS
+    const uint32_t* offsets;  // Q4_SORTED
+    void* y;
+    int64_t ldx, ldy;
+    uint32_t rows;            // rows of y
+    uint32_t x_div;           // Q4_IDS: x row of routed row r is r / x_div
+    uint32_t n, k, group, gated, n_experts;
+    uint32_t tiles;           // set by the launcher: row tiles of the grid
+    int32_t dtype, scale_dtype, mode;
+};
+hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L);
+
 // Library-held scratch for the allocation-free prefill call: its size, and
 // its device address on the GPU of stream `s` (looked up once per GPU).
 constexpr uint64_t kStaticScratchBytes = MM_ID_NOALLOC_SCRATCH_BYTES;

@@ -78,7 +78,11 @@ typedef enum {
     MM_ROUTE_ID_MAP = 3,
     MM_ROUTE_ID_GROUPED = 4,
     MM_ROUTE_ID_PREFILL = 5, /* map + grouped in one call */
-    MM_ROUTE_GEMV_WIDE = 6   /* skinny product: 2..64 rows on one side */
+    MM_ROUTE_GEMV_WIDE = 6,  /* skinny product: 2..64 rows on one side */
+    MM_ROUTE_TOPK = 7,       /* router, and its gradient */
+    MM_ROUTE_SORT = 8,       /* rows in expert order, and the gradient */
+    MM_ROUTE_COMBINE = 9,    /* expert rows back to tokens, and the gradient */
+    MM_ROUTE_Q4 = 10         /* products with 4-bit weights */
 } mm_route;
 
 /* Kernel family of a launch (reported in receipts; the choice depends on
@@ -97,7 +101,14 @@ typedef enum {
     MM_KERNEL_ID_GROUPED_FMA = 10,   /* grouped pass, FMA tiles (other f16/f32 layouts) */
     MM_KERNEL_GEMV_WIDE = 11,        /* skinny route, one to four 16 x 16 MFMA fragments per block */
     MM_KERNEL_GEMM_F32_SMALL = 12,   /* f32, k <= 128, few tiles: one wave per 16 x 16 f32 MFMA tile */
-    MM_KERNEL_GEMM_PANEL = 13        /* NT, k in {32, 64, 128}: 64- or 128-row A panel in LDS, B tiles streamed */
+    MM_KERNEL_GEMM_PANEL = 13,       /* NT, k in {32, 64, 128}: 64- or 128-row A panel in LDS, B tiles streamed */
+    MM_KERNEL_TOPK = 14,             /* router */
+    MM_KERNEL_TOPK_GRAD = 15,        /* router gradient */
+    MM_KERNEL_SORT_PLAN = 16,        /* offsets, order and position */
+    MM_KERNEL_SORT_GATHER = 17,      /* sorted rows (with the plan, when in one launch) */
+    MM_KERNEL_COMBINE = 18,          /* weighted sum of expert rows (and mm_id_sort_grad) */
+    MM_KERNEL_COMBINE_GRAD = 19,     /* its gradients */
+    MM_KERNEL_Q4 = 20                /* 4-bit weights on MFMA */
 } mm_kernel;
 
 typedef struct {
@@ -355,6 +366,187 @@ mm_status mm_id_prefill_noalloc(const mm_id_params *params, mm_dtype weight_dtyp
                                 void *stream, mm_receipt *receipt);
 
 /* ------------------------------------------------------------------------ */
+/* Mixture-of-experts layer around the expert-ID products                    */
+/* ------------------------------------------------------------------------ */
+/*
+ * The operators of one layer, in the order a program calls them:
+ *   mm_topk         router logits -> expert ids and weights of each token
+ *   mm_id_sort      token rows -> rows in expert order
+ *   (products over the sorted rows: mm_q4_id_sorted, or mm_gemm by segment)
+ *   mm_id_combine   expert rows -> tokens, weighted, onto the residual
+ * and their gradients (the 4-bit products are for serving and have none).
+ * Expert ids are u32 [m, top_k] as in the expert-ID matmul above: an id
+ * outside the expert count marks a slot without an expert, and the routed row
+ * of token t, slot s is r = t*top_k + s. Every dimension must be >= 1.
+ * Pitches (ld*) are elements between rows, 0 = tight, else at least the row
+ * length. Buffers need only their element's alignment unless stated; outputs
+ * may overlap no input and no other output (OVERLAP) unless stated. No call
+ * uses scratch, allocates, or adds with global atomics: results do not depend
+ * on timing, and every call can be captured into a graph.
+ */
+
+/* Largest expert count and slots per token of mm_topk, and largest expert
+ * count of the sorted rows. */
+#define MM_TOPK_MAX_EXPERTS 1024u
+#define MM_TOPK_MAX_SLOTS 64u
+
+typedef struct {
+    mm_dtype dtype;          /* logits (and dlogits): f32, f16 or bf16 */
+    uint32_t m;              /* tokens */
+    uint32_t n_experts;      /* <= MM_TOPK_MAX_EXPERTS */
+    uint32_t top_k;          /* <= n_experts and <= MM_TOPK_MAX_SLOTS */
+    uint32_t renormalize;    /* 0: softmax over all experts; 1: over the chosen */
+    uint32_t reserved;       /* 0 */
+    int64_t ld;              /* row pitch of logits and dlogits */
+} mm_topk_params;
+
+/*
+ * Router. For each token t, with p the softmax of its logits over the experts:
+ *   ids[t][s]     = the expert of the s-th largest logit, equal logits in
+ *                   ascending expert order
+ *   weights[t][s] = p[ids[t][s]]                        (renormalize = 0)
+ *                   p[ids[t][s]] / sum_s' p[ids[t][s']]  (renormalize = 1)
+ * A logit of -inf masks its expert: it is never chosen and adds nothing. When
+ * fewer than top_k experts are left, the remaining slots get id 0xFFFFFFFF
+ * and weight +0. A NaN logit is never chosen and makes the weights of the
+ * token's chosen experts NaN, in both forms; so does a +inf logit, as inf -
+ * inf in the softmax's exponent. Buffers: logits dtype [m, n_experts], ids
+ * u32 [m, top_k], weights f32 [m, top_k].
+ */
+mm_status mm_topk(const mm_topk_params *params, mm_buf logits, mm_buf ids, mm_buf weights,
+                  void *stream, mm_receipt *receipt);
+
+/*
+ * Gradient of mm_topk's weights to the logits, with the choice held fixed.
+ * With g the gradient scattered to the chosen experts (0 elsewhere) and p the
+ * softmax over all experts (renormalize = 0) or over the chosen (1, p = 0
+ * elsewhere):
+ *   dlogits[t][e] = p[e] * (g[e] - sum_e' g[e'] * p[e'])
+ * Slots whose id is outside the expert count are skipped, whatever their
+ * gradient holds; a token without any gets a row of +0. dlogits is written
+ * whole. The ids of one token must be distinct, as mm_topk gives them. Buffers:
+ * logits and dlogits dtype [m, n_experts], ids u32 and dweights f32 [m, top_k].
+ */
+mm_status mm_topk_grad(const mm_topk_params *params, mm_buf logits, mm_buf ids, mm_buf dweights,
+                       mm_buf dlogits, void *stream, mm_receipt *receipt);
+
+typedef struct {
+    mm_dtype dtype;          /* token rows and expert rows: f32, f16 or bf16 */
+    uint32_t m, top_k;       /* tokens, slots per token; m*top_k < 2^31 */
+    uint32_t n_experts;      /* <= MM_TOPK_MAX_EXPERTS */
+    uint32_t width;          /* elements of a row */
+    uint32_t reserved;       /* 0 */
+    int64_t ld_tokens;       /* row pitch of the [m, width] tensors */
+    int64_t ld_rows;         /* row pitch of the [m*top_k, width] tensors */
+} mm_sort_params;
+
+/*
+ * Token rows in expert order (a stable counting sort of the routed rows).
+ * With the routed rows ordered by expert, rows of one expert in ascending r,
+ * and rows without an expert last:
+ *   offsets[e]  = first place of expert e's rows; offsets[n_experts] = number
+ *                 of rows that have an expert           (u32 [n_experts + 1])
+ *   order[i]    = routed row at place i                  (u32 [m*top_k])
+ *   position[r] = place of routed row r                  (u32 [m*top_k])
+ *   xs[i][:]    = x[order[i] / top_k][:], or +0 for i >= offsets[n_experts]
+ * Ids may repeat within a token. x is dtype [m, width], xs dtype
+ * [m*top_k, width].
+ */
+mm_status mm_id_sort(const mm_sort_params *params, mm_buf x, mm_buf ids, mm_buf xs,
+                     mm_buf offsets, mm_buf order, mm_buf position, void *stream,
+                     mm_receipt *receipt);
+
+/*
+ * Gradient of mm_id_sort's rows to the tokens, with offsets and position as
+ * mm_id_sort wrote them:
+ *   dx[t][:] = sum over the slots s of t with position < offsets[n_experts]
+ *              of dxs[position[t*top_k + s]][:]
+ * summed in f32 in ascending s and rounded once; +0 for a token without an
+ * expert. Rows of dxs past offsets[n_experts] are not read.
+ */
+mm_status mm_id_sort_grad(const mm_sort_params *params, mm_buf dxs, mm_buf offsets,
+                          mm_buf position, mm_buf dx, void *stream, mm_receipt *receipt);
+
+/*
+ * Expert rows back to tokens:
+ *   out[t][:] = residual[t][:] + sum_s weights[t][s] * y[position[t*top_k + s]][:]
+ * over the slots whose position is below offsets[n_experts]; in f32, rounded
+ * once. A slot without an expert is skipped: neither its weight nor any row is
+ * read for it. y is dtype [m*top_k, width], weights f32 [m, top_k].
+ * Optional buffers ({NULL, 0}):
+ *   residual    without it the sum starts at +0; out may be the same buffer as
+ *               residual (same address and pitch), but not overlap it otherwise
+ *   position with offsets   without both, y is in routed-row order as mm_id
+ *               writes it and every slot counts (mm_id gives +0 rows where a
+ *               slot has no expert); one without the other is INVALID_ARGUMENT
+ */
+mm_status mm_id_combine(const mm_sort_params *params, mm_buf y, mm_buf offsets, mm_buf position,
+                        mm_buf weights, mm_buf residual, mm_buf out, void *stream,
+                        mm_receipt *receipt);
+
+/*
+ * Gradients of mm_id_combine (the residual's gradient is dout itself). For
+ * each routed row r = t*top_k + s at place i = position[r] (i = r without
+ * position and offsets):
+ *   dy[i][:]       = weights[t][s] * dout[t][:]     rounded once
+ *   dweights[t][s] = sum_j dout[t][j] * y[i][j]      in f32
+ * and +0 in both for rows without an expert (y is not read there), so both are
+ * written whole. dout is dtype [m, width], y and dy dtype [m*top_k, width]
+ * with one pitch, weights and dweights f32 [m, top_k].
+ */
+mm_status mm_id_combine_grad(const mm_sort_params *params, mm_buf dout, mm_buf y, mm_buf offsets,
+                             mm_buf position, mm_buf weights, mm_buf dy, mm_buf dweights,
+                             void *stream, mm_receipt *receipt);
+
+/*
+ * Products with 4-bit weights. A matrix of N rows of k is held as
+ *   codes   4 bits each, q(j, p) the nibble p % 2 (0 = low) of byte p / 2 of
+ *           row j: N*k/2 bytes, rows tight
+ *   scales, biases   f16 or bf16 [N, k/group], one pair for each group of
+ *           `group` neighbouring elements of a row
+ * and stands for W[j][p] = scales[j][p/group] * q(j, p) + biases[j][p/group].
+ * N = n, or 2n for the gated form, whose first n rows G and last n rows U give
+ *   y[r][j] = silu(G[j] . x) * (U[j] . x),   silu(a) = a / (1 + exp(-a)).
+ * Otherwise y[r][j] = W[j] . x. Sums are f32; nothing of the weights is
+ * rounded, f32 activations are used to their full 24 bits, and the result is
+ * rounded once to the dtype. n_experts matrices lie one after the other in
+ * each of the three buffers. Activations must be finite and below 2^120 in
+ * magnitude: with others the row's results are unspecified (other rows are not
+ * affected).
+ */
+typedef struct {
+    mm_dtype dtype;          /* x and y: f32, f16 or bf16 */
+    mm_dtype scale_dtype;    /* scales and biases: f16 or bf16 */
+    uint32_t m;              /* tokens */
+    uint32_t top_k;          /* rows per token; 1 for mm_q4_gemv */
+    uint32_t n_experts;      /* 1 for mm_q4_gemv; <= 1024 for mm_q4_id_sorted */
+    uint32_t n, k;           /* outputs of a row; k a multiple of group */
+    uint32_t group;          /* 32, 64 or 128 */
+    uint32_t gated;          /* 0 or 1 */
+    uint32_t input_layout;   /* mm_q4_id_direct: 0 shared per token, 1 slotted */
+    int64_t ldx, ldy;        /* row pitches of x and y */
+} mm_q4_params;
+
+/* One matrix: y[i] = W . x[i] for i < m. The codes must be 16-byte aligned
+ * here and below. */
+mm_status mm_q4_gemv(const mm_q4_params *params, mm_buf codes, mm_buf scales, mm_buf biases,
+                     mm_buf x, mm_buf y, void *stream, mm_receipt *receipt);
+
+/* One expert for each routed row, as in mm_id_direct: y[r] = W_ids[r] . x[r /
+ * top_k] (input_layout 0, x [m, k]) or . x[r] (1, x [m*top_k, k]); +0 rows and
+ * no weight address where the id is outside the expert count. For few rows:
+ * an expert that several rows name is read for each of them. */
+mm_status mm_q4_id_direct(const mm_q4_params *params, mm_buf codes, mm_buf scales, mm_buf biases,
+                          mm_buf x, mm_buf ids, mm_buf y, void *stream, mm_receipt *receipt);
+
+/* Rows sorted by expert, with mm_id_sort's offsets: y[i] = W_e . x[i] for
+ * offsets[e] <= i < offsets[e + 1], and +0 rows from offsets[n_experts] on. x
+ * is [m*top_k, k]. Offsets that descend or pass m*top_k are cut, so no access
+ * leaves the buffers; the output is then unspecified. */
+mm_status mm_q4_id_sorted(const mm_q4_params *params, mm_buf codes, mm_buf scales, mm_buf biases,
+                          mm_buf x, mm_buf offsets, mm_buf y, void *stream, mm_receipt *receipt);
+
+/* ------------------------------------------------------------------------ */
 /* Device and library information                                            */
 /* ------------------------------------------------------------------------ */
 
@@ -395,8 +587,8 @@ const char *mm_last_error(void);
 
 /* Make the next launch-resolution step on this thread fail for the kernel
  * family `name` ("gemv", "gemv_wide", "gemm", "id_direct", "id_map",
- * "id_grouped"), before
- * anything is enqueued, like the pipeline-lookup failure injected in
+ * "id_grouped", "topk", "topk_grad", "sort", "combine", "combine_grad", "q4"),
+ * before anything is enqueued, like the pipeline-lookup failure injected in
  * mlx-native's `grouped_pipeline_resolution_failure_does_not_mutate_encoder`.
  * NULL clears it. */
 void mm_test_inject_resolve_failure(const char *name);
