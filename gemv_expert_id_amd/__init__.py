@@ -29,7 +29,7 @@ MM_ROUTE_TOPK, MM_ROUTE_SORT, MM_ROUTE_COMBINE, MM_ROUTE_Q4 = 7, 8, 9, 10
  MM_KERNEL_GEMM_LARGE, MM_KERNEL_GEMM_F32, MM_KERNEL_ID_DIRECT_FAST, MM_KERNEL_ID_DIRECT,
  MM_KERNEL_ID_MAP, MM_KERNEL_ID_GROUPED_MFMA, MM_KERNEL_ID_GROUPED_FMA,
  MM_KERNEL_GEMV_WIDE, MM_KERNEL_GEMM_F32_SMALL, MM_KERNEL_GEMM_PANEL, MM_KERNEL_TOPK,
- MM_KERNEL_TOPK_GRAD, MM_KERNEL_SORT_PLAN, MM_KERNEL_SORT_GATHER, MM_KERNEL_COMBINE,
+ MM_KERNEL_TOPK_GRAD, MM_KERNEL_SORT_PLAN, MM_KERNEL_SORT_ROWS, MM_KERNEL_COMBINE,
  MM_KERNEL_COMBINE_GRAD, MM_KERNEL_Q4) = range(21)
 MM_ID_SCHEMA_VERSION = 5
 MM_ID_GROUPED_MAX_EXPERTS = 1024

@@ -684,6 +684,8 @@ mm_status run_q4(mmk::Q4Mode mode, const mm_q4_params* p, mm_buf codes, mm_buf s
     const bool shared_x = mode == mmk::Q4_IDS && p->input_layout == 0;
     mm_status st;
     if ((st = rows_extent("q4 x", shared_x ? p->m : R, p->k, &a.ldx, es, &xbytes)) != MM_OK) return st;
+    if (a.ldx >= (1 << 25))
+        return fail(MM_ERR_INVALID_ARGUMENT, "q4 x: row pitch %lld is not below 2^25", (long long)a.ldx);
     if ((st = rows_extent("q4 y", R, p->n, &a.ldy, es, &ybytes)) != MM_OK) return st;
     const char* route_label = mode == mmk::Q4_IDS ? "q4 ids" : mode == mmk::Q4_SORTED ? "q4 offsets" : nullptr;
     const uint64_t route_bytes = mode == mmk::Q4_IDS ? R * 4 : ((uint64_t)p->n_experts + 1) * 4;
@@ -952,15 +954,18 @@ mm_status mm_id_sort(const mm_sort_params* params, mm_buf x, mm_buf ids, mm_buf 
     a.ids = static_cast<const uint32_t*>(ids.ptr);
     a.offsets = a.offsets_w = static_cast<uint32_t*>(offsets.ptr);
     a.order = a.order_w = static_cast<uint32_t*>(order.ptr);
-    a.position_w = static_cast<uint32_t*>(position.ptr);
+    a.position = a.position_w = static_cast<uint32_t*>(position.ptr);
     if ((st = resolve("sort")) != MM_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     mmk::Launched L;
+    const int launches = mmk::sort_launches(a);
+    if (launches == 2) {
+        ++g_launches;
+        if ((st = finish(mmk::launch_sort_plan(a, s, &L), s, "sort")) != MM_OK) return st;
+    }
     ++g_launches;
-    if ((st = finish(mmk::launch_sort_plan(a, s, &L), s, "sort")) != MM_OK) return st;
-    ++g_launches;
-    if ((st = finish(mmk::launch_sort_gather(a, s, &L), s, "sort")) != MM_OK) return st;
-    set_receipt(receipt, MM_ROUTE_SORT, (uint32_t)a.dtype, 2, L);
+    if ((st = finish(mmk::launch_sort_rows(a, s, &L), s, "sort")) != MM_OK) return st;
+    set_receipt(receipt, MM_ROUTE_SORT, (uint32_t)a.dtype, (uint32_t)launches, L);
     return ok();
 }
 

@@ -1,31 +1,32 @@
 // Products with 4-bit weights and group scales, y = sum over groups of
 // s * (q . x) + b * sum(x), on matrix instructions.
 //
-// A wave takes TN tiles of 16 rows of W and a contiguous piece of k, 128
-// elements (64 bytes of codes a row) at a step: lane l loads the 16 bytes at
-// chunk l / 16 of row l % 16. The W waves of a block take the pieces of k and
-// join their sums through LDS. The codes are the B operand of
-// v_mfma_f32_16x16x32 (column = row of W), the activations the A operand (row =
-// token):
+// A wave reads tiles of 16 rows of W, 128 elements of k (64 bytes of codes a
+// row) at a step: lane l loads the 16 bytes at chunk l / 16 of row l % 16. The
+// codes are the B operand of v_mfma_f32_16x16x32 (column = row of W), the
+// activations the A operand (row = token):
 //   - A code becomes an operand by placing its four bits in the mantissa of
 //     16.0, which is 16 + q, exact in f16 and bf16: one shift and one
-//     and-or for two codes, no conversion. The 16 is taken back with the
-//     group's sum of x, which the same instruction gives from a constant
-//     operand: D0 = (-16) . x, so q . x = (16 + q) . x + D0 and
-//     b * sum(x) = (-b / 16) * D0. Scales enter in f32 after a group's
-//     instructions, so no weight is ever rounded.
-//   - One instruction must stay inside a group. Its four lane groups hold the
-//     four 32-element chunks, so for groups of 64 two, for groups of 32 four
-//     lane-half swaps (v_permlane32_swap, v_permlane16_swap) exchange words
-//     between the lane groups first.
+//     and-or for two codes, no conversion. With the group's sum of x, which the
+//     same instruction gives from a constant operand, s (q . x) + b sum(x) =
+//     s ((16 + q) . x) + (b - 16 s) sum(x). Scales enter in f32 after a
+//     group's instructions, so no weight is ever rounded.
 //   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact) that
 //     accumulate into one result.
-// MI = 1 is for up to 4 tokens: token v is row 4v of the A operand, so each
-// lane has one live result instead of four, and the scaling costs a quarter.
-// MI = 4 takes 16 tokens. Each wave stages its own piece of x in LDS, in the
-// element order that the unpacking gives the codes; no barrier until the join.
-// The loads of the next chunk (activations, codes, scales) are issued before
-// the current one is computed.
+//   - A sum must not leave its group. The four lane groups of an instruction
+//     hold the step's four 32-element chunks. With up to 4 tokens (MI = 1) the A
+//     operand has 16 rows for 4 tokens: row 4v + g holds token v in lane group g
+//     and zeros in the others, so the four results of a lane are the four
+//     chunks' sums. With 16 tokens (MI = 4) lane-half swaps
+//     (v_permlane32_swap, v_permlane16_swap) first exchange words between the
+//     lane groups, two for groups of 64, four for groups of 32.
+//
+// q4_split (few blocks): the W waves of a block take pieces of k for the same
+// rows, each stages its own piece of x in LDS, and the sums are joined there;
+// no barrier until then. q4_block (many rows and tokens): the waves take
+// different rows of W and share x, staged a chunk of k at a time in two buffers,
+// one barrier a chunk. Both issue the loads of the next chunk before computing
+// the current one.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -43,7 +44,7 @@ struct __attribute__((packed, aligned(sizeof(S)))) QChunk {
 // Operand format of the codes and the activations.
 struct CoreF16 {
     static constexpr uint32_t kSixteen = 0x4C004C00u;
-    static constexpr uint32_t kMinusSixteen = 0xCC00CC00u;
+    static constexpr uint32_t kOne = 0x3C003C00u;
     static constexpr int kShift = 6;  // the code's place in the mantissa of 16.0
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
@@ -52,7 +53,7 @@ struct CoreF16 {
 };
 struct CoreBF16 {
     static constexpr uint32_t kSixteen = 0x41804180u;
-    static constexpr uint32_t kMinusSixteen = 0xC180C180u;
+    static constexpr uint32_t kOne = 0x3F803F80u;
     static constexpr int kShift = 3;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -99,10 +100,6 @@ __device__ __forceinline__ void octet(const u32x4* in, u32x4* out) {
     }
 }
 
-__device__ __forceinline__ float scale_value(uint16_t h, bool bf16) {
-    return bf16 ? widen(TBF16{}, h) : widen(TF16{}, h);
-}
-
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
     a = r[0];
@@ -137,6 +134,19 @@ __device__ __forceinline__ void load_pairs(const uint16_t* p, uint32_t* r) {
     }
 }
 
+// Inclusive sum over the lanes up to this one: within rows of 16 lanes, then
+// each row's last lane onto the rows after it.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    int x = (int)v;
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);  // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);  // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);  // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31
+    return (uint32_t)x;
+}
+
 // Row tile `tile` of sorted rows: its expert, first row and row count (0: none).
 // Every wave walks the experts' tile counts, 64 experts at a time.
 template <int VT>
@@ -152,12 +162,7 @@ __device__ __forceinline__ void find_tile(const Q4Args& a, uint32_t tile, int la
         }
         hi = hi < a.rows ? hi : a.rows;
         const uint32_t n = lo < hi ? (hi - lo + VT - 1) / VT : 0;
-        uint32_t upto = n;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const uint32_t v = (uint32_t)__shfl_up((int)upto, o, kWave);
-            if (lane >= o) upto += v;
-        }
+        const uint32_t upto = wave_scan(n);
         const uint64_t past = __ballot(tile < before + upto);
         if (past) {
             const int f = __ffsll((unsigned long long)past) - 1;
@@ -173,261 +178,432 @@ __device__ __forceinline__ void find_tile(const Q4Args& a, uint32_t tile, int la
     *cnt = 0;
 }
 
-template <class T, int GROUP, int MI, bool GATED, int TN, int W>
-__global__ __launch_bounds__(W* kWave) void q4_rows(Q4Args a) {
-    using S = typename T::store_t;
-    using C = typename CoreOf<T>::type;
-    constexpr int PARTS = T::code == 0 ? 3 : 1;
-    constexpr int VT = MI == 1 ? 4 : 16;                                        // tokens of a pass
-    constexpr int CS = MI == 1 ? (PARTS == 3 ? 2 : 4) : (PARTS == 3 ? 1 : 2);   // steps of a chunk
-    constexpr int NT = GATED ? 2 * TN : TN;       // tiles of 16 weight rows
-    constexpr int GPS = QStep / GROUP;            // groups of a step
-    constexpr int NV = CS * GPS;                  // groups of a chunk
-    constexpr int SR = NV == 1 ? 1 : NV / 2;      // registers of their scales
-    constexpr int OCT = CS * QStep / 8;           // octets of a token's chunk
-    constexpr int XL = VT * OCT / kWave;          // octets a lane stages
-    constexpr int PITCH = OCT + 1;                // in 16-byte units; odd: banks
-    __shared__ u32x4 xs[W][PARTS][VT][PITCH];
-    __shared__ float join[W][NT][VT][17];
-
+// The rows of x and y that a block takes, and their expert. A block without
+// rows (or whose rows have no expert: written as zeros here) has cnt = 0.
+struct Rows {
+    uint32_t expert, row0, cnt;
+};
+// VT: tokens of a tile; COLS: output columns of a block of THREADS, from n0 on.
+template <class S, int VT, int COLS, int THREADS>
+__device__ __forceinline__ Rows block_rows(const Q4Args& a, uint32_t n0) {
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r16 = lane & 15, c = lane >> 4;
-    const uint32_t n0 = blockIdx.x * (16 * TN);
     const uint32_t tile = blockIdx.z * gridDim.y + blockIdx.y;
-    if (tile >= a.tiles) return;
-    const bool sbf = a.scale_dtype == 2;
-    const uint32_t N = GATED ? 2 * a.n : a.n;
-    const uint32_t G = a.k / GROUP;
-    // This wave's steps of k.
-    const uint32_t steps = (a.k + QStep - 1) / QStep;
-    const uint32_t st0 = steps * wave / W, st1 = steps * (wave + 1) / W;
-
-    // Where this block's rows come from.
-    uint32_t expert = 0, row0 = 0, cnt = 0;
+    Rows r{0, 0, 0};
+    if (tile >= a.tiles) return r;
+    S* const y = static_cast<S*>(a.y);
     if (a.mode == Q4_DENSE) {
-        row0 = tile * VT;
-        cnt = a.rows - row0 < VT ? a.rows - row0 : VT;
+        r.row0 = tile * VT;
+        r.cnt = a.rows - r.row0 < VT ? a.rows - r.row0 : VT;
     } else if (a.mode == Q4_IDS) {
-        row0 = tile;
-        cnt = 1;
-        expert = a.ids[row0];
+        r.row0 = tile;
+        r.expert = a.ids[tile];
+        r.cnt = r.expert < a.n_experts;
+        if (!r.cnt) {
+            for (uint32_t j = threadIdx.x; j < COLS; j += THREADS)
+                if (n0 + j < a.n) y[(int64_t)tile * a.ldy + n0 + j] = 0;
+        }
     } else {
-        find_tile<VT>(a, tile, lane, &expert, &row0, &cnt);
+        find_tile<VT>(a, tile, lane, &r.expert, &r.row0, &r.cnt);
         // Rows past the last expert's are zeros; the first tile's block writes them.
         if (tile == 0) {
-            const uint32_t live = a.offsets[a.n_experts];
-            for (uint64_t i = (uint64_t)live + wave; i < a.rows; i += W) {
-                if (lane < 16 * TN && n0 + lane < a.n) static_cast<S*>(a.y)[i * a.ldy + n0 + lane] = 0;
-            }
+            for (uint64_t i = a.offsets[a.n_experts]; i < a.rows; ++i)
+                for (uint32_t j = threadIdx.x; j < COLS; j += THREADS)
+                    if (n0 + j < a.n) y[i * a.ldy + n0 + j] = 0;
         }
-        if (cnt == 0) return;
     }
-    S* const y = static_cast<S*>(a.y) + (int64_t)row0 * a.ldy;
-    if (a.mode == Q4_IDS && expert >= a.n_experts) {
-        if (threadIdx.x < 16 * TN && n0 + threadIdx.x < a.n) y[n0 + threadIdx.x] = 0;
-        return;
-    }
-    const S* const x = static_cast<const S*>(a.x) +
-                       (int64_t)(a.mode == Q4_IDS ? row0 / a.x_div : row0) * a.ldx;
+    return r;
+}
 
-    // This lane's weight row in each tile (gate tiles, then up tiles); rows past
-    // n repeat the last and are not stored.
-    const uint8_t* codes[NT];
-    const uint16_t *sc[NT], *bi[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const uint32_t j0 = n0 + (t % TN) * 16 + r16;
-        const uint32_t j = (j0 < a.n ? j0 : a.n - 1) + (t / TN) * a.n;
-        const uint64_t row = (uint64_t)expert * N + j;
-        codes[t] = a.codes + row * (a.k / 2);
-        sc[t] = a.scales + row * G;
-        bi[t] = a.biases + row * G;
-    }
-    // The token whose activations this lane reads as row r16 of the A operand;
-    // rows past the last token repeat it and are not stored.
-    const int tok = MI == 1 ? r16 >> 2 : r16;
-    const int vtok = tok < (int)cnt ? tok : (int)cnt - 1;
+// Sums of NT tiles of 16 weight rows over a range of k: the operands' places,
+// the loads of a chunk of CS steps, and its arithmetic.
+template <class T, class ST, int GROUP, int MI, int NT, int CS>
+struct Tiles {
+    using S = typename T::store_t;
+    using C = typename CoreOf<T>::type;
+    static constexpr int PARTS = T::code == 0 ? 3 : 1;
+    static constexpr int VT = MI == 1 ? 4 : 16;             // tokens
+    static constexpr bool MASKED = MI == 1 && GROUP < QStep;
+    static constexpr int ROWS = MASKED ? VT + 1 : VT;       // staged rows: a last one of zeros
+    static constexpr int GPS = QStep / GROUP;               // groups of a step
+    static constexpr int NV = CS * GPS;                     // groups of a chunk
+    static constexpr int SR = NV == 1 ? 1 : NV / 2;         // registers of their scales
+    static constexpr int OCT = CS * QStep / 8;              // octets of a token's chunk
+    static constexpr int PITCH = OCT + 1;                   // in 16-byte units; odd: banks
+    static constexpr int XR = PARTS == 3 ? 2 : 1;           // 16-byte loads of an octet
+    using Stage = u32x4[PARTS][ROWS][PITCH];
 
-    struct Chunk {
-        u32x4 x[XL][PARTS == 3 ? 2 : 1];
+    struct Codes {
         u32x4 w[CS][NT];
         uint32_t s[NT][SR], b[NT][SR];
     };
-    const auto load = [&](Chunk& q, uint32_t s0) {
+
+    const uint8_t* codes[NT];      // first row of each tile, the same for the wave
+    const uint16_t *sc[NT], *bi[NT];
+    uint32_t coff[NT], goff[NT];   // this lane's row and chunk from there
+    f32x4 out[NT];                 // MI = 1: out[t][0] alone
+    uint32_t k, groups;
+    int c, xrow;
+
+    // j[t]: first row of tile t; rows past `end` repeat the last and are not stored.
+    __device__ __forceinline__ void init(const Q4Args& a, uint64_t expert_row, const uint32_t (&j)[NT],
+                                         const uint32_t (&end)[NT], int lane, uint32_t cnt) {
+        k = a.k;
+        groups = k / GROUP;
+        c = lane >> 4;
+        const int r16 = lane & 15;
 #pragma unroll
-        for (int i = 0; i < XL; ++i) {
-            const uint32_t v = (i * kWave + lane) / OCT, o = (i * kWave + lane) % OCT;
-            const uint32_t k0 = s0 * QStep + o * 8;
-#pragma unroll
-            for (int p = 0; p < (PARTS == 3 ? 2 : 1); ++p) {
-                q.x[i][p] = u32x4{0, 0, 0, 0};
-                if (v < cnt && s0 + o / (QStep / 8) < st1 && k0 < a.k)
-                    q.x[i][p] = reinterpret_cast<const QChunk<S>*>(x + (int64_t)v * a.ldx + k0 + 4 * p)->v;
-            }
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t j0 = j[t] < end[t] ? j[t] : end[t] - 1;
+            const uint32_t r = r16 < (int)(end[t] - j0) ? r16 : end[t] - j0 - 1;
+            codes[t] = a.codes + (expert_row + j0) * (k / 2);
+            sc[t] = a.scales + (expert_row + j0) * groups;
+            bi[t] = a.biases + (expert_row + j0) * groups;
+            coff[t] = r * (k / 2) + c * 16;
+            goff[t] = r * groups;
+            out[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-#pragma unroll
-        for (int i = 0; i < CS; ++i) {
-            if (s0 + i >= st1) break;
-            // Chunks past the row's end read its start: their activations are 0.
-            const uint32_t k0 = (s0 + i) * QStep + c * 32;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) q.w[i][t] = ld16(codes[t] + (k0 < a.k ? k0 / 2 : 0));
-        }
+        // The staged row that is this lane's row of the A operand; rows past the
+        // last token repeat it and are not stored.
+        const int tok = MI == 1 ? r16 >> 2 : r16;
+        xrow = tok < (int)cnt ? tok : (int)cnt - 1;
+        if (MASKED && (r16 & 3) != c) xrow = VT;
+    }
+
+    // Scales first, codes by step: a step is computed as soon as its own have arrived.
+    __device__ __forceinline__ void load(Codes& q, uint32_t s0, uint32_t st1) const {
         const uint32_t g0 = s0 * GPS;
-        if (g0 + NV <= G) {
+        if (g0 + NV <= groups) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                load_pairs<NV>(sc[t] + g0, q.s[t]);
-                load_pairs<NV>(bi[t] + g0, q.b[t]);
+                load_pairs<NV>(sc[t] + (goff[t] + g0), q.s[t]);
+                load_pairs<NV>(bi[t] + (goff[t] + g0), q.b[t]);
             }
         } else {  // the row's last chunk, cut short
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < SR; ++i) {
-                    const uint32_t e0 = g0 + 2 * i < G ? g0 + 2 * i : G - 1;
-                    const uint32_t e1 = g0 + 2 * i + 1 < G ? g0 + 2 * i + 1 : G - 1;
+                    const uint32_t e0 = goff[t] + (g0 + 2 * i < groups ? g0 + 2 * i : groups - 1);
+                    const uint32_t e1 = goff[t] + (g0 + 2 * i + 1 < groups ? g0 + 2 * i + 1 : groups - 1);
                     q.s[t][i] = sc[t][e0] | ((uint32_t)sc[t][e1] << 16);
                     q.b[t][i] = bi[t][e0] | ((uint32_t)bi[t][e1] << 16);
                 }
         }
-    };
-
-    f32x4 out[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) out[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const u32x4 minus16 = {C::kMinusSixteen, C::kMinusSixteen, C::kMinusSixteen, C::kMinusSixteen};
-
-    Chunk cur;
-    if (st0 < st1) load(cur, st0);
-    for (uint32_t s0 = st0; s0 < st1; s0 += CS) {
-        // Activations of the chunk into LDS.
-#pragma unroll
-        for (int i = 0; i < XL; ++i) {
-            const uint32_t v = (i * kWave + lane) / OCT, o = (i * kWave + lane) % OCT;
-            u32x4 parts[PARTS];
-            octet<T>(cur.x[i], parts);
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-                if (v < cnt) xs[wave][p][v][o] = parts[p];
-        }
-        Chunk nxt;
-        if (s0 + CS < st1) load(nxt, s0 + CS);
-        // One wave writes and reads its LDS in order: only the compiler needs telling.
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
         for (int i = 0; i < CS; ++i) {
             if (s0 + i >= st1) break;
-            // Words to instruction order.
+            // Chunks past the row's end read its start: their activations are 0.
+            const uint32_t k0 = (s0 + i) * QStep;
+            const bool in = k0 + c * 32 < k;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                uint32_t off = coff[t] + k0 / 2;
+                if (k0 + QStep > k) off = in ? off : coff[t] - c * 16;
+                q.w[i][t] = ld16(codes[t] + off);
+            }
+        }
+    }
+
+    // Octet `o` of token v's chunk from s0 on; past the row's end, another of the row.
+    __device__ __forceinline__ void load_x(u32x4 (&q)[XR], const char* x, uint32_t v, uint32_t ldx,
+                                           uint32_t s0, uint32_t o) const {
+        const uint32_t k0 = s0 * QStep + o * 8 < k ? s0 * QStep + o * 8 : 0;
+        const uint32_t at = (v * ldx + k0) * sizeof(S);
+#pragma unroll
+        for (int p = 0; p < XR; ++p) q[p] = reinterpret_cast<const QChunk<S>*>(x + (at + 16 * p))->v;
+    }
+    // Its place in LDS; zeros past the row's end.
+    __device__ __forceinline__ void stage(Stage& xs, u32x4 (&q)[XR], uint32_t v, uint32_t s0,
+                                          uint32_t o) const {
+        if ((s0 + CS) * QStep > k && s0 * QStep + o * 8 >= k) {
+#pragma unroll
+            for (int p = 0; p < XR; ++p) q[p] = u32x4{0, 0, 0, 0};
+        }
+        u32x4 parts[PARTS];
+        octet<T>(q, parts);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) xs[p][v][o] = parts[p];
+    }
+
+    __device__ __forceinline__ void compute(const Codes& q, const Stage& xs, uint32_t s0, uint32_t st1) {
+        const u32x4 one = {C::kOne, C::kOne, C::kOne, C::kOne};
+        // Accumulators that one chain of instructions fills; groups of those.
+        constexpr int CHAINS = MI == 1 ? 1 : GPS, PER = 4 / CHAINS;
+#pragma unroll
+        for (int i = 0; i < CS; ++i) {
+            if (s0 + i >= st1) break;
             uint32_t cw[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) cw[t][g] = cur.w[i][t][g];
-                if constexpr (GROUP <= 64) {
+                for (int g = 0; g < 4; ++g) cw[t][g] = q.w[i][t][g];
+                if constexpr (MI > 1 && GROUP <= 64) {
                     swap32(cw[t][0], cw[t][2]);
                     swap32(cw[t][1], cw[t][3]);
                 }
-                if constexpr (GROUP == 32) {
+                if constexpr (MI > 1 && GROUP == 32) {
                     swap16(cw[t][0], cw[t][1]);
                     swap16(cw[t][2], cw[t][3]);
                 }
             }
 #pragma unroll
-            for (int gp = 0; gp < GPS; ++gp) {
-                f32x4 d0 = {0.f, 0.f, 0.f, 0.f};
-                u32x4 av[PARTS][4 / GPS];
+            for (int gp = 0; gp < CHAINS; ++gp) {
+                f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+                u32x4 av[PARTS][PER];
 #pragma unroll
-                for (int j = 0; j < 4 / GPS; ++j) {
+                for (int j = 0; j < PER; ++j) {
                     // Word g of lane group c is octet oct of the step.
-                    const int g = gp * (4 / GPS) + j;
-                    const int oct = GROUP == 128  ? 4 * c + g
+                    const int g = gp * PER + j;
+                    const int oct = MI == 1 || GROUP == 128 ? 4 * c + g
                                     : GROUP == 64 ? 8 * (g >> 1) + 4 * (c & 1) + 2 * (c >> 1) + (g & 1)
                                                   : 4 * g + c;
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) {
-                        av[p][j] = xs[wave][p][vtok][i * (QStep / 8) + oct];
-                        d0 = C::mma(av[p][j], minus16, d0);
+                        av[p][j] = xs[p][xrow][i * (QStep / 8) + oct];
+                        sum = C::mma(av[p][j], one, sum);
                     }
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    f32x4 d = d0;
+                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < 4 / GPS; ++j) {
-                        const u32x4 bq = codes16<C>(cw[t][gp * (4 / GPS) + j]);
+                    for (int j = 0; j < PER; ++j) {
+                        const u32x4 bq = codes16<C>(cw[t][gp * PER + j]);
 #pragma unroll
                         for (int p = 0; p < PARTS; ++p) d = C::mma(av[p][j], bq, d);
                     }
-                    const int gi = i * GPS + gp;
-                    const uint16_t sh = (uint16_t)(cur.s[t][gi / 2] >> (16 * (gi & 1)));
-                    const uint16_t bh = (uint16_t)(cur.b[t][gi / 2] >> (16 * (gi & 1)));
-                    const float sv = scale_value(sh, sbf);
-                    const float bv = scale_value(bh, sbf) * -0.0625f;
+                    // MI = 1: results 0..3 are the step's chunks (one value without
+                    // the mask); MI = 4: four tokens of one group.
 #pragma unroll
-                    for (int v = 0; v < MI; ++v)
-                        out[t][v] = __builtin_fmaf(bv, d0[v], __builtin_fmaf(sv, d[v], out[t][v]));
+                    for (int h = 0; h < GPS / CHAINS; ++h) {
+                        const int gi = i * GPS + gp + h;
+                        const float sv = widen(ST{}, (uint16_t)(q.s[t][gi / 2] >> (16 * (gi & 1))));
+                        const float bv = widen(ST{}, (uint16_t)(q.b[t][gi / 2] >> (16 * (gi & 1))));
+                        const float b16 = __builtin_fmaf(-16.f, sv, bv);
+                        if constexpr (MI == 1) {
+                            const float dv = GROUP == 64 ? d[2 * h] + d[2 * h + 1] : d[h];
+                            const float xv = GROUP == 64 ? sum[2 * h] + sum[2 * h + 1] : sum[h];
+                            out[t][0] = __builtin_fmaf(b16, xv, __builtin_fmaf(sv, dv, out[t][0]));
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < MI; ++v)
+                                out[t][v] = __builtin_fmaf(b16, sum[v], __builtin_fmaf(sv, d[v], out[t][v]));
+                        }
+                    }
                 }
             }
         }
-        // The next chunk overwrites what this one reads.
+    }
+};
+
+// silu(g) u of the gated form.
+__device__ __forceinline__ float gate(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// Each wave takes a piece of k of the block's rows (16, or 16 gates and 16 ups).
+template <class T, class ST, int GROUP, int MI, bool GATED, int W>
+__global__ __launch_bounds__(W* kWave, MI == 4 ? 2 : 4) void q4_split(Q4Args a) {
+    constexpr int NT = GATED ? 2 : 1;
+    constexpr int CS = T::code == 0 ? (MI == 1 ? 2 : 1) : (MI == 1 && !GATED ? 4 : 2);
+    using Z = Tiles<T, ST, GROUP, MI, NT, CS>;
+    using S = typename T::store_t;
+    constexpr int VT = Z::VT, OCT = Z::OCT;
+    constexpr int XL = VT * OCT / kWave;  // octets a lane stages
+    // The staged activations, then (after a barrier) the sums to join.
+    constexpr int XBYTES = W * sizeof(typename Z::Stage), JBYTES = W * NT * VT * 17 * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[XBYTES > JBYTES ? XBYTES : JBYTES];
+    const auto join = reinterpret_cast<float(*)[NT][VT][17]>(lds);
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    typename Z::Stage& xs = reinterpret_cast<typename Z::Stage*>(lds)[wave];
+    const uint32_t n0 = blockIdx.x * 16;
+    const Rows rows = block_rows<S, VT, 16, W * kWave>(a, n0);
+    if (rows.cnt == 0) return;
+    const uint32_t cnt = rows.cnt;
+    const uint32_t steps = (a.k + QStep - 1) / QStep;
+    const uint32_t st0 = steps * wave / W, st1 = steps * (wave + 1) / W;
+    const uint32_t ldx = (uint32_t)a.ldx;  // below 2^25: offsets in a tile fit 32 bits
+    const char* const x = reinterpret_cast<const char*>(
+        static_cast<const S*>(a.x) + (int64_t)(a.mode == Q4_IDS ? rows.row0 / a.x_div : rows.row0) * a.ldx);
+
+    Z z;
+    if constexpr (GATED) {
+        const uint32_t j[2] = {n0, a.n + n0}, end[2] = {a.n, 2 * a.n};
+        z.init(a, (uint64_t)rows.expert * 2 * a.n, j, end, lane, cnt);
+    } else {
+        const uint32_t j[1] = {n0}, end[1] = {a.n};
+        z.init(a, (uint64_t)rows.expert * a.n, j, end, lane, cnt);
+    }
+    if (Z::MASKED) {
+        for (int o = lane; o < OCT; o += kWave)
+#pragma unroll
+            for (int p = 0; p < Z::PARTS; ++p) xs[p][Z::ROWS - 1][o] = u32x4{0, 0, 0, 0};
+    }
+
+    struct Chunk {
+        u32x4 x[XL][Z::XR];
+        typename Z::Codes q;
+    };
+    const auto load = [&](Chunk& h, uint32_t s0) {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            if (i * kWave / OCT >= cnt) break;
+            const uint32_t v = (i * kWave + lane) / OCT, o = (i * kWave + lane) % OCT;
+            z.load_x(h.x[i], x, v < cnt ? v : cnt - 1, ldx, s0, o);
+        }
+        z.load(h.q, s0, st1);
+    };
+    const auto step = [&](Chunk& cur, Chunk& nxt, uint32_t s0) {
+        if (MI == 1 && s0 + CS < st1) load(nxt, s0 + CS);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            if (i * kWave / OCT >= cnt) break;
+            const uint32_t v = (i * kWave + lane) / OCT, o = (i * kWave + lane) % OCT;
+            if (v < cnt) z.stage(xs, cur.x[i], v, s0, o);
+        }
+        // With 16 tokens, only after x has left its registers: there are few.
+        if (MI > 1 && s0 + CS < st1) load(nxt, s0 + CS);
+        // One wave writes and reads its LDS in order: only the compiler needs telling.
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        cur = nxt;
+        z.compute(cur.q, xs, s0, st1);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+    Chunk even, odd;
+    if (st0 < st1) load(even, st0);
+    for (uint32_t s0 = st0; s0 < st1; s0 += 2 * CS) {
+        step(even, odd, s0);
+        if (s0 + CS < st1) step(odd, even, s0 + CS);
     }
 
     // Join the W pieces of k.
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int v = 0; v < MI; ++v) join[wave][t][MI == 1 ? c : 4 * c + v][r16] = out[t][v];
+        for (int v = 0; v < MI; ++v) join[wave][t][MI == 1 ? z.c : 4 * z.c + v][lane & 15] = z.out[t][v];
     __syncthreads();
-    for (uint32_t q = threadIdx.x; q < VT * 16 * TN; q += W * kWave) {
-        const uint32_t v = q / (16 * TN), tt = q / 16 % TN, j = q % 16;
-        const uint32_t col = n0 + tt * 16 + j;
-        if (v >= cnt || col >= a.n) continue;
-        float sum[GATED ? 2 : 1];
+    S* const y = static_cast<S*>(a.y) + (int64_t)rows.row0 * a.ldy;
+    const uint32_t v = threadIdx.x / 16, j = threadIdx.x % 16;
+    if (v >= cnt || n0 + j >= a.n) return;
+    float sum[NT];
 #pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            sum[h] = join[0][h * TN + tt][v][j];
+    for (int t = 0; t < NT; ++t) {
+        sum[t] = join[0][t][v][j];
 #pragma unroll
-            for (int w = 1; w < W; ++w) sum[h] += join[w][h * TN + tt][v][j];
+        for (int w = 1; w < W; ++w) sum[t] += join[w][t][v][j];
+    }
+    y[(int64_t)v * a.ldy + n0 + j] = narrow(T{}, GATED ? gate(sum[0], sum[NT - 1]) : sum[0]);
+}
+
+// Each wave takes 32 rows of W (16 gates and 16 ups) and all of k, for 16 tokens.
+template <class T, class ST, int GROUP, bool GATED, int W>
+__global__ __launch_bounds__(W* kWave, 4) void q4_block(Q4Args a) {
+    constexpr int CS = 2;
+    using Z = Tiles<T, ST, GROUP, 4, 2, CS>;
+    using S = typename T::store_t;
+    constexpr int VT = Z::VT, OCT = Z::OCT;
+    constexpr int COLS = (GATED ? 16 : 32) * W;
+    static_assert(VT * OCT % (W * kWave) == 0, "whole octets a lane");
+    constexpr int XL = VT * OCT / (W * kWave);
+    __shared__ typename Z::Stage xs[2];
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t n0 = blockIdx.x * COLS;
+    const Rows rows = block_rows<S, VT, COLS, W * kWave>(a, n0);
+    if (rows.cnt == 0) return;
+    const uint32_t cnt = rows.cnt;
+    const uint32_t steps = (a.k + QStep - 1) / QStep;
+    const uint32_t ldx = (uint32_t)a.ldx;  // below 2^25: offsets in a tile fit 32 bits
+    const char* const x = reinterpret_cast<const char*>(static_cast<const S*>(a.x) + (int64_t)rows.row0 * a.ldx);
+
+    Z z;
+    const uint32_t nw = n0 + wave * (COLS / W);
+    if constexpr (GATED) {
+        const uint32_t j[2] = {nw < a.n ? nw : a.n - 1, a.n + (nw < a.n ? nw : a.n - 1)}, end[2] = {a.n, 2 * a.n};
+        z.init(a, (uint64_t)rows.expert * 2 * a.n, j, end, lane, cnt);
+    } else {
+        const uint32_t j[2] = {nw, nw + 16}, end[2] = {a.n, a.n};
+        z.init(a, (uint64_t)rows.expert * a.n, j, end, lane, cnt);
+    }
+
+    u32x4 xr[XL][Z::XR];
+    const auto load_x = [&](uint32_t s0) {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const uint32_t q = i * (W * kWave) + threadIdx.x, v = q / OCT;
+            if (v < cnt) z.load_x(xr[i], x, v, ldx, s0, q % OCT);
         }
-        float r = sum[0];
-        if constexpr (GATED) r = sum[0] / (1.f + expf(-sum[0])) * sum[1];
-        y[(int64_t)v * a.ldy + col] = narrow(T{}, r);
+    };
+    const auto step = [&](typename Z::Codes& cur, typename Z::Codes& nxt, typename Z::Stage& buf, uint32_t s0) {
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const uint32_t q = i * (W * kWave) + threadIdx.x, v = q / OCT;
+            if (v < cnt) z.stage(buf, xr[i], v, s0, q % OCT);
+        }
+        if (s0 + CS < steps) {
+            load_x(s0 + CS);
+            z.load(nxt, s0 + CS, steps);
+        }
+        // A buffer is written again two chunks later: past the next barrier.
+        __syncthreads();
+        z.compute(cur, buf, s0, steps);
+    };
+    typename Z::Codes even, odd;
+    load_x(0);
+    z.load(even, 0, steps);
+    for (uint32_t s0 = 0; s0 < steps; s0 += 2 * CS) {
+        step(even, odd, xs[0], s0);
+        if (s0 + CS < steps) step(odd, even, xs[1], s0 + CS);
+    }
+
+    S* const y = static_cast<S*>(a.y) + (int64_t)rows.row0 * a.ldy;
+#pragma unroll
+    for (int t = 0; t < (GATED ? 1 : 2); ++t) {
+        const uint32_t col = nw + t * 16 + (lane & 15);
+        if (col >= a.n) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (4 * z.c + v < (int)cnt)
+                y[(int64_t)(4 * z.c + v) * a.ldy + col] =
+                    narrow(T{}, GATED ? gate(z.out[0][v], z.out[1][v]) : z.out[t][v]);
     }
 }
 
-// The instances: up to 4 tokens a pass on one tile; 16 on one tile (eight
-// pieces of k, for few blocks) or on 64 weight rows (staging x costs less).
-enum Form { NARROW, WIDE_FEW, WIDE };
-template <class T, int GROUP, bool GATED>
+// The instances: up to 4 tokens a tile; 16 tokens with k split over eight waves
+// (few blocks), or with the rows split over them.
+enum Form { NARROW, SPLIT, BLOCK };
+constexpr int kBlockWaves = 4;
+template <class T, class ST, int GROUP, bool GATED>
 const void* pick(Form f) {
     switch (f) {
-        case NARROW: return (const void*)&q4_rows<T, GROUP, 1, GATED, 1, 4>;
-        case WIDE_FEW: return (const void*)&q4_rows<T, GROUP, 4, GATED, 1, 8>;
-        default: return (const void*)&q4_rows<T, GROUP, 4, GATED, GATED ? 2 : 4, 4>;
+        case NARROW: return (const void*)&q4_split<T, ST, GROUP, 1, GATED, 4>;
+        case SPLIT: return (const void*)&q4_split<T, ST, GROUP, 4, GATED, 8>;
+        default: return (const void*)&q4_block<T, ST, GROUP, GATED, kBlockWaves>;
     }
 }
-template <class T, int GROUP>
-const void* pick(Form f, bool gated) {
-    return gated ? pick<T, GROUP, true>(f) : pick<T, GROUP, false>(f);
+template <class T, class ST>
+const void* pick(const Q4Args& a, Form f) {
+    switch (a.group) {
+        case 32: return a.gated ? pick<T, ST, 32, true>(f) : pick<T, ST, 32, false>(f);
+        case 64: return a.gated ? pick<T, ST, 64, true>(f) : pick<T, ST, 64, false>(f);
+        default: return a.gated ? pick<T, ST, 128, true>(f) : pick<T, ST, 128, false>(f);
+    }
 }
 template <class T>
-const void* pick(uint32_t group, Form f, bool gated) {
-    return group == 32 ? pick<T, 32>(f, gated) : group == 64 ? pick<T, 64>(f, gated) : pick<T, 128>(f, gated);
+const void* pick(const Q4Args& a, Form f) {
+    return a.scale_dtype == 1 ? pick<T, TF16>(a, f) : pick<T, TBF16>(a, f);
 }
 
 }  // namespace
 
 hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_Q4;
-    // Sixteen tokens a pass where an expert has more than 4 rows on average.
+    // Sixteen tokens a tile where an expert has more than 4 rows on average.
     const bool wide = a.mode == Q4_DENSE ? a.rows > 4 : a.mode == Q4_SORTED && a.rows > 4ull * a.n_experts;
     const uint32_t vt = wide ? 16 : 4;
     uint64_t tiles = a.rows;
@@ -435,26 +611,25 @@ hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L) {
     // Sorted: every expert with rows may end inside a tile.
     if (a.mode == Q4_SORTED) tiles = a.rows / vt + (a.rows < a.n_experts ? a.rows : a.n_experts);
     Form f = NARROW;
-    uint32_t tn = 1, w = 4;
+    uint32_t cols = 16, waves = 4;
     if (wide) {
-        tn = a.gated ? 2 : 4;
-        f = WIDE;
-        if (tiles * ((a.n + 16 * tn - 1) / (16 * tn)) < 512) {
-            f = WIDE_FEW;
-            tn = 1;
-            w = 8;
+        f = BLOCK;
+        waves = kBlockWaves;
+        cols = (a.gated ? 16 : 32) * waves;
+        if (tiles * ((a.n + cols - 1) / cols) < 256) {
+            f = SPLIT;
+            cols = 16;
+            waves = 8;
         }
     }
-    L->variant = (int)(vt + 256 * tn);
-    const void* fn = a.dtype == 0   ? pick<TF32>(a.group, f, a.gated)
-                     : a.dtype == 1 ? pick<TF16>(a.group, f, a.gated)
-                                    : pick<TBF16>(a.group, f, a.gated);
+    L->variant = (int)(vt + 256 * cols);
+    const void* fn = a.dtype == 0 ? pick<TF32>(a, f) : a.dtype == 1 ? pick<TF16>(a, f) : pick<TBF16>(a, f);
     Q4Args b = a;
     b.tiles = (uint32_t)tiles;
     const uint32_t gy = (uint32_t)(tiles < 32768 ? tiles : 32768);
     void* args[] = {&b};
-    return hipLaunchKernel(fn, dim3((a.n + 16 * tn - 1) / (16 * tn), gy, (uint32_t)((tiles + gy - 1) / gy)),
-                           dim3(w * kWave), args, 0, s);
+    return hipLaunchKernel(fn, dim3((a.n + cols - 1) / cols, gy, (uint32_t)((tiles + gy - 1) / gy)),
+                           dim3(waves * kWave), args, 0, s);
 }
 
 }  // namespace mmk

@@ -1,12 +1,21 @@
-// Routed rows in expert order, and back to tokens: the sort's plan and its row
-// gather, the weighted combination, and the gradients.
+// Routed rows in expert order, and back to tokens: the stable sort and its row
+// copies, the weighted combination, and the gradients.
 //
-// Plan: a stable counting sort without scratch. Block b (one for each expert,
-// and one for the rows without) counts over all ids the keys below b, which is
-// the first place of its rows, and those equal to b, wave by wave; a second
-// pass over the ids gives each row of b its rank. Blocks exchange nothing, and
-// the ids are small next to the rows (4 bytes against a row), so reading them
-// once a block costs less than a second launch or a wait between blocks.
+// The place of a routed row is a count over all ids: the rows of lower experts,
+// and those of its own before it. Few rows (sort_small): every token's block
+// counts for its own slots while its row of x is under way, one launch and
+// nothing exchanged between blocks. Many (sort_plan, then sort_copy): block b
+// counts the keys below expert b, which is where its rows begin, then ranks its
+// rows in a second pass. Neither needs scratch or atomics on memory; the ids
+// are 4 bytes against a row, so reading them more than once is cheap.
+//
+// The rows are bound by memory: a block takes one token, so a token's row is
+// read or written once whatever top_k, and up to eight expert rows are under way
+// at a time. Rows are only element-aligned where pitch or width is odd; 16-byte
+// accesses at such addresses are what the hardware allows and measured faster
+// than element ones.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -19,47 +28,108 @@ constexpr int PWaves = PThreads / kWave;
 constexpr int CThreads = 256;
 constexpr int CWaves = CThreads / kWave;
 
-__device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
-    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
-                                     __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+// Inclusive sum over the lanes up to this one: within rows of 16 lanes, then
+// each row's last lane onto the rows after it.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    int x = (int)v;
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);  // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);  // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);  // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31
+    return (uint32_t)x;
+}
+__device__ __forceinline__ uint32_t wave_total(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(v), kWave - 1);
+}
+__device__ __forceinline__ float wave_add(float v) {
+    const auto add = [&](float o) { v += o; };
+    const auto mov = [&](auto ctrl, auto rows) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+            0, (int)__float_as_uint(v), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+    };
+    using std::integral_constant;
+    add(mov(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{}));
+    add(mov(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{}));
+    add(mov(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{}));
+    add(mov(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{}));
+    add(mov(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{}));
+    add(mov(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{}));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), kWave - 1));
+}
+
+// Four neighbouring ids' keys (expert, or E for a row without), `pad` past the end.
+struct __attribute__((packed, aligned(4))) Ids4 {
+    uint32_t v[4];
+};
+__device__ __forceinline__ void load_keys(const SortArgs& a, int64_t r, int64_t end, uint32_t pad,
+                                          uint32_t (&key)[4]) {
+    if (r + 4 <= end) {
+        const Ids4 q = *reinterpret_cast<const Ids4*>(a.ids + r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) key[i] = q.v[i] < a.n_experts ? q.v[i] : a.n_experts;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t id = r + i < end ? a.ids[r + i] : 0u;
+            key[i] = r + i < end ? (id < a.n_experts ? id : a.n_experts) : pad;
+        }
+    }
 }
 
 __global__ __launch_bounds__(PThreads) void sort_plan(SortArgs a) {
     __shared__ uint32_t s_less[PWaves], s_eq[PWaves];
+    constexpr int U = 4, SPAN = kWave * 4;  // ids of a wave's load; loads under way
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const uint32_t E = a.n_experts, b = blockIdx.x;  // b == E: rows without an expert
+    const uint32_t b = blockIdx.x;  // b == E: rows without an expert
     const int64_t R = (int64_t)a.m * a.top_k;
     // Wave w owns a contiguous piece of the routed rows.
-    const int64_t piece = (R + PWaves * kWave - 1) / (PWaves * kWave) * kWave;
+    const int64_t piece = (R + PWaves * SPAN - 1) / (PWaves * SPAN) * SPAN;
     const int64_t r0 = wave * piece, r1 = r0 + piece < R ? r0 + piece : R;
     uint32_t less = 0, eq = 0;
-    for (int64_t r = r0 + lane; r < r1; r += kWave) {
-        const uint32_t id = a.ids[r], key = id < E ? id : E;
-        less += key < b;
-        eq += key == b;
-    }
+    for (int64_t r = r0; r < r1; r += U * SPAN) {
+        uint32_t key[U][4];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        less += __shfl_xor((int)less, o, kWave);
-        eq += __shfl_xor((int)eq, o, kWave);
+        for (int u = 0; u < U; ++u) load_keys(a, r + u * SPAN + lane * 4, r1, 0xFFFFFFFFu, key[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                less += key[u][i] < b;
+                eq += key[u][i] == b;
+            }
     }
+    less = wave_total(less);
+    eq = wave_total(eq);
     if (lane == 0) { s_less[wave] = less; s_eq[wave] = eq; }
     __syncthreads();
     uint32_t place = 0;
     for (int w = 0; w < PWaves; ++w) place += s_less[w];
     if (threadIdx.x == 0) a.offsets_w[b] = place;
     for (int w = 0; w < wave; ++w) place += s_eq[w];
-    if (s_eq[wave] == 0) return;
-    for (int64_t r = r0; r < r1; r += kWave) {
-        const bool in = r + lane < r1;
-        const uint32_t id = in ? a.ids[r + lane] : 0u, key = id < E ? id : E;
-        const uint64_t mask = __ballot(in && key == b);
-        if (in && key == b) {
-            const uint32_t i = place + lanes_below(mask);
-            a.order_w[i] = (uint32_t)(r + lane);
-            a.position_w[r + lane] = i;
+    if (eq == 0) return;
+    for (int64_t r = r0; r < r1; r += U * SPAN) {
+        uint32_t key[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) load_keys(a, r + u * SPAN + lane * 4, r1, 0xFFFFFFFFu, key[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n += key[u][i] == b;
+            const uint32_t upto = wave_scan(n);
+            uint32_t at = place + upto - n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (key[u][i] == b) {
+                    const uint32_t row = (uint32_t)(r + u * SPAN + lane * 4 + i);
+                    a.order_w[at] = row;
+                    a.position_w[row] = at;
+                    ++at;
+                }
+            place += (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
         }
-        place += (uint32_t)__popcll(mask);
     }
 }
 
@@ -96,108 +166,229 @@ __device__ __forceinline__ u32x4 repack(const float* f) {
     return v;
 }
 
-// xs[i] = x[order[i] / top_k], +0 past offsets[E]. The rows are moved as bits.
+constexpr int KU = 8;  // slots handled together
+
+// A storage type's bits as they are moved.
+template <class T>
+using Bits = std::conditional_t<T::code == 0, uint32_t, uint16_t>;
+
+// Elements j .. of a row of `width` at element offset `row`, up to 16 bytes of
+// them; zeros, and nothing touched, past the row's end.
 template <class S>
-__global__ __launch_bounds__(CThreads) void sort_gather(SortArgs a) {
+__device__ __forceinline__ u32x4 get(const void* base, int64_t row, uint32_t j, uint32_t width) {
+    const S* src = static_cast<const S*>(base) + row + j;
+    if (j + 16 / sizeof(S) <= width) return ld_chunk(src);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (uint32_t q = 0; q < 16 / sizeof(S) - 1; ++q) {
+        if (j + q < width) v[q * sizeof(S) / 4] |= (uint32_t)src[q] << (16 * (q & (4 / sizeof(S) - 1)));
+    }
+    return v;
+}
+template <class S>
+__device__ __forceinline__ void put(void* base, int64_t row, uint32_t j, uint32_t width, u32x4 v) {
+    S* dst = static_cast<S*>(base) + row + j;
+    if (j + 16 / sizeof(S) <= width) {
+        st_chunk(dst, v);
+        return;
+    }
+#pragma unroll
+    for (uint32_t q = 0; q < 16 / sizeof(S) - 1; ++q) {
+        if (j + q < width) dst[q] = (S)(v[q * sizeof(S) / 4] >> (16 * (q & (4 / sizeof(S) - 1))));
+    }
+}
+
+// xs[position[t * top_k + s]] = x[t], zeros past the rows that have an expert.
+// A block takes a token and one piece of its row; the rows are moved as bits.
+template <class S>
+__global__ __launch_bounds__(CThreads) void sort_copy(SortArgs a) {
     constexpr int CH = 16 / sizeof(S);
-    const int64_t R = (int64_t)a.m * a.top_k;
+    const uint32_t j = (blockIdx.y * CThreads + threadIdx.x) * CH;
+    if (j >= a.width) return;
     const uint32_t live = a.offsets[a.n_experts];
-    for (int64_t i = blockIdx.x; i < R; i += gridDim.x) {
-        const uint32_t r = a.order[i];
-        const S* src = static_cast<const S*>(a.tokens) + (int64_t)(r / a.top_k) * a.ld_tokens;
-        S* dst = static_cast<S*>(a.rows_w) + i * a.ld_rows;
-        const bool on = i < live && r < R;
-        for (uint32_t j = threadIdx.x * CH; j < a.width; j += CThreads * CH) {
-            if (j + CH <= a.width) {
-                st_chunk(dst + j, on ? ld_chunk(src + j) : u32x4{0, 0, 0, 0});
-            } else {
-                for (uint32_t q = j; q < a.width; ++q) dst[q] = on ? src[q] : (S)0;
-            }
+    for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
+        const u32x4 v = get<S>(a.tokens, t * a.ld_tokens, j, a.width);
+        for (uint32_t s = 0; s < a.top_k; ++s) {
+            const uint32_t i = a.position[t * a.top_k + s];
+            put<S>(a.rows_w, (int64_t)i * a.ld_rows, j, a.width, i < live ? v : u32x4{0, 0, 0, 0});
         }
     }
+}
+
+// The whole sort in one launch, for few rows: block 0 counts the offsets, block
+// t + 1 the places of token t's slots.
+template <class S>
+__global__ __launch_bounds__(CThreads) void sort_small(SortArgs a) {
+    constexpr int CH = 16 / sizeof(S);
+    __shared__ uint32_t hist[MM_GROUPED_MAX_E + 1];
+    __shared__ uint32_t part[CWaves][KU];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const uint32_t E = a.n_experts, R = a.m * a.top_k;
+    if (blockIdx.x == 0) {
+        if (blockIdx.y) return;
+        for (uint32_t e = threadIdx.x; e < E; e += CThreads) hist[e] = 0;
+        __syncthreads();
+        for (uint32_t r = threadIdx.x; r < R; r += CThreads) {
+            const uint32_t id = a.ids[r];
+            if (id < E) atomicAdd(&hist[id], 1u);
+        }
+        __syncthreads();
+        uint32_t before = 0;
+        if (wave == 0) {
+            for (uint32_t e0 = 0; e0 < E; e0 += kWave) {
+                const uint32_t n = e0 + lane < E ? hist[e0 + lane] : 0;
+                const uint32_t upto = wave_scan(n);
+                if (e0 + lane < E) a.offsets_w[e0 + lane] = before + upto - n;
+                before += (uint32_t)__builtin_amdgcn_readlane((int)upto, kWave - 1);
+            }
+            if (lane == 0) a.offsets_w[E] = before;
+        }
+        return;
+    }
+    const uint32_t t = blockIdx.x - 1;
+    const uint32_t j = (blockIdx.y * CThreads + threadIdx.x) * CH;
+    u32x4 v = {0, 0, 0, 0};
+    if (j < a.width) v = get<S>(a.tokens, (int64_t)t * a.ld_tokens, j, a.width);
+    for (uint32_t s0 = 0; s0 < a.top_k; s0 += KU) {
+        uint32_t key[KU], n[KU];
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+            const uint32_t s = s0 + u < a.top_k ? s0 + u : a.top_k - 1;
+            const uint32_t id = a.ids[t * a.top_k + s];
+            key[u] = id < E ? id : E;
+            n[u] = 0;
+        }
+        for (uint32_t r = threadIdx.x * 4; r < R; r += CThreads * 4) {
+            uint32_t k4[4];
+            load_keys(a, r, R, 0xFFFFFFFFu, k4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int u = 0; u < KU; ++u)
+                    n[u] += k4[i] < key[u] + (r + i < t * a.top_k + s0 + u);  // equal ones before it too
+        }
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+            const uint32_t w = wave_total(n[u]);
+            if (lane == 0) part[wave][u] = w;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+            if (s0 + u >= a.top_k) break;
+            uint32_t i = 0;
+#pragma unroll
+            for (int w = 0; w < CWaves; ++w) i += part[w][u];
+            const uint32_t r = t * a.top_k + s0 + u;
+            if (threadIdx.x == 0 && blockIdx.y == 0) {
+                a.order_w[i] = r;
+                a.position_w[r] = i;
+            }
+            if (j < a.width)
+                put<S>(a.rows_w, (int64_t)i * a.ld_rows, j, a.width, key[u] < E ? v : u32x4{0, 0, 0, 0});
+        }
+        __syncthreads();
+    }
+}
+
+// Rows that have an expert: all of them without positions.
+__device__ __forceinline__ uint32_t live_rows(const SortArgs& a) {
+    const uint32_t R = a.m * a.top_k;
+    if (!a.position) return R;
+    const uint32_t live = a.offsets[a.n_experts];
+    return live < R ? live : R;
 }
 
 // out[t] = residual[t] + sum_s w[t][s] y[position]; without weights each is 1.
 // W: has weights. A block takes one token and one piece of its row.
 template <class T, bool W>
 __global__ __launch_bounds__(CThreads) void combine(SortArgs a) {
-    using S = typename T::store_t;
     constexpr int CH = T::Elems16;
-    const uint32_t R = a.m * a.top_k;
-    const uint32_t live = a.position ? (a.offsets[a.n_experts] < R ? a.offsets[a.n_experts] : R) : R;
+    const uint32_t live = live_rows(a);
     const uint32_t j = (blockIdx.y * CThreads + threadIdx.x) * CH;
     if (j >= a.width) return;
-    const bool whole = j + CH <= a.width;
     for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
         float acc[CH] = {};
-        if (a.residual) {
-            const S* res = static_cast<const S*>(a.residual) + t * a.ld_tokens + j;
-            if (whole) unpack<T>(ld_chunk(res), acc);
-            else
-                for (uint32_t q = 0; j + q < a.width; ++q) acc[q] = widen(T{}, res[q]);
-        }
-        for (uint32_t s = 0; s < a.top_k; ++s) {
-            const uint32_t r = (uint32_t)t * a.top_k + s;
-            const uint32_t i = a.position ? a.position[r] : r;
-            if (i >= live) continue;
-            const float w = W ? a.weights[r] : 1.f;
-            const S* y = static_cast<const S*>(a.rows) + (int64_t)i * a.ld_rows + j;
-            float f[CH] = {};
-            if (whole) unpack<T>(ld_chunk(y), f);
-            else
-                for (uint32_t q = 0; j + q < a.width; ++q) f[q] = widen(T{}, y[q]);
+        if (a.residual) unpack<T>(get<Bits<T>>(a.residual, t * a.ld_tokens, j, a.width), acc);
+        for (uint32_t s0 = 0; s0 < a.top_k; s0 += KU) {
+            u32x4 y[KU];
+            bool on[KU];
 #pragma unroll
-            for (int q = 0; q < CH; ++q) acc[q] = __builtin_fmaf(w, f[q], acc[q]);
+            for (int u = 0; u < KU; ++u) {
+                const uint32_t r = (uint32_t)t * a.top_k + s0 + u;
+                const uint32_t i = s0 + u < a.top_k ? (a.position ? a.position[r] : r) : 0xFFFFFFFFu;
+                on[u] = i < live;
+                if (on[u]) y[u] = get<Bits<T>>(a.rows, (int64_t)i * a.ld_rows, j, a.width);
+            }
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                if (!on[u]) continue;
+                const float w = W ? a.weights[(uint32_t)t * a.top_k + s0 + u] : 1.f;
+                float f[CH];
+                unpack<T>(y[u], f);
+#pragma unroll
+                for (int q = 0; q < CH; ++q) acc[q] = __builtin_fmaf(w, f[q], acc[q]);
+            }
         }
-        S* out = static_cast<S*>(a.tokens_w) + t * a.ld_tokens + j;
-        if (whole) st_chunk(out, repack<T>(acc));
-        else
-            for (uint32_t q = 0; j + q < a.width; ++q) out[q] = narrow(T{}, acc[q]);
+        put<Bits<T>>(a.tokens_w, t * a.ld_tokens, j, a.width, repack<T>(acc));
     }
 }
 
-// dy[i] = w dout[t], dw = <dout[t], y[i]>. One wave for each routed row.
+// dy[i] = w dout[t], dw = <dout[t], y[i]>. A block takes one token.
 template <class T>
 __global__ __launch_bounds__(CThreads) void combine_grad(SortArgs a) {
-    using S = typename T::store_t;
     constexpr int CH = T::Elems16;
-    const int lane = threadIdx.x & (kWave - 1);
-    const uint32_t R = a.m * a.top_k;
-    const uint32_t live = a.position ? a.offsets[a.n_experts] : R;
-    for (int64_t r = (int64_t)blockIdx.x * CWaves + threadIdx.x / kWave; r < R;
-         r += (int64_t)gridDim.x * CWaves) {
-        const uint32_t i = a.position ? a.position[r] : (uint32_t)r;
-        const bool on = i < live;
-        const float w = on ? a.weights[r] : 0.f;
-        const S* d = static_cast<const S*>(a.tokens) + (r / a.top_k) * a.ld_tokens;
-        const S* y = static_cast<const S*>(a.rows) + (int64_t)i * a.ld_rows;
-        S* dy = static_cast<S*>(a.rows_w) + (int64_t)i * a.ld_rows;
-        float dot = 0.f;
-        if (i < R) {
-            for (uint32_t j = lane * CH; j < a.width; j += kWave * CH) {
-                float g[CH] = {}, f[CH] = {}, o[CH] = {};
-                if (j + CH <= a.width) {
-                    if (on) {
-                        unpack<T>(ld_chunk(d + j), g);
-                        unpack<T>(ld_chunk(y + j), f);
-                    }
+    __shared__ float part[CWaves][KU];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const uint32_t R = a.m * a.top_k, live = live_rows(a);
+    for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
+        for (uint32_t s0 = 0; s0 < a.top_k; s0 += KU) {
+            uint32_t at[KU];
+            float w[KU], dot[KU];
 #pragma unroll
-                    for (int q = 0; q < CH; ++q) {
-                        dot = __builtin_fmaf(g[q], f[q], dot);
-                        o[q] = on ? w * g[q] : 0.f;
+            for (int u = 0; u < KU; ++u) {
+                const uint32_t r = (uint32_t)t * a.top_k + s0 + u;
+                at[u] = s0 + u < a.top_k ? (a.position ? a.position[r] : r) : 0xFFFFFFFFu;
+                w[u] = at[u] < live ? a.weights[r] : 0.f;
+                dot[u] = 0.f;
+            }
+            for (uint32_t j = threadIdx.x * CH; j < a.width; j += CThreads * CH) {
+                u32x4 y[KU];
+                const u32x4 d = get<Bits<T>>(a.tokens, t * a.ld_tokens, j, a.width);
+#pragma unroll
+                for (int u = 0; u < KU; ++u)
+                    if (at[u] < live) y[u] = get<Bits<T>>(a.rows, (int64_t)at[u] * a.ld_rows, j, a.width);
+                float g[CH];
+                unpack<T>(d, g);
+#pragma unroll
+                for (int u = 0; u < KU; ++u) {
+                    if (at[u] >= R) continue;
+                    float f[CH] = {}, o[CH] = {};
+                    if (at[u] < live) {
+                        unpack<T>(y[u], f);
+#pragma unroll
+                        for (int q = 0; q < CH; ++q) {
+                            dot[u] = __builtin_fmaf(g[q], f[q], dot[u]);
+                            o[q] = w[u] * g[q];
+                        }
                     }
-                    st_chunk(dy + j, repack<T>(o));
-                } else {
-                    for (uint32_t q = j; q < a.width; ++q) {
-                        const float gq = on ? widen(T{}, d[q]) : 0.f;
-                        if (on) dot = __builtin_fmaf(gq, widen(T{}, y[q]), dot);
-                        dy[q] = narrow(T{}, on ? w * gq : 0.f);
-                    }
+                    put<Bits<T>>(a.rows_w, (int64_t)at[u] * a.ld_rows, j, a.width, repack<T>(o));
                 }
             }
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                const float sum = wave_add(dot[u]);
+                if (lane == 0) part[wave][u] = sum;
+            }
+            __syncthreads();
+            if (threadIdx.x < KU && s0 + threadIdx.x < a.top_k) {
+                float sum = 0.f;
+#pragma unroll
+                for (int v = 0; v < CWaves; ++v) sum += part[v][threadIdx.x];
+                a.dweights_w[(uint32_t)t * a.top_k + s0 + threadIdx.x] = sum;
+            }
+            __syncthreads();
         }
-        dot = wave_sum(dot);
-        if (lane == 0) a.dweights_w[r] = on ? dot : 0.f;
     }
 }
 
@@ -205,17 +396,36 @@ uint32_t cap(int64_t n) { return (uint32_t)(n < 1 ? 1 : n < (1 << 20) ? n : (1 <
 
 }  // namespace
 
+namespace {
+
+// Grid over tokens and pieces of a row (width <= 2^24: at most 2^14 pieces).
+dim3 row_grid(int64_t blocks, uint32_t width, int dtype) {
+    const uint32_t per = CThreads * (dtype == 0 ? 4 : 8);
+    return dim3(cap(blocks), (width + per - 1) / per);
+}
+
+}  // namespace
+
+// Up to this many routed rows are sorted in one launch: its blocks read the ids
+// m * m * top_k times in all, which costs less than a second launch until then.
+constexpr int64_t kSmallRows = 8192;
+int sort_launches(const SortArgs& a) { return (int64_t)a.m * a.top_k <= kSmallRows ? 1 : 2; }
+
 hipError_t launch_sort_plan(const SortArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_SORT_PLAN;
     void* args[] = {const_cast<SortArgs*>(&a)};
     return hipLaunchKernel((const void*)&sort_plan, dim3(a.n_experts + 1), dim3(PThreads), args, 0, s);
 }
 
-hipError_t launch_sort_gather(const SortArgs& a, hipStream_t s, Launched* L) {
-    L->kernel = MM_KERNEL_SORT_GATHER;
-    const void* fn = a.dtype == 0 ? (const void*)&sort_gather<uint32_t> : (const void*)&sort_gather<uint16_t>;
+hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s, Launched* L) {
+    L->kernel = MM_KERNEL_SORT_ROWS;
+    const bool small = sort_launches(a) == 1;
+    L->variant = small ? 1 : 0;
+    const void* fn = small ? (a.dtype == 0 ? (const void*)&sort_small<uint32_t> : (const void*)&sort_small<uint16_t>)
+                           : (a.dtype == 0 ? (const void*)&sort_copy<uint32_t> : (const void*)&sort_copy<uint16_t>);
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, dim3(cap((int64_t)a.m * a.top_k)), dim3(CThreads), args, 0, s);
+    return hipLaunchKernel(fn, row_grid(small ? (int64_t)a.m + 1 : (int64_t)a.m, a.width, a.dtype), dim3(CThreads),
+                           args, 0, s);
 }
 
 hipError_t launch_combine(const SortArgs& a, hipStream_t s, Launched* L) {
@@ -224,10 +434,8 @@ hipError_t launch_combine(const SortArgs& a, hipStream_t s, Launched* L) {
     const void* fn = a.dtype == 0   ? (w ? (const void*)&combine<TF32, true> : (const void*)&combine<TF32, false>)
                      : a.dtype == 1 ? (w ? (const void*)&combine<TF16, true> : (const void*)&combine<TF16, false>)
                                     : (w ? (const void*)&combine<TBF16, true> : (const void*)&combine<TBF16, false>);
-    const int64_t per = CThreads * (a.dtype == 0 ? 4 : 8);
-    const int64_t pieces = (a.width + per - 1) / per;  // width < 2^26: at most 2^16
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, dim3(cap(a.m < 65536 ? a.m : 65536), (uint32_t)pieces), dim3(CThreads), args, 0, s);
+    return hipLaunchKernel(fn, row_grid(a.m, a.width, a.dtype), dim3(CThreads), args, 0, s);
 }
 
 hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s, Launched* L) {
@@ -236,7 +444,7 @@ hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s, Launched* L) {
                      : a.dtype == 1 ? (const void*)&combine_grad<TF16>
                                     : (const void*)&combine_grad<TBF16>;
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, dim3(cap(((int64_t)a.m * a.top_k + CWaves - 1) / CWaves)), dim3(CThreads), args, 0, s);
+    return hipLaunchKernel(fn, dim3(cap(a.m)), dim3(CThreads), args, 0, s);
 }
 
 }  // namespace mmk

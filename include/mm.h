@@ -105,7 +105,7 @@ typedef enum {
     MM_KERNEL_TOPK = 14,             /* router */
     MM_KERNEL_TOPK_GRAD = 15,        /* router gradient */
     MM_KERNEL_SORT_PLAN = 16,        /* offsets, order and position */
-    MM_KERNEL_SORT_GATHER = 17,      /* sorted rows (with the plan, when in one launch) */
+    MM_KERNEL_SORT_ROWS = 17,      /* sorted rows (with the plan, when in one launch) */
     MM_KERNEL_COMBINE = 18,          /* weighted sum of expert rows (and mm_id_sort_grad) */
     MM_KERNEL_COMBINE_GRAD = 19,     /* its gradients */
     MM_KERNEL_Q4 = 20                /* 4-bit weights on MFMA */
@@ -524,7 +524,7 @@ typedef struct {
     uint32_t group;          /* 32, 64 or 128 */
     uint32_t gated;          /* 0 or 1 */
     uint32_t input_layout;   /* mm_q4_id_direct: 0 shared per token, 1 slotted */
-    int64_t ldx, ldy;        /* row pitches of x and y */
+    int64_t ldx, ldy;        /* row pitches of x (below 2^25) and y */
 } mm_q4_params;
 
 /* One matrix: y[i] = W . x[i] for i < m. The codes must be 16-byte aligned

@@ -215,7 +215,7 @@ def run_sort(dt, x, ids, E, ld_t=0, ld_r=0, shift=0):
     di = ids_buf(ids)
     p = mm.sort_params(dt, m, k, E, h, ld_tokens=ld_t, ld_rows=ld_r)
     rec = mm.mm_id_sort(p, xt.buf, mm.buf(di), xs.buf, off.buf, order.buf, pos.buf, stream=stream())
-    assert rec.route == mm.MM_ROUTE_SORT and rec.kernel == mm.MM_KERNEL_SORT_GATHER
+    assert rec.route == mm.MM_ROUTE_SORT and rec.kernel == mm.MM_KERNEL_SORT_ROWS
     for b in (xs, off, order, pos):
         b.untouched()
     return xs, off, order, pos
