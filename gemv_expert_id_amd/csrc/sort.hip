@@ -27,6 +27,8 @@ constexpr int PThreads = 1024;
 constexpr int PWaves = PThreads / kWave;
 constexpr int CThreads = 256;
 constexpr int CWaves = CThreads / kWave;
+constexpr int SThreads = 512;  // of the sort in one launch: its blocks share the count
+constexpr int SWaves = SThreads / kWave;
 
 // Inclusive sum over the lanes up to this one: within rows of 16 lanes, then
 // each row's last lane onto the rows after it.
@@ -133,18 +135,23 @@ __global__ __launch_bounds__(PThreads) void sort_plan(SortArgs a) {
     }
 }
 
-// 16 bytes of a row that is aligned to its element only.
+// 16 bytes of a row that is aligned to its element only. Rows are stored past
+// the caches: they are large, and the reads beside them keep their place
+// (sort of 512 x 8 f32 rows of 2048 12.8 -> 10.8 us, combination of 8192 x 8
+// bf16 rows of 2048 73 -> 67 us, gradient at 2048 x 4 f16 rows of 4096 32 -> 24 us).
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 template <class S>
-struct __attribute__((packed, aligned(sizeof(S)))) Chunk {
-    u32x4 v;
-};
-template <class S>
+using Chunk = std::conditional_t<sizeof(S) == 4, u32x4_a4, u32x4_a2>;
+template <class S, bool NT = false>
 __device__ __forceinline__ u32x4 ld_chunk(const S* p) {
-    return reinterpret_cast<const Chunk<S>*>(p)->v;
+    const auto q = reinterpret_cast<const Chunk<S>*>(p);
+    if constexpr (NT) return __builtin_nontemporal_load(q);
+    else return *q;
 }
 template <class S>
 __device__ __forceinline__ void st_chunk(S* p, u32x4 v) {
-    reinterpret_cast<Chunk<S>*>(p)->v = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<Chunk<S>*>(p));
 }
 
 template <class T>
@@ -174,10 +181,10 @@ using Bits = std::conditional_t<T::code == 0, uint32_t, uint16_t>;
 
 // Elements j .. of a row of `width` at element offset `row`, up to 16 bytes of
 // them; zeros, and nothing touched, past the row's end.
-template <class S>
+template <class S, bool NT = false>
 __device__ __forceinline__ u32x4 get(const void* base, int64_t row, uint32_t j, uint32_t width) {
     const S* src = static_cast<const S*>(base) + row + j;
-    if (j + 16 / sizeof(S) <= width) return ld_chunk(src);
+    if (j + 16 / sizeof(S) <= width) return ld_chunk<S, NT>(src);
     u32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (uint32_t q = 0; q < 16 / sizeof(S) - 1; ++q) {
@@ -218,17 +225,17 @@ __global__ __launch_bounds__(CThreads) void sort_copy(SortArgs a) {
 // The whole sort in one launch, for few rows: block 0 counts the offsets, block
 // t + 1 the places of token t's slots.
 template <class S>
-__global__ __launch_bounds__(CThreads) void sort_small(SortArgs a) {
+__global__ __launch_bounds__(SThreads) void sort_small(SortArgs a) {
     constexpr int CH = 16 / sizeof(S);
     __shared__ uint32_t hist[MM_GROUPED_MAX_E + 1];
-    __shared__ uint32_t part[CWaves][KU];
+    __shared__ uint32_t part[SWaves][KU];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const uint32_t E = a.n_experts, R = a.m * a.top_k;
     if (blockIdx.x == 0) {
         if (blockIdx.y) return;
-        for (uint32_t e = threadIdx.x; e < E; e += CThreads) hist[e] = 0;
+        for (uint32_t e = threadIdx.x; e < E; e += SThreads) hist[e] = 0;
         __syncthreads();
-        for (uint32_t r = threadIdx.x; r < R; r += CThreads) {
+        for (uint32_t r = threadIdx.x; r < R; r += SThreads) {
             const uint32_t id = a.ids[r];
             if (id < E) atomicAdd(&hist[id], 1u);
         }
@@ -246,7 +253,7 @@ __global__ __launch_bounds__(CThreads) void sort_small(SortArgs a) {
         return;
     }
     const uint32_t t = blockIdx.x - 1;
-    const uint32_t j = (blockIdx.y * CThreads + threadIdx.x) * CH;
+    const uint32_t j = (blockIdx.y * SThreads + threadIdx.x) * CH;
     u32x4 v = {0, 0, 0, 0};
     if (j < a.width) v = get<S>(a.tokens, (int64_t)t * a.ld_tokens, j, a.width);
     for (uint32_t s0 = 0; s0 < a.top_k; s0 += KU) {
@@ -258,7 +265,7 @@ __global__ __launch_bounds__(CThreads) void sort_small(SortArgs a) {
             key[u] = id < E ? id : E;
             n[u] = 0;
         }
-        for (uint32_t r = threadIdx.x * 4; r < R; r += CThreads * 4) {
+        for (uint32_t r = threadIdx.x * 4; r < R; r += SThreads * 4) {
             uint32_t k4[4];
             load_keys(a, r, R, 0xFFFFFFFFu, k4);
 #pragma unroll
@@ -278,7 +285,7 @@ __global__ __launch_bounds__(CThreads) void sort_small(SortArgs a) {
             if (s0 + u >= a.top_k) break;
             uint32_t i = 0;
 #pragma unroll
-            for (int w = 0; w < CWaves; ++w) i += part[w][u];
+            for (int w = 0; w < SWaves; ++w) i += part[w][u];
             const uint32_t r = t * a.top_k + s0 + u;
             if (threadIdx.x == 0 && blockIdx.y == 0) {
                 a.order_w[i] = r;
@@ -300,8 +307,9 @@ __device__ __forceinline__ uint32_t live_rows(const SortArgs& a) {
 }
 
 // out[t] = residual[t] + sum_s w[t][s] y[position]; without weights each is 1.
-// W: has weights. A block takes one token and one piece of its row.
-template <class T, bool W>
+// W: has weights. A block takes one token and one piece of its row. NT: the
+// expert rows are read past the caches.
+template <class T, bool W, bool NT>
 __global__ __launch_bounds__(CThreads) void combine(SortArgs a) {
     constexpr int CH = T::Elems16;
     const uint32_t live = live_rows(a);
@@ -318,7 +326,7 @@ __global__ __launch_bounds__(CThreads) void combine(SortArgs a) {
                 const uint32_t r = (uint32_t)t * a.top_k + s0 + u;
                 const uint32_t i = s0 + u < a.top_k ? (a.position ? a.position[r] : r) : 0xFFFFFFFFu;
                 on[u] = i < live;
-                if (on[u]) y[u] = get<Bits<T>>(a.rows, (int64_t)i * a.ld_rows, j, a.width);
+                if (on[u]) y[u] = get<Bits<T>, NT>(a.rows, (int64_t)i * a.ld_rows, j, a.width);
             }
 #pragma unroll
             for (int u = 0; u < KU; ++u) {
@@ -334,61 +342,67 @@ __global__ __launch_bounds__(CThreads) void combine(SortArgs a) {
     }
 }
 
-// dy[i] = w dout[t], dw = <dout[t], y[i]>. A block takes one token.
+// dy[i] = w dout[t], dw = <dout[t], y[i]>. One wave for each routed row: rows of
+// an odd length begin anywhere in 16 bytes, and a wave can take dy's from its
+// first 16-byte boundary on, with single elements before and after (2048 x 8
+// bf16 rows of 4095: 68 us from the row's start, 62 us so; a block for all
+// rows of a token, which reads dout once, 89 us).
 template <class T>
 __global__ __launch_bounds__(CThreads) void combine_grad(SortArgs a) {
-    constexpr int CH = T::Elems16;
-    __shared__ float part[CWaves][KU];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    using S = typename T::store_t;
+    constexpr int CH = T::Elems16, U = 4;  // chunks under way
+    const int lane = threadIdx.x & (kWave - 1);
     const uint32_t R = a.m * a.top_k, live = live_rows(a);
-    for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
-        for (uint32_t s0 = 0; s0 < a.top_k; s0 += KU) {
-            uint32_t at[KU];
-            float w[KU], dot[KU];
+    for (int64_t r = (int64_t)blockIdx.x * CWaves + threadIdx.x / kWave; r < R;
+         r += (int64_t)gridDim.x * CWaves) {
+        const uint32_t i = a.position ? a.position[r] : (uint32_t)r;
+        const bool on = i < live;
+        const float w = on ? a.weights[r] : 0.f;
+        float dot = 0.f;
+        if (i < R) {
+            const S* d = static_cast<const S*>(a.tokens) + (r / a.top_k) * a.ld_tokens;
+            const S* y = static_cast<const S*>(a.rows) + (int64_t)i * a.ld_rows;
+            S* dy = static_cast<S*>(a.rows_w) + (int64_t)i * a.ld_rows;
+            const uint32_t to16 = (uint32_t)(-(uintptr_t)dy & 15) / sizeof(S);
+            const uint32_t head = to16 < a.width ? to16 : a.width;
+            const uint32_t end = head + (a.width - head) / CH * CH;
+            const auto one = [&](uint32_t q) {
+                const float g = on ? widen(T{}, d[q]) : 0.f;
+                if (on) dot = __builtin_fmaf(g, widen(T{}, y[q]), dot);
+                dy[q] = narrow(T{}, on ? w * g : 0.f);
+            };
+            if (lane < (int)head) one(lane);
+            if (end + lane < a.width) one(end + lane);
+            for (uint32_t j = head + lane * CH; j < end; j += U * kWave * CH) {
+                u32x4 vd[U], vy[U];
 #pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                const uint32_t r = (uint32_t)t * a.top_k + s0 + u;
-                at[u] = s0 + u < a.top_k ? (a.position ? a.position[r] : r) : 0xFFFFFFFFu;
-                w[u] = at[u] < live ? a.weights[r] : 0.f;
-                dot[u] = 0.f;
-            }
-            for (uint32_t j = threadIdx.x * CH; j < a.width; j += CThreads * CH) {
-                u32x4 y[KU];
-                const u32x4 d = get<Bits<T>>(a.tokens, t * a.ld_tokens, j, a.width);
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t q = j + u * kWave * CH;
+                    if (on && q < end) {
+                        vd[u] = ld_chunk(d + q);
+                        vy[u] = ld_chunk(y + q);
+                    }
+                }
 #pragma unroll
-                for (int u = 0; u < KU; ++u)
-                    if (at[u] < live) y[u] = get<Bits<T>>(a.rows, (int64_t)at[u] * a.ld_rows, j, a.width);
-                float g[CH];
-                unpack<T>(d, g);
-#pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    if (at[u] >= R) continue;
-                    float f[CH] = {}, o[CH] = {};
-                    if (at[u] < live) {
-                        unpack<T>(y[u], f);
+                for (int u = 0; u < U; ++u) {
+                    const uint32_t q0 = j + u * kWave * CH;
+                    if (q0 >= end) break;
+                    float g[CH], f[CH], o[CH] = {};
+                    if (on) {
+                        unpack<T>(vd[u], g);
+                        unpack<T>(vy[u], f);
 #pragma unroll
                         for (int q = 0; q < CH; ++q) {
-                            dot[u] = __builtin_fmaf(g[q], f[q], dot[u]);
-                            o[q] = w[u] * g[q];
+                            dot = __builtin_fmaf(g[q], f[q], dot);
+                            o[q] = w * g[q];
                         }
                     }
-                    put<Bits<T>>(a.rows_w, (int64_t)at[u] * a.ld_rows, j, a.width, repack<T>(o));
+                    st_chunk(dy + q0, repack<T>(o));
                 }
             }
-#pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                const float sum = wave_add(dot[u]);
-                if (lane == 0) part[wave][u] = sum;
-            }
-            __syncthreads();
-            if (threadIdx.x < KU && s0 + threadIdx.x < a.top_k) {
-                float sum = 0.f;
-#pragma unroll
-                for (int v = 0; v < CWaves; ++v) sum += part[v][threadIdx.x];
-                a.dweights_w[(uint32_t)t * a.top_k + s0 + threadIdx.x] = sum;
-            }
-            __syncthreads();
         }
+        dot = wave_add(dot);
+        if (lane == 0) a.dweights_w[r] = on ? dot : 0.f;
     }
 }
 
@@ -399,8 +413,8 @@ uint32_t cap(int64_t n) { return (uint32_t)(n < 1 ? 1 : n < (1 << 20) ? n : (1 <
 namespace {
 
 // Grid over tokens and pieces of a row (width <= 2^24: at most 2^14 pieces).
-dim3 row_grid(int64_t blocks, uint32_t width, int dtype) {
-    const uint32_t per = CThreads * (dtype == 0 ? 4 : 8);
+dim3 row_grid(int64_t blocks, uint32_t width, int dtype, uint32_t threads) {
+    const uint32_t per = threads * (dtype == 0 ? 4 : 8);
     return dim3(cap(blocks), (width + per - 1) / per);
 }
 
@@ -421,21 +435,38 @@ hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_SORT_ROWS;
     const bool small = sort_launches(a) == 1;
     L->variant = small ? 1 : 0;
+    const uint32_t threads = small ? SThreads : CThreads;
     const void* fn = small ? (a.dtype == 0 ? (const void*)&sort_small<uint32_t> : (const void*)&sort_small<uint16_t>)
                            : (a.dtype == 0 ? (const void*)&sort_copy<uint32_t> : (const void*)&sort_copy<uint16_t>);
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, row_grid(small ? (int64_t)a.m + 1 : (int64_t)a.m, a.width, a.dtype), dim3(CThreads),
-                           args, 0, s);
+    return hipLaunchKernel(fn, row_grid(small ? (int64_t)a.m + 1 : (int64_t)a.m, a.width, a.dtype, threads),
+                           dim3(threads), args, 0, s);
 }
+
+namespace {
+
+template <class T>
+const void* pick_combine(bool w, bool nt) {
+    if (!w) return nt ? (const void*)&combine<T, false, true> : (const void*)&combine<T, false, false>;
+    return nt ? (const void*)&combine<T, true, true> : (const void*)&combine<T, true, false>;
+}
+
+}  // namespace
+
+// From this size on the expert rows pass the caches by. They come from the call
+// before: up to about half of the 256 MiB Infinity Cache is still there, more is
+// not (268 MB 66.8 -> 62.8 us, 134 MB 35.0 -> 32.1 us; 67 MB 15.5 -> 16.8 us).
+constexpr int64_t kPastCacheBytes = 128 << 20;
 
 hipError_t launch_combine(const SortArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_COMBINE;
     const bool w = a.weights != nullptr;
-    const void* fn = a.dtype == 0   ? (w ? (const void*)&combine<TF32, true> : (const void*)&combine<TF32, false>)
-                     : a.dtype == 1 ? (w ? (const void*)&combine<TF16, true> : (const void*)&combine<TF16, false>)
-                                    : (w ? (const void*)&combine<TBF16, true> : (const void*)&combine<TBF16, false>);
+    const bool nt = (int64_t)a.m * a.top_k * a.width * (a.dtype == 0 ? 4 : 2) >= kPastCacheBytes;
+    const void* fn = a.dtype == 0   ? pick_combine<TF32>(w, nt)
+                     : a.dtype == 1 ? pick_combine<TF16>(w, nt)
+                                    : pick_combine<TBF16>(w, nt);
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, row_grid(a.m, a.width, a.dtype), dim3(CThreads), args, 0, s);
+    return hipLaunchKernel(fn, row_grid(a.m, a.width, a.dtype, CThreads), dim3(CThreads), args, 0, s);
 }
 
 hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s, Launched* L) {
@@ -444,7 +475,8 @@ hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s, Launched* L) {
                      : a.dtype == 1 ? (const void*)&combine_grad<TF16>
                                     : (const void*)&combine_grad<TBF16>;
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, dim3(cap(a.m)), dim3(CThreads), args, 0, s);
+    return hipLaunchKernel(fn, dim3(cap(((int64_t)a.m * a.top_k + CWaves - 1) / CWaves)), dim3(CThreads),
+                           args, 0, s);
 }
 
 }  // namespace mmk
