@@ -7,10 +7,10 @@
 // activations the A operand (row = token):
 //   - A code becomes an operand by placing its four bits in the mantissa of
 //     16.0, which is 16 + q, exact in f16 and bf16: one shift and one
-//     and-or for two codes, no conversion. With the group's sum of x, which the
-//     same instruction gives from a constant operand, s (q . x) + b sum(x) =
-//     s ((16 + q) . x) + (b - 16 s) sum(x). Scales enter in f32 after a
-//     group's instructions, so no weight is ever rounded.
+//     and-or for two codes, no conversion. With the group's sum of x, taken
+//     where x is staged, s (q . x) + b sum(x) = s ((16 + q) . x) + (b - 16 s)
+//     sum(x). Scales enter in f32 after a group's instructions, so no weight
+//     is ever rounded.
 //   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact) that
 //     accumulate into one result.
 //   - A sum must not leave its group. The four lane groups of an instruction
@@ -27,6 +27,8 @@
 // different rows of W and share x, staged a chunk of k at a time in two buffers,
 // one barrier a chunk. Both issue the loads of the next chunk before computing
 // the current one.
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -44,7 +46,6 @@ struct __attribute__((packed, aligned(sizeof(S)))) QChunk {
 // Operand format of the codes and the activations.
 struct CoreF16 {
     static constexpr uint32_t kSixteen = 0x4C004C00u;
-    static constexpr uint32_t kOne = 0x3C003C00u;
     static constexpr int kShift = 6;  // the code's place in the mantissa of 16.0
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
@@ -53,7 +54,6 @@ struct CoreF16 {
 };
 struct CoreBF16 {
     static constexpr uint32_t kSixteen = 0x41804180u;
-    static constexpr uint32_t kOne = 0x3F803F80u;
     static constexpr int kShift = 3;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -64,14 +64,16 @@ template <class T> struct CoreOf { using type = CoreBF16; };
 template <> struct CoreOf<TF16> { using type = CoreF16; };
 
 // Eight codes (nibble i = element i) to 16 + q in the order 0 4 1 5 2 6 3 7.
+// The mask is a scalar, the 16.0s a vector register: as literals they would not
+// fit one and-or.
 template <class C>
-__device__ __forceinline__ u32x4 codes16(uint32_t w) {
+__device__ __forceinline__ u32x4 codes16(uint32_t w, uint32_t mask, uint32_t sixteen) {
     u32x4 r;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int sh = 4 * p - C::kShift;
         const uint32_t t = sh >= 0 ? w >> (sh >= 0 ? sh : 0) : w << (sh < 0 ? -sh : 0);
-        r[p] = (t & (0x000F000Fu << C::kShift)) | C::kSixteen;
+        r[p] = (t & mask) | sixteen;
     }
     return r;
 }
@@ -214,6 +216,28 @@ __device__ __forceinline__ Rows block_rows(const Q4Args& a, uint32_t n0) {
     return r;
 }
 
+// Sum of an octet's activations over the GROUP / 8 lanes that hold its group.
+template <class T, int GROUP, int XR>
+__device__ __forceinline__ float group_sum(const u32x4 (&q)[XR]) {
+    float f[8];
+    if constexpr (T::code == 0) {
+        unpack4(q[0], f);
+        unpack4(q[XR - 1], f + 4);
+    } else {
+        unpack8(T{}, q[0], f);
+    }
+    float v = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+    const auto from = [&](auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+            0, (int)__float_as_uint(v), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    v += from(std::integral_constant<int, 0xB1>{});   // quad_perm 1 0 3 2
+    v += from(std::integral_constant<int, 0x4E>{});   // quad_perm 2 3 0 1
+    if constexpr (GROUP >= 64) v += from(std::integral_constant<int, 0x141>{});   // row_half_mirror
+    if constexpr (GROUP >= 128) v += from(std::integral_constant<int, 0x140>{});  // row_mirror
+    return v;
+}
+
 // Sums of NT tiles of 16 weight rows over a range of k: the operands' places,
 // the loads of a chunk of CS steps, and its arithmetic.
 template <class T, class ST, int GROUP, int MI, int NT, int CS>
@@ -230,7 +254,11 @@ struct Tiles {
     static constexpr int OCT = CS * QStep / 8;              // octets of a token's chunk
     static constexpr int PITCH = OCT + 1;                   // in 16-byte units; odd: banks
     static constexpr int XR = PARTS == 3 ? 2 : 1;           // 16-byte loads of an octet
-    using Stage = u32x4[PARTS][ROWS][PITCH];
+    struct Stage {
+        u32x4 x[PARTS][ROWS][PITCH];
+        // Each token's sum of a group; MI = 1: a token's groups together.
+        __attribute__((aligned(16))) float sum[MI == 1 ? VT : NV][MI == 1 ? NV : VT];
+    };
 
     struct Codes {
         u32x4 w[CS][NT];
@@ -241,7 +269,7 @@ struct Tiles {
     const uint16_t *sc[NT], *bi[NT];
     uint32_t coff[NT], goff[NT];   // this lane's row and chunk from there
     f32x4 out[NT];                 // MI = 1: out[t][0] alone
-    uint32_t k, groups;
+    uint32_t k, groups, mask, sixteen;
     int c, xrow;
 
     // j[t]: first row of tile t; rows past `end` repeat the last and are not stored.
@@ -267,6 +295,9 @@ struct Tiles {
         const int tok = MI == 1 ? r16 >> 2 : r16;
         xrow = tok < (int)cnt ? tok : (int)cnt - 1;
         if (MASKED && (r16 & 3) != c) xrow = VT;
+        mask = 0x000F000Fu << C::kShift;
+        sixteen = C::kSixteen;
+        asm volatile("" : "+s"(mask), "+v"(sixteen));
     }
 
     // Scales first, codes by step: a step is computed as soon as its own have arrived.
@@ -322,11 +353,13 @@ struct Tiles {
         u32x4 parts[PARTS];
         octet<T>(q, parts);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) xs[p][v][o] = parts[p];
+        for (int p = 0; p < PARTS; ++p) xs.x[p][v][o] = parts[p];
+        // The lanes of 16 neighbouring octets hold one token: whole rows of lanes are here.
+        const float sum = group_sum<T, GROUP>(q);
+        if (o % (GROUP / 8) == 0) xs.sum[MI == 1 ? v : o / (GROUP / 8)][MI == 1 ? o / (GROUP / 8) : v] = sum;
     }
 
     __device__ __forceinline__ void compute(const Codes& q, const Stage& xs, uint32_t s0, uint32_t st1) {
-        const u32x4 one = {C::kOne, C::kOne, C::kOne, C::kOne};
         // Accumulators that one chain of instructions fills; groups of those.
         constexpr int CHAINS = MI == 1 ? 1 : GPS, PER = 4 / CHAINS;
 #pragma unroll
@@ -348,7 +381,6 @@ struct Tiles {
             }
 #pragma unroll
             for (int gp = 0; gp < CHAINS; ++gp) {
-                f32x4 sum = {0.f, 0.f, 0.f, 0.f};
                 u32x4 av[PARTS][PER];
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
@@ -358,17 +390,22 @@ struct Tiles {
                                     : GROUP == 64 ? 8 * (g >> 1) + 4 * (c & 1) + 2 * (c >> 1) + (g & 1)
                                                   : 4 * g + c;
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) {
-                        av[p][j] = xs[p][xrow][i * (QStep / 8) + oct];
-                        sum = C::mma(av[p][j], one, sum);
-                    }
+                    for (int p = 0; p < PARTS; ++p) av[p][j] = xs.x[p][xrow][i * (QStep / 8) + oct];
+                }
+                float sum[4];
+                if constexpr (MI == 1) {
+#pragma unroll
+                    for (int h = 0; h < GPS; ++h) sum[h] = xs.sum[c][i * GPS + h];
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sum[v] = xs.sum[i * GPS + gp][4 * c + v];
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
-                        const u32x4 bq = codes16<C>(cw[t][gp * PER + j]);
+                        const u32x4 bq = codes16<C>(cw[t][gp * PER + j], mask, sixteen);
 #pragma unroll
                         for (int p = 0; p < PARTS; ++p) d = C::mma(av[p][j], bq, d);
                     }
@@ -382,8 +419,7 @@ struct Tiles {
                         const float b16 = __builtin_fmaf(-16.f, sv, bv);
                         if constexpr (MI == 1) {
                             const float dv = GROUP == 64 ? d[2 * h] + d[2 * h + 1] : d[h];
-                            const float xv = GROUP == 64 ? sum[2 * h] + sum[2 * h + 1] : sum[h];
-                            out[t][0] = __builtin_fmaf(b16, xv, __builtin_fmaf(sv, dv, out[t][0]));
+                            out[t][0] = __builtin_fmaf(b16, sum[h], __builtin_fmaf(sv, dv, out[t][0]));
                         } else {
 #pragma unroll
                             for (int v = 0; v < MI; ++v)
@@ -401,7 +437,7 @@ __device__ __forceinline__ float gate(float g, float u) { return g / (1.f + expf
 
 // Each wave takes a piece of k of the block's rows (16, or 16 gates and 16 ups).
 template <class T, class ST, int GROUP, int MI, bool GATED, int W>
-__global__ __launch_bounds__(W* kWave, MI == 4 ? 2 : 4) void q4_split(Q4Args a) {
+__global__ __launch_bounds__(W* kWave, MI == 4 && T::code == 0 ? 2 : 4) void q4_split(Q4Args a) {
     constexpr int NT = GATED ? 2 : 1;
     constexpr int CS = T::code == 0 ? (MI == 1 ? 2 : 1) : (MI == 1 && !GATED ? 4 : 2);
     using Z = Tiles<T, ST, GROUP, MI, NT, CS>;
@@ -437,7 +473,7 @@ __global__ __launch_bounds__(W* kWave, MI == 4 ? 2 : 4) void q4_split(Q4Args a) 
     if (Z::MASKED) {
         for (int o = lane; o < OCT; o += kWave)
 #pragma unroll
-            for (int p = 0; p < Z::PARTS; ++p) xs[p][Z::ROWS - 1][o] = u32x4{0, 0, 0, 0};
+            for (int p = 0; p < Z::PARTS; ++p) xs.x[p][Z::ROWS - 1][o] = u32x4{0, 0, 0, 0};
     }
 
     struct Chunk {
@@ -499,14 +535,13 @@ __global__ __launch_bounds__(W* kWave, MI == 4 ? 2 : 4) void q4_split(Q4Args a) 
     y[(int64_t)v * a.ldy + n0 + j] = narrow(T{}, GATED ? gate(sum[0], sum[NT - 1]) : sum[0]);
 }
 
-// Each wave takes 32 rows of W (16 gates and 16 ups) and all of k, for 16 tokens.
-template <class T, class ST, int GROUP, bool GATED, int W>
-__global__ __launch_bounds__(W* kWave, 4) void q4_block(Q4Args a) {
-    constexpr int CS = 2;
-    using Z = Tiles<T, ST, GROUP, 4, 2, CS>;
+// Each wave takes 16 * NT rows of W (half gates, half ups) and all of k, for 16 tokens.
+template <class T, class ST, int GROUP, bool GATED, int NT, int CS, int W>
+__global__ __launch_bounds__(W* kWave, T::code == 0 ? 3 : 4) void q4_block(Q4Args a) {
+    using Z = Tiles<T, ST, GROUP, 4, NT, CS>;
     using S = typename T::store_t;
     constexpr int VT = Z::VT, OCT = Z::OCT;
-    constexpr int COLS = (GATED ? 16 : 32) * W;
+    constexpr int TN = GATED ? NT / 2 : NT, COLS = 16 * TN * W;
     static_assert(VT * OCT % (W * kWave) == 0, "whole octets a lane");
     constexpr int XL = VT * OCT / (W * kWave);
     __shared__ typename Z::Stage xs[2];
@@ -523,13 +558,14 @@ __global__ __launch_bounds__(W* kWave, 4) void q4_block(Q4Args a) {
 
     Z z;
     const uint32_t nw = n0 + wave * (COLS / W);
-    if constexpr (GATED) {
-        const uint32_t j[2] = {nw < a.n ? nw : a.n - 1, a.n + (nw < a.n ? nw : a.n - 1)}, end[2] = {a.n, 2 * a.n};
-        z.init(a, (uint64_t)rows.expert * 2 * a.n, j, end, lane, cnt);
-    } else {
-        const uint32_t j[2] = {nw, nw + 16}, end[2] = {a.n, a.n};
-        z.init(a, (uint64_t)rows.expert * a.n, j, end, lane, cnt);
+    uint32_t j[NT], end[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const uint32_t jt = nw + t % TN * 16;
+        j[t] = (jt < a.n ? jt : a.n - 1) + t / TN * a.n;
+        end[t] = (1 + t / TN) * a.n;
     }
+    z.init(a, (uint64_t)rows.expert * (GATED ? 2 * a.n : a.n), j, end, lane, cnt);
 
     u32x4 xr[XL][Z::XR];
     const auto load_x = [&](uint32_t s0) {
@@ -549,7 +585,7 @@ __global__ __launch_bounds__(W* kWave, 4) void q4_block(Q4Args a) {
             load_x(s0 + CS);
             z.load(nxt, s0 + CS, steps);
         }
-        // A buffer is written again two chunks later: past the next barrier.
+        // A buffer is written again two chunks later, past the next barrier.
         __syncthreads();
         z.compute(cur, buf, s0, steps);
     };
@@ -563,27 +599,27 @@ __global__ __launch_bounds__(W* kWave, 4) void q4_block(Q4Args a) {
 
     S* const y = static_cast<S*>(a.y) + (int64_t)rows.row0 * a.ldy;
 #pragma unroll
-    for (int t = 0; t < (GATED ? 1 : 2); ++t) {
+    for (int t = 0; t < TN; ++t) {
         const uint32_t col = nw + t * 16 + (lane & 15);
         if (col >= a.n) continue;
 #pragma unroll
         for (int v = 0; v < 4; ++v)
             if (4 * z.c + v < (int)cnt)
                 y[(int64_t)(4 * z.c + v) * a.ldy + col] =
-                    narrow(T{}, GATED ? gate(z.out[0][v], z.out[1][v]) : z.out[t][v]);
+                    narrow(T{}, GATED ? gate(z.out[t][v], z.out[NT - TN + t][v]) : z.out[t][v]);
     }
 }
 
 // The instances: up to 4 tokens a tile; 16 tokens with k split over eight waves
 // (few blocks), or with the rows split over them.
 enum Form { NARROW, SPLIT, BLOCK };
-constexpr int kBlockWaves = 4;
+constexpr int kBlockWaves = 4, kBlockTiles = 2, kBlockSteps = 2;
 template <class T, class ST, int GROUP, bool GATED>
 const void* pick(Form f) {
     switch (f) {
         case NARROW: return (const void*)&q4_split<T, ST, GROUP, 1, GATED, 4>;
         case SPLIT: return (const void*)&q4_split<T, ST, GROUP, 4, GATED, 8>;
-        default: return (const void*)&q4_block<T, ST, GROUP, GATED, kBlockWaves>;
+        default: return (const void*)&q4_block<T, ST, GROUP, GATED, kBlockTiles, kBlockSteps, kBlockWaves>;
     }
 }
 template <class T, class ST>
@@ -615,7 +651,7 @@ hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L) {
     if (wide) {
         f = BLOCK;
         waves = kBlockWaves;
-        cols = (a.gated ? 16 : 32) * waves;
+        cols = 16 * (a.gated ? kBlockTiles / 2 : kBlockTiles) * waves;
         if (tiles * ((a.n + cols - 1) / cols) < 256) {
             f = SPLIT;
             cols = 16;
