@@ -7,12 +7,16 @@
 // activations the A operand (row = token):
 //   - A code becomes an operand by placing its four bits in the mantissa of
 //     16.0, which is 16 + q, exact in f16 and bf16: one shift and one
-//     and-or for two codes, no conversion. With the group's sum of x, taken
-//     where x is staged, s (q . x) + b sum(x) = s ((16 + q) . x) + (b - 16 s)
-//     sum(x). Scales enter in f32 after a group's instructions, so no weight
-//     is ever rounded.
-//   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact) that
-//     accumulate into one result.
+//     and-or for two codes, no conversion. The accumulator starts at -16 times
+//     the group's sum of x, taken where x is staged, and so ends at q . x
+//     (the 16 taken back after the instructions instead, by a coefficient
+//     b - 16 s, had 1.5 times the error). Scales enter in f32 after a group's
+//     instructions, so no weight is ever rounded.
+//   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact). The upper
+//     parts have an accumulator and a sum of their own: their products and sums
+//     are short enough to be nearly exact in f32, and the lower parts' roundings
+//     are small (error against 64 bits 2e-7 of the result; with one accumulator
+//     and one sum 5e-7 to 1.5e-6).
 //   - A sum must not leave its group. The four lane groups of an instruction
 //     hold the step's four 32-element chunks. With up to 4 tokens (MI = 1) the A
 //     operand has 16 rows for 4 tokens: row 4v + g holds token v in lane group g
@@ -216,16 +220,9 @@ __device__ __forceinline__ Rows block_rows(const Q4Args& a, uint32_t n0) {
     return r;
 }
 
-// Sum of an octet's activations over the GROUP / 8 lanes that hold its group.
-template <class T, int GROUP, int XR>
-__device__ __forceinline__ float group_sum(const u32x4 (&q)[XR]) {
-    float f[8];
-    if constexpr (T::code == 0) {
-        unpack4(q[0], f);
-        unpack4(q[XR - 1], f + 4);
-    } else {
-        unpack8(T{}, q[0], f);
-    }
+// Sum of eight values a lane over the GROUP / 8 lanes that hold a group.
+template <int GROUP>
+__device__ __forceinline__ float group_sum(const float (&f)[8]) {
     float v = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
     const auto from = [&](auto ctrl) {
         return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
@@ -245,6 +242,7 @@ struct Tiles {
     using S = typename T::store_t;
     using C = typename CoreOf<T>::type;
     static constexpr int PARTS = T::code == 0 ? 3 : 1;
+    static constexpr int SUMS = T::code == 0 ? 2 : 1;
     static constexpr int VT = MI == 1 ? 4 : 16;             // tokens
     static constexpr bool MASKED = MI == 1 && GROUP < QStep;
     static constexpr int ROWS = MASKED ? VT + 1 : VT;       // staged rows: a last one of zeros
@@ -256,8 +254,9 @@ struct Tiles {
     static constexpr int XR = PARTS == 3 ? 2 : 1;           // 16-byte loads of an octet
     struct Stage {
         u32x4 x[PARTS][ROWS][PITCH];
-        // Each token's sum of a group; MI = 1: a token's groups together.
-        __attribute__((aligned(16))) float sum[MI == 1 ? VT : NV][MI == 1 ? NV : VT];
+        // -16 times each token's sum of a group; MI = 1: a token's groups together.
+        // f32: of the upper parts, and of the rest.
+        __attribute__((aligned(16))) float sum[SUMS][MI == 1 ? VT : NV][MI == 1 ? NV : VT];
     };
 
     struct Codes {
@@ -355,8 +354,23 @@ struct Tiles {
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) xs.x[p][v][o] = parts[p];
         // The lanes of 16 neighbouring octets hold one token: whole rows of lanes are here.
-        const float sum = group_sum<T, GROUP>(q);
-        if (o % (GROUP / 8) == 0) xs.sum[MI == 1 ? v : o / (GROUP / 8)][MI == 1 ? o / (GROUP / 8) : v] = sum;
+        float f[SUMS][8];
+        if constexpr (T::code == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = q[i / 4][i % 4];
+                f[0][i] = __uint_as_float(bits & 0xFFFF0000u);
+                f[SUMS - 1][i] = __uint_as_float(bits) - f[0][i];
+            }
+        } else {
+            unpack8(T{}, q[0], f[0]);
+        }
+        const uint32_t g = o / (GROUP / 8);
+#pragma unroll
+        for (int h = 0; h < SUMS; ++h) {
+            const float sum = group_sum<GROUP>(f[h]);
+            if (o % (GROUP / 8) == 0) xs.sum[h][MI == 1 ? v : g][MI == 1 ? g : v] = -16.f * sum;
+        }
     }
 
     __device__ __forceinline__ void compute(const Codes& q, const Stage& xs, uint32_t s0, uint32_t st1) {
@@ -392,22 +406,39 @@ struct Tiles {
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) av[p][j] = xs.x[p][xrow][i * (QStep / 8) + oct];
                 }
-                float sum[4];
-                if constexpr (MI == 1) {
+                // -16 sum(x) of each group (MI = 1) or token: by parts, and whole.
+                float sums[SUMS][4], sum[4];
 #pragma unroll
-                    for (int h = 0; h < GPS; ++h) sum[h] = xs.sum[c][i * GPS + h];
-                } else {
+                for (int h = 0; h < SUMS; ++h)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) sum[v] = xs.sum[i * GPS + gp][4 * c + v];
-                }
+                    for (int v = 0; v < (MI == 1 ? GPS : 4); ++v)
+                        sums[h][v] = MI == 1 ? xs.sum[h][c][i * GPS + v] : xs.sum[h][i * GPS + gp][4 * c + v];
+#pragma unroll
+                for (int v = 0; v < (MI == 1 ? GPS : 4); ++v)
+                    sum[v] = SUMS == 1 ? sums[0][v] : sums[0][v] + sums[SUMS - 1][v];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                    f32x4 acc[SUMS];
+#pragma unroll
+                    for (int h = 0; h < SUMS; ++h) {
+                        // MI = 1: result i starts a group or continues it (two chunks of 64).
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            acc[h][v] = MI > 1               ? sums[h][v]
+                                        : v % (4 / GPS) == 0 ? sums[h][v / (4 / GPS)]
+                                                             : 0.f;
+                    }
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
                         const u32x4 bq = codes16<C>(cw[t][gp * PER + j], mask, sixteen);
+                        acc[0] = C::mma(av[0][j], bq, acc[0]);
 #pragma unroll
-                        for (int p = 0; p < PARTS; ++p) d = C::mma(av[p][j], bq, d);
+                        for (int p = 1; p < PARTS; ++p) acc[SUMS - 1] = C::mma(av[p][j], bq, acc[SUMS - 1]);
+                    }
+                    f32x4 d = acc[0];
+                    if constexpr (SUMS > 1) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) d[v] += acc[1][v];
                     }
                     // MI = 1: results 0..3 are the step's chunks (one value without
                     // the mask); MI = 4: four tokens of one group.
@@ -416,7 +447,7 @@ struct Tiles {
                         const int gi = i * GPS + gp + h;
                         const float sv = widen(ST{}, (uint16_t)(q.s[t][gi / 2] >> (16 * (gi & 1))));
                         const float bv = widen(ST{}, (uint16_t)(q.b[t][gi / 2] >> (16 * (gi & 1))));
-                        const float b16 = __builtin_fmaf(-16.f, sv, bv);
+                        const float b16 = bv * -0.0625f;  // of -16 sum(x)
                         if constexpr (MI == 1) {
                             const float dv = GROUP == 64 ? d[2 * h] + d[2 * h + 1] : d[h];
                             out[t][0] = __builtin_fmaf(b16, sum[h], __builtin_fmaf(sv, dv, out[t][0]));
