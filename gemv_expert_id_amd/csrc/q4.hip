@@ -8,10 +8,12 @@
 //   - A code becomes an operand by placing its four bits in the mantissa of
 //     16.0, which is 16 + q, exact in f16 and bf16: one shift and one
 //     and-or for two codes, no conversion. The accumulator starts at -16 times
-//     the group's sum of x, taken where x is staged, and so ends at q . x
-//     (the 16 taken back after the instructions instead, by a coefficient
-//     b - 16 s, had 1.5 times the error). Scales enter in f32 after a group's
-//     instructions, so no weight is ever rounded.
+//     the group's sum of x and so ends at q . x (the 16 taken back after the
+//     instructions instead, by a coefficient b - 16 s, had 1.5 times the error).
+//     The sum is taken where x is staged, or, for 16 tokens of 16 bits, by the
+//     same instruction with a constant operand (staging 31 -> 10 instructions
+//     an octet). Scales enter in f32 after a group's instructions, so no weight
+//     is ever rounded.
 //   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact). The upper
 //     parts have an accumulator and a sum of their own: their products and sums
 //     are short enough to be nearly exact in f32, and the lower parts' roundings
@@ -50,6 +52,7 @@ struct __attribute__((packed, aligned(sizeof(S)))) QChunk {
 // Operand format of the codes and the activations.
 struct CoreF16 {
     static constexpr uint32_t kSixteen = 0x4C004C00u;
+    static constexpr uint32_t kMinusSixteen = 0xCC00CC00u;
     static constexpr int kShift = 6;  // the code's place in the mantissa of 16.0
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
@@ -58,6 +61,7 @@ struct CoreF16 {
 };
 struct CoreBF16 {
     static constexpr uint32_t kSixteen = 0x41804180u;
+    static constexpr uint32_t kMinusSixteen = 0xC180C180u;
     static constexpr int kShift = 3;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -243,6 +247,7 @@ struct Tiles {
     using C = typename CoreOf<T>::type;
     static constexpr int PARTS = T::code == 0 ? 3 : 1;
     static constexpr int SUMS = T::code == 0 ? 2 : 1;
+    static constexpr bool STAGED_SUMS = MI == 1 || PARTS > 1;
     static constexpr int VT = MI == 1 ? 4 : 16;             // tokens
     static constexpr bool MASKED = MI == 1 && GROUP < QStep;
     static constexpr int ROWS = MASKED ? VT + 1 : VT;       // staged rows: a last one of zeros
@@ -354,6 +359,7 @@ struct Tiles {
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) xs.x[p][v][o] = parts[p];
         // The lanes of 16 neighbouring octets hold one token: whole rows of lanes are here.
+        if constexpr (!STAGED_SUMS) return;
         float f[SUMS][8];
         if constexpr (T::code == 0) {
 #pragma unroll
@@ -408,11 +414,20 @@ struct Tiles {
                 }
                 // -16 sum(x) of each group (MI = 1) or token: by parts, and whole.
                 float sums[SUMS][4], sum[4];
+                if constexpr (STAGED_SUMS) {
 #pragma unroll
-                for (int h = 0; h < SUMS; ++h)
+                    for (int h = 0; h < SUMS; ++h)
 #pragma unroll
-                    for (int v = 0; v < (MI == 1 ? GPS : 4); ++v)
-                        sums[h][v] = MI == 1 ? xs.sum[h][c][i * GPS + v] : xs.sum[h][i * GPS + gp][4 * c + v];
+                        for (int v = 0; v < (MI == 1 ? GPS : 4); ++v)
+                            sums[h][v] = MI == 1 ? xs.sum[h][c][i * GPS + v] : xs.sum[h][i * GPS + gp][4 * c + v];
+                } else {
+                    const u32x4 m16 = {C::kMinusSixteen, C::kMinusSixteen, C::kMinusSixteen, C::kMinusSixteen};
+                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) d = C::mma(av[0][j], m16, d);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sums[0][v] = d[v];
+                }
 #pragma unroll
                 for (int v = 0; v < (MI == 1 ? GPS : 4); ++v)
                     sum[v] = SUMS == 1 ? sums[0][v] : sums[0][v] + sums[SUMS - 1][v];
@@ -466,11 +481,20 @@ struct Tiles {
 // silu(g) u of the gated form.
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.f + expf(-g)) * u; }
 
-// Each wave takes a piece of k of the block's rows (16, or 16 gates and 16 ups).
-template <class T, class ST, int GROUP, int MI, bool GATED, int W>
-__global__ __launch_bounds__(W* kWave, MI == 4 && T::code == 0 ? 2 : 4) void q4_split(Q4Args a) {
-    constexpr int NT = GATED ? 2 : 1;
-    constexpr int CS = T::code == 0 ? (MI == 1 ? 2 : 1) : (MI == 1 && !GATED ? 4 : 2);
+// Waves on a SIMD that leave q4_split its registers: a spill would wait for every
+// load under way.
+constexpr int split_waves(bool f32, int group, int mi, bool two) {
+    if (mi == 4) return f32 ? 2 : two ? 3 : 4;
+    return two && f32 ? 2 : group == 32 ? 3 : 4;
+}
+
+// Each wave takes a piece of k of the block's rows (16 * TN; gated, as many gates
+// and ups).
+template <class T, class ST, int GROUP, int MI, bool GATED, int TN, int W>
+__global__ __launch_bounds__(W* kWave, split_waves(T::code == 0, GROUP, MI, GATED || TN > 1)) void q4_split(
+    Q4Args a) {
+    constexpr int NT = GATED ? 2 * TN : TN;
+    constexpr int CS = MI == 4 ? 1 : T::code == 0 || GATED ? 2 : 4;
     using Z = Tiles<T, ST, GROUP, MI, NT, CS>;
     using S = typename T::store_t;
     constexpr int VT = Z::VT, OCT = Z::OCT;
@@ -483,8 +507,8 @@ __global__ __launch_bounds__(W* kWave, MI == 4 && T::code == 0 ? 2 : 4) void q4_
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     typename Z::Stage& xs = reinterpret_cast<typename Z::Stage*>(lds)[wave];
-    const uint32_t n0 = blockIdx.x * 16;
-    const Rows rows = block_rows<S, VT, 16, W * kWave>(a, n0);
+    const uint32_t n0 = blockIdx.x * (16 * TN);
+    const Rows rows = block_rows<S, VT, 16 * TN, W * kWave>(a, n0);
     if (rows.cnt == 0) return;
     const uint32_t cnt = rows.cnt;
     const uint32_t steps = (a.k + QStep - 1) / QStep;
@@ -494,13 +518,14 @@ __global__ __launch_bounds__(W* kWave, MI == 4 && T::code == 0 ? 2 : 4) void q4_
         static_cast<const S*>(a.x) + (int64_t)(a.mode == Q4_IDS ? rows.row0 / a.x_div : rows.row0) * a.ldx);
 
     Z z;
-    if constexpr (GATED) {
-        const uint32_t j[2] = {n0, a.n + n0}, end[2] = {a.n, 2 * a.n};
-        z.init(a, (uint64_t)rows.expert * 2 * a.n, j, end, lane, cnt);
-    } else {
-        const uint32_t j[1] = {n0}, end[1] = {a.n};
-        z.init(a, (uint64_t)rows.expert * a.n, j, end, lane, cnt);
+    uint32_t first[NT], end[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const uint32_t jt = n0 + t % TN * 16;
+        first[t] = (jt < a.n ? jt : a.n - 1) + t / TN * a.n;
+        end[t] = (1 + t / TN) * a.n;
     }
+    z.init(a, (uint64_t)rows.expert * (GATED ? 2 * a.n : a.n), first, end, lane, cnt);
     if (Z::MASKED) {
         for (int o = lane; o < OCT; o += kWave)
 #pragma unroll
@@ -554,21 +579,23 @@ __global__ __launch_bounds__(W* kWave, MI == 4 && T::code == 0 ? 2 : 4) void q4_
         for (int v = 0; v < MI; ++v) join[wave][t][MI == 1 ? z.c : 4 * z.c + v][lane & 15] = z.out[t][v];
     __syncthreads();
     S* const y = static_cast<S*>(a.y) + (int64_t)rows.row0 * a.ldy;
-    const uint32_t v = threadIdx.x / 16, j = threadIdx.x % 16;
-    if (v >= cnt || n0 + j >= a.n) return;
-    float sum[NT];
+    for (uint32_t q = threadIdx.x; q < VT * 16 * TN; q += W * kWave) {
+        const uint32_t v = q / (16 * TN), t = q / 16 % TN, j = q % 16, col = n0 + t * 16 + j;
+        if (v >= cnt || col >= a.n) continue;
+        float sum[2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        sum[t] = join[0][t][v][j];
+        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            sum[h] = join[0][h * TN + t][v][j];
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum[t] += join[w][t][v][j];
+            for (int w = 1; w < W; ++w) sum[h] += join[w][h * TN + t][v][j];
+        }
+        y[(int64_t)v * a.ldy + col] = narrow(T{}, GATED ? gate(sum[0], sum[1]) : sum[0]);
     }
-    y[(int64_t)v * a.ldy + n0 + j] = narrow(T{}, GATED ? gate(sum[0], sum[NT - 1]) : sum[0]);
 }
 
 // Each wave takes 16 * NT rows of W (half gates, half ups) and all of k, for 16 tokens.
 template <class T, class ST, int GROUP, bool GATED, int NT, int CS, int W>
-__global__ __launch_bounds__(W* kWave, T::code == 0 ? 3 : 4) void q4_block(Q4Args a) {
+__global__ __launch_bounds__(W* kWave, T::code == 0 || GROUP == 32 ? 3 : 4) void q4_block(Q4Args a) {
     using Z = Tiles<T, ST, GROUP, 4, NT, CS>;
     using S = typename T::store_t;
     constexpr int VT = Z::VT, OCT = Z::OCT;
@@ -643,13 +670,16 @@ __global__ __launch_bounds__(W* kWave, T::code == 0 ? 3 : 4) void q4_block(Q4Arg
 
 // The instances: up to 4 tokens a tile; 16 tokens with k split over eight waves
 // (few blocks), or with the rows split over them.
-enum Form { NARROW, SPLIT, BLOCK };
+enum Form { NARROW, SPLIT, SPLIT2, BLOCK };
 constexpr int kBlockWaves = 4, kBlockTiles = 2, kBlockSteps = 2;
 template <class T, class ST, int GROUP, bool GATED>
 const void* pick(Form f) {
     switch (f) {
-        case NARROW: return (const void*)&q4_split<T, ST, GROUP, 1, GATED, 4>;
-        case SPLIT: return (const void*)&q4_split<T, ST, GROUP, 4, GATED, 8>;
+        case NARROW: return (const void*)&q4_split<T, ST, GROUP, 1, GATED, 1, 4>;
+        case SPLIT: return (const void*)&q4_split<T, ST, GROUP, 4, GATED, 1, GATED ? 4 : 8>;
+        case SPLIT2:
+            if constexpr (!GATED && T::code != 0) return (const void*)&q4_split<T, ST, GROUP, 4, false, 2, 4>;
+            return nullptr;
         default: return (const void*)&q4_block<T, ST, GROUP, GATED, kBlockTiles, kBlockSteps, kBlockWaves>;
     }
 }
@@ -684,9 +714,11 @@ hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L) {
         waves = kBlockWaves;
         cols = 16 * (a.gated ? kBlockTiles / 2 : kBlockTiles) * waves;
         if (tiles * ((a.n + cols - 1) / cols) < 256) {
-            f = SPLIT;
-            cols = 16;
-            waves = 8;
+            // Rows for 512 blocks: two tiles share the staged x (as gate and up do; with
+            // f32's three parts their registers do not fit).
+            f = tiles * ((a.n + 15) / 16) < 512 || a.gated || a.dtype == 0 ? SPLIT : SPLIT2;
+            cols = f == SPLIT ? 16 : 32;
+            waves = f == SPLIT && !a.gated ? 8 : 4;
         }
     }
     L->variant = (int)(vt + 256 * cols);
