@@ -134,8 +134,13 @@ typedef struct {
                                  times the panel height in rows (64 or 128);
                                  for MM_KERNEL_GEMM_LARGE the tile edge
                                  (256 or 128), plus 1 for the paired-stage
-                                 form (two k-stages per LDS region); 0 for
-                                 every other family */
+                                 form (two k-stages per LDS region); for
+                                 MM_KERNEL_TOPK and MM_KERNEL_TOPK_GRAD the
+                                 lanes a token takes (16 or 64); for
+                                 MM_KERNEL_SORT_ROWS 1 when the plan was made
+                                 in the same launch; for MM_KERNEL_Q4 the
+                                 tokens of a tile (4 or 16) plus 256 times the
+                                 outputs of a block; 0 for every other family */
 } mm_receipt;
 
 /* ------------------------------------------------------------------------ */

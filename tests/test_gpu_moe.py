@@ -143,6 +143,17 @@ def test_topk_masked_rows(dt, renormalize):
     check_topk(l, 4, renormalize)
 
 
+@pytest.mark.parametrize("dt", [0, 2])
+def test_topk_of_more_tokens_than_the_grid(dt):
+    m, E, k = 65536 * (4 if dt == 0 else 16) + 77, 5, 2
+    l = torch.randn(m, E, generator=gen(13)).to(TORCH[dt])
+    ids, w = run_topk(l, k, 1)
+    top = l.double().sort(dim=1, descending=True, stable=True)
+    np.testing.assert_array_equal(ids, top.indices[:, :k].numpy().astype(np.uint32))
+    want = torch.softmax(top.values[:, :k], 1).numpy()
+    near(w, want, 160 * U * want, "weights")
+
+
 @pytest.mark.parametrize("renormalize", [0, 1])
 def test_topk_nan_and_inf(renormalize):
     l = torch.randn(4, 70, generator=gen(11))
@@ -159,6 +170,24 @@ def test_topk_nan_and_inf(renormalize):
     assert ids[2, 0] == 9 and np.isnan(w[2]).all()
     np.testing.assert_array_equal(ids[3], want[3])
     assert np.isfinite(w[3]).all()
+
+
+@pytest.mark.parametrize("dt", [1, 2])
+def test_topk_nan_and_inf_in_16_bits(dt):
+    l = torch.randn(5, 70, generator=gen(12)).to(TORCH[dt])
+    l[0, 5], l[0, 60] = float("nan"), -float("nan")
+    l[1, :] = float("nan")
+    l[2, 9] = float("inf")
+    l[3, 1:] = float("-inf")
+    for renormalize in (0, 1):
+        ids, w = run_topk(l, 3, renormalize)
+        clean = l.clone()
+        clean[0, 5] = clean[0, 60] = float("-inf")
+        want, _ = ref.topk(f64(clean), 3, renormalize)
+        np.testing.assert_array_equal(ids[[0, 3, 4]], want[[0, 3, 4]])
+        assert np.isnan(w[0]).all() and (ids[1] == NONE).all() and (w[1] == 0).all()
+        assert ids[2, 0] == 9 and np.isnan(w[2]).all()
+        assert w[3, 0] == 1 and (w[3, 1:] == 0).all() and np.isfinite(w[4]).all()
 
 
 @pytest.mark.parametrize("dt", DTYPES)
@@ -509,6 +538,68 @@ def test_q4_id_sorted(dt, m, k_slots, counts, n, k, group, gated):
         expert[off[e]:off[e + 1]] = e
     want, err = routed(case, group, x, expert, bool(gated), dt, n)
     q4_check(y.cpu(), dt, want, err, "y")
+    y.untouched()
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k,group,gated", [(16, 8201, 352, 32, 0), (9, 8201, 704, 64, 0), (11, 4100, 1152, 128, 1),
+                                               (61, 8201, 352, 32, 0), (64, 8200, 704, 64, 0), (50, 4105, 640, 128, 1)])
+def test_q4_gemv_of_many_rows(dt, m, n, k, group, gated):
+    """Enough blocks for two staged tiles a wave, and for waves that split the rows."""
+    case = q4_case(1, n * (1 + gated), k, group, 1, n + k)
+    x = torch.randn(m, k, generator=gen(k)).to(TORCH[dt])
+    dev, xd, y = q4_dev(case), x.to(DEV), Padded(m, n, TORCH[dt])
+    rec = mm.mm_q4_gemv(mm.q4_params(dt, 1, m, n, k, group, gated=gated), *(mm.buf(t) for t in dev), mm.buf(xd), y.buf,
+                        stream=stream())
+    if -(-m // 16) * -(-n // (64 if gated else 128)) >= 256:
+        cols = 64 if gated else 128
+    else:
+        cols = 32 if dt != 0 and not gated else 16
+    assert rec.variant == 16 + 256 * cols
+    want, err = ref.q4_product(case[0][0], case[1][0], case[2][0], group, x, bool(gated), dt == 0)
+    q4_check(y.cpu(), dt, want, err, "y")
+    y.untouched()
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("n,k,group,gated", [(520, 704, 64, 0), (333, 352, 32, 1), (301, 1152, 128, 0), (260, 256, 64, 1),
+                                             (600, 32, 32, 0)])
+def test_q4_id_sorted_of_many_rows(dt, n, k, group, gated):
+    m, slots, E = 100, 8, 40
+    R = m * slots
+    counts = np.random.default_rng(n).multinomial(R - 30, np.random.default_rng(1).dirichlet(np.ones(E)))
+    off = offsets_of(counts, R)
+    case = q4_case(E, n * (1 + gated), k, group, 2, n + k)
+    x = torch.randn(R, k, generator=gen(k)).to(TORCH[dt])
+    x[int(off[-1]):] = float("nan")
+    y = Padded(R, n, TORCH[dt], n + 1, 1)
+    dev, xd, do = q4_dev(case), x.to(DEV), ids_buf(off)
+    p = mm.q4_params(dt, 2, m, n, k, group, n_experts=E, top_k=slots, gated=gated, ldy=n + 1)
+    rec = mm.mm_q4_id_sorted(p, *(mm.buf(t) for t in dev), mm.buf(xd), mm.buf(do), y.buf, stream=stream())
+    assert rec.variant == 16 + 256 * (64 if gated else 128)
+    expert = np.full(R, NONE, dtype=np.uint32)
+    for e in range(E):
+        expert[off[e]:off[e + 1]] = e
+    want, err = routed(case, group, x, expert, bool(gated), dt, n)
+    q4_check(y.cpu(), dt, want, err, "y")
+    y.untouched()
+
+
+def test_q4_more_tiles_than_one_grid_dimension():
+    n, k, group = 3, 32, 32
+    case = q4_case(1, n, k, group, 1, 5)
+    dev = q4_dev(case)
+    m = 16 * 33000 - 5
+    x = torch.randn(m, k, generator=gen(1)).to(torch.float16)
+    y, xd = Padded(m, n, torch.float16), x.to(DEV)
+    mm.mm_q4_gemv(mm.q4_params(1, 1, m, n, k, group), *(mm.buf(t) for t in dev), mm.buf(xd), y.buf, stream=stream())
+    want, err = ref.q4_product(case[0][0], case[1][0], case[2][0], group, x, False, False)
+    q4_check(y.cpu(), 1, want, err, "y")
+    m = 40000
+    ids, y = torch.zeros(m, 1, dtype=torch.int32, device=DEV), Padded(m, n, torch.float16)
+    mm.mm_q4_id_direct(mm.q4_params(1, 1, m, n, k, group), *(mm.buf(t) for t in dev), mm.buf(xd), mm.buf(ids), y.buf,
+                       stream=stream())
+    q4_check(y.cpu(), 1, want[:m], err[:m], "y by id")
     y.untouched()
 
 
