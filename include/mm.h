@@ -19,8 +19,9 @@
  *   `grouped_pipeline_resolution_failure_does_not_mutate_encoder`). A call
  *   that returns an error other than MM_ERR_DEVICE has enqueued nothing.
  *   MM_ERR_DEVICE means the HIP runtime refused a launch after validation;
- *   the one call that makes two launches (mm_id with the grouped route) may
- *   then leave its first launch, the map pass, enqueued (see mm_id).
+ *   a call that makes two launches (mm_id with the grouped route; mm_id_sort
+ *   of more than 8192 rows) may then leave its first launch, the map pass or
+ *   the sort's plan, enqueued (see mm_id, mm_id_sort).
  * - Asynchrony: on MM_OK the work is enqueued on `stream` (a hipStream_t; 0 =
  *   the null stream) and results are valid once the stream has reached that
  *   point. Stream order is the only ordering: a map launch followed by a
@@ -455,7 +456,8 @@ typedef struct {
  *   position[r] = place of routed row r                  (u32 [m*top_k])
  *   xs[i][:]    = x[order[i] / top_k][:], or +0 for i >= offsets[n_experts]
  * Ids may repeat within a token. x is dtype [m, width], xs dtype
- * [m*top_k, width].
+ * [m*top_k, width]. One launch up to 8192 routed rows, two beyond: if the HIP
+ * runtime refuses the second, offsets, order and position are still written.
  */
 mm_status mm_id_sort(const mm_sort_params *params, mm_buf x, mm_buf ids, mm_buf xs,
                      mm_buf offsets, mm_buf order, mm_buf position, void *stream,
