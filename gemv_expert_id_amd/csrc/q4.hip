@@ -33,6 +33,13 @@
 // different rows of W and share x, staged a chunk of k at a time in two buffers,
 // one barrier a chunk. Both issue the loads of the next chunk before computing
 // the current one.
+//
+// Measured (kernel alone): one token, 11008 x 4096 f16, groups of 128: 8.3 us, 2.9
+// TB/s; one token's eight gated experts of 1408 x 2048, bf16, groups of 32: 10.1 us,
+// 2.9 TB/s; both a launch, one or two memory round trips and 2 to 3 us of vector
+// issue. 512 f32 rows over 64 experts of 2048 x 1408, groups of 64: 46 us, 2.4 TB/s,
+// bound by vector issue (19 us) and matrix instructions (8 us) between barriers. A
+// stream of the same bytes in this access pattern reaches 5.1 TB/s.
 #include <type_traits>
 
 #include "common.hpp"
@@ -700,26 +707,36 @@ const void* pick(const Q4Args& a, Form f) {
 
 hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_Q4;
-    // Sixteen tokens a tile where an expert has more than 4 rows on average.
-    const bool wide = a.mode == Q4_DENSE ? a.rows > 4 : a.mode == Q4_SORTED && a.rows > 4ull * a.n_experts;
-    const uint32_t vt = wide ? 16 : 4;
-    uint64_t tiles = a.rows;
-    if (a.mode == Q4_DENSE) tiles = (a.rows + vt - 1) / vt;
     // Sorted: every expert with rows may end inside a tile.
-    if (a.mode == Q4_SORTED) tiles = a.rows / vt + (a.rows < a.n_experts ? a.rows : a.n_experts);
+    const uint64_t ends = a.mode == Q4_SORTED ? (a.rows < a.n_experts ? a.rows : a.n_experts) : 0;
+    const auto tiles_of = [&](uint32_t vt) { return a.mode == Q4_SORTED ? a.rows / vt + ends : (a.rows + vt - 1ull) / vt; };
+    // The sharing form from two blocks a CU on (64 tokens, n = 4096, 8192, 11008: it takes 27, 28,
+    // 43 us, the split 16, 29, 40), where rows repeat a staged x and an unpacked code
+    // enough: sorted from 1 row an expert on (f16 2048 x 1408, 64 experts: 17.0 us
+    // against 19.4 with tiles of 4; f32 23.8 and 26.5), gated 16-bit ones from 3
+    // (51.6 and 51.8; at 2 46.1 and 42.5).
+    const uint32_t block_cols = 16 * (a.gated ? kBlockTiles / 2 : kBlockTiles) * kBlockWaves;
+    const uint32_t per_expert = a.mode == Q4_DENSE ? 5 : a.gated && a.dtype != 0 ? 3 : 1;
+    const bool block = a.mode != Q4_IDS && a.rows >= (uint64_t)per_expert * a.n_experts &&
+                       tiles_of(16) * ((a.n + block_cols - 1) / block_cols) >= 512;
+    // Otherwise 16 tokens a tile from 5 on (11008 x 4096: 3 tokens 9.8 us with tiles
+    // of 4, 13.4 with 16; 5 13.5 and 13.9; 8 14.5 and 13.5).
+    const bool wide = block || (a.mode != Q4_IDS && a.rows > 4ull * a.n_experts);
+    const uint32_t vt = wide ? 16 : 4;
+    const uint64_t tiles = a.mode == Q4_IDS ? a.rows : tiles_of(vt);
     Form f = NARROW;
     uint32_t cols = 16, waves = 4;
-    if (wide) {
+    if (block) {
         f = BLOCK;
+        cols = block_cols;
         waves = kBlockWaves;
-        cols = 16 * (a.gated ? kBlockTiles / 2 : kBlockTiles) * waves;
-        if (tiles * ((a.n + cols - 1) / cols) < 256) {
-            // Rows for 512 blocks: two tiles share the staged x (as gate and up do; with
-            // f32's three parts their registers do not fit).
-            f = tiles * ((a.n + 15) / 16) < 512 || a.gated || a.dtype == 0 ? SPLIT : SPLIT2;
-            cols = f == SPLIT ? 16 : 32;
-            waves = f == SPLIT && !a.gated ? 8 : 4;
-        }
+    } else if (wide) {
+        // Two tiles share the staged x from 1024 blocks on (gate and up do always; with
+        // f32's three parts their registers do not fit): 688 blocks 15.4 us, with two
+        // tiles 16.2; 1024 18.8 and 16.5; 2048 33.5 and 29.5.
+        f = tiles * ((a.n + 15) / 16) < 1024 || a.gated || a.dtype == 0 ? SPLIT : SPLIT2;
+        cols = f == SPLIT ? 16 : 32;
+        waves = f == SPLIT && !a.gated ? 8 : 4;
     }
     L->variant = (int)(vt + 256 * cols);
     const void* fn = a.dtype == 0 ? pick<TF32>(a, f) : a.dtype == 1 ? pick<TF16>(a, f) : pick<TBF16>(a, f);

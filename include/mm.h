@@ -20,7 +20,7 @@
  *   that returns an error other than MM_ERR_DEVICE has enqueued nothing.
  *   MM_ERR_DEVICE means the HIP runtime refused a launch after validation;
  *   a call that makes two launches (mm_id with the grouped route; mm_id_sort
- *   of more than 8192 rows) may then leave its first launch, the map pass or
+ *   of many rows) may then leave its first launch, the map pass or
  *   the sort's plan, enqueued (see mm_id, mm_id_sort).
  * - Asynchrony: on MM_OK the work is enqueued on `stream` (a hipStream_t; 0 =
  *   the null stream) and results are valid once the stream has reached that
@@ -456,7 +456,7 @@ typedef struct {
  *   position[r] = place of routed row r                  (u32 [m*top_k])
  *   xs[i][:]    = x[order[i] / top_k][:], or +0 for i >= offsets[n_experts]
  * Ids may repeat within a token. x is dtype [m, width], xs dtype
- * [m*top_k, width]. One launch up to 8192 routed rows, two beyond: if the HIP
+ * [m*top_k, width]. One launch while m*m*top_k <= 2^21, two beyond: if the HIP
  * runtime refuses the second, offsets, order and position are still written.
  */
 mm_status mm_id_sort(const mm_sort_params *params, mm_buf x, mm_buf ids, mm_buf xs,

@@ -542,8 +542,9 @@ def test_q4_id_sorted(dt, m, k_slots, counts, n, k, group, gated):
 
 
 @pytest.mark.parametrize("dt", DTYPES)
-@pytest.mark.parametrize("m,n,k,group,gated", [(16, 8201, 352, 32, 0), (9, 8201, 704, 64, 0), (11, 4100, 1152, 128, 1),
-                                               (61, 8201, 352, 32, 0), (64, 8200, 704, 64, 0), (50, 4105, 640, 128, 1)])
+@pytest.mark.parametrize("m,n,k,group,gated", [(61, 4100, 352, 32, 0), (50, 4201, 704, 64, 0), (11, 4100, 1152, 128, 1),
+                                               (61, 16290, 352, 32, 0), (64, 16300, 704, 64, 0), (50, 8150, 640, 128, 1),
+                                               (33, 8201, 1152, 128, 0)])
 def test_q4_gemv_of_many_rows(dt, m, n, k, group, gated):
     """Enough blocks for two staged tiles a wave, and for waves that split the rows."""
     case = q4_case(1, n * (1 + gated), k, group, 1, n + k)
@@ -551,10 +552,10 @@ def test_q4_gemv_of_many_rows(dt, m, n, k, group, gated):
     dev, xd, y = q4_dev(case), x.to(DEV), Padded(m, n, TORCH[dt])
     rec = mm.mm_q4_gemv(mm.q4_params(dt, 1, m, n, k, group, gated=gated), *(mm.buf(t) for t in dev), mm.buf(xd), y.buf,
                         stream=stream())
-    if -(-m // 16) * -(-n // (64 if gated else 128)) >= 256:
+    if -(-m // 16) * -(-n // (64 if gated else 128)) >= 512:
         cols = 64 if gated else 128
     else:
-        cols = 32 if dt != 0 and not gated else 16
+        cols = 32 if dt != 0 and not gated and -(-m // 16) * -(-n // 16) >= 1024 else 16
     assert rec.variant == 16 + 256 * cols
     want, err = ref.q4_product(case[0][0], case[1][0], case[2][0], group, x, bool(gated), dt == 0)
     q4_check(y.cpu(), dt, want, err, "y")
@@ -562,8 +563,8 @@ def test_q4_gemv_of_many_rows(dt, m, n, k, group, gated):
 
 
 @pytest.mark.parametrize("dt", DTYPES)
-@pytest.mark.parametrize("n,k,group,gated", [(520, 704, 64, 0), (333, 352, 32, 1), (301, 1152, 128, 0), (260, 256, 64, 1),
-                                             (600, 32, 32, 0)])
+@pytest.mark.parametrize("n,k,group,gated", [(800, 704, 64, 0), (333, 352, 32, 1), (801, 1152, 128, 0), (340, 256, 64, 1),
+                                             (900, 32, 32, 0)])
 def test_q4_id_sorted_of_many_rows(dt, n, k, group, gated):
     m, slots, E = 100, 8, 40
     R = m * slots
