@@ -269,6 +269,24 @@ def test_sort(dt, m, k, E, h):
     assert torch.equal(xs.cpu(), want)
 
 
+@pytest.mark.parametrize("m,k,E", [(8200, 8, 40), (9000, 8, 5), (70001, 1, 300)])
+def test_sort_plan_of_many_rows(m, k, E):
+    """Up to and past the rows whose matches the plan keeps in registers (65536)."""
+    ids = some_ids(m, k, E, E, repeat=True, dropped=0.05)
+    x = torch.randn(m, 3, generator=gen(m))
+    xs, off, order, pos = run_sort(0, x, ids, E)
+    key = np.minimum(ids.reshape(-1).astype(np.int64), E)
+    want = np.argsort(key, kind="stable")
+    np.testing.assert_array_equal(u32(order.cpu())[0], want)
+    np.testing.assert_array_equal(u32(off.cpu())[0], np.searchsorted(key[want], np.arange(E + 1)))
+    place = np.empty(m * k, dtype=np.int64)
+    place[want] = np.arange(m * k)
+    np.testing.assert_array_equal(u32(pos.cpu())[0], place)
+    rows = x[torch.from_numpy(want) // k]
+    rows[int(u32(off.cpu())[0][E]):] = 0
+    assert torch.equal(xs.cpu(), rows)
+
+
 def test_sort_carries_bits():
     """NaN, infinities, denormals and -0 arrive as they are."""
     bits = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).reshape(64, 1024)
