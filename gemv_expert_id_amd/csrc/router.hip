@@ -96,8 +96,22 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
                     }
 }
 
-// 16-bit logits, E <= 16 * EPL <= 512, top_k <= 16.
-template <class T, int EPL>
+// The order of a 16-bit logit as a number around 0x8000 (both zeros give
+// 0x8000), and back. kInf: the magnitude of infinity; above it lie the NaNs.
+template <class T>
+constexpr uint32_t kInf = T::code == 1 ? 0x7C00u : 0x7F80u;
+__device__ __forceinline__ uint32_t order16(uint32_t bits) {
+    const uint32_t mag = bits & 0x7FFFu;
+    return bits & 0x8000u ? 0x8000u - mag : 0x8000u + mag;
+}
+template <class T>
+__device__ __forceinline__ float value16(uint32_t order) {
+    return widen(T{}, (uint16_t)(order < 0x8000u ? 0x8000u | (0x8000u - order) : order - 0x8000u));
+}
+
+// 16-bit logits, E <= 16 * EPL <= 512, top_k <= KEEP or, where KEEP is EPL, 16. A
+// lane's list can lose no more than KEEP keys, so the others need not move up.
+template <class T, int EPL, int KEEP>
 __global__ __launch_bounds__(RThreads) void topk_rows(TopkArgs a) {
     constexpr int TPB = RThreads / 16;  // tokens of a block
     const int l = threadIdx.x & 15;
@@ -112,27 +126,22 @@ __global__ __launch_bounds__(RThreads) void topk_rows(TopkArgs a) {
         Pack raw;
         if (e0 + EPL <= E) {
             raw = *reinterpret_cast<const Pack*>(row + e0);
-        } else {
+        } else {  // -inf past the row's end: never chosen
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) raw.h[j] = e0 + j < E ? row[e0 + j] : (uint16_t)0;
+            for (int j = 0; j < EPL; ++j) raw.h[j] = e0 + j < E ? row[e0 + j] : (uint16_t)(0x8000u | kInf<T>);
         }
         bool nan = false;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const float v = widen(T{}, raw.h[j]);
-            // The upper half of the key is the logit's own order; -0 counts as +0.
-            uint32_t b = raw.h[j] == 0x8000u ? 0u : raw.h[j];
-            b = b & 0x8000u ? ~b & 0xFFFFu : b | 0x8000u;
-            key[j] = e0 + j < E && v > -INFINITY ? b << 16 | (0xFFFFu - (e0 + j)) : 0u;
-            nan |= e0 + j < E && v != v;
+            const uint32_t o = order16(raw.h[j]);
+            // What can be chosen lies above -inf and up to +inf.
+            key[j] = o - (0x8001u - kInf<T>) < 2 * kInf<T> ? o << 16 | (0xFFFFu - j - e0) : 0u;
+            nan |= (raw.h[j] & 0x7FFFu) > kInf<T>;
         }
         const uint64_t nans = __ballot(nan);
         const bool any_nan = (nans >> (threadIdx.x & 48) & 0xFFFFu) != 0;
         sort_keys<EPL>(key);
-        const auto value = [](uint32_t k) {
-            const uint32_t b = k >> 16;
-            return widen(T{}, (uint16_t)(b & 0x8000u ? b & 0x7FFFu : ~b));
-        };
+        const auto value = [](uint32_t k) { return value16<T>(k >> 16); };
         const uint32_t first = row_reduce(key[0], MaxU{});
         const float peak = value(first);
         float total = 0.f;
@@ -146,8 +155,8 @@ __global__ __launch_bounds__(RThreads) void topk_rows(TopkArgs a) {
             mine = l == s ? m : mine;
             const bool own = key[0] == m;
 #pragma unroll
-            for (int j = 0; j < EPL - 1; ++j) key[j] = own ? key[j + 1] : key[j];
-            key[EPL - 1] = own ? 0u : key[EPL - 1];
+            for (int j = 0; j < KEEP - 1; ++j) key[j] = own ? key[j + 1] : key[j];
+            key[KEEP - 1] = own ? 0u : key[KEEP - 1];
         }
         const float w = mine ? expf(value(mine) - peak) : 0.f;
         if (a.renormalize) total = w;
@@ -290,10 +299,10 @@ const void* pick(bool grad, uint32_t E) {
     return nullptr;
 }
 template <class T>
-const void* pick_rows(uint32_t E) {
+const void* pick_rows(uint32_t E, uint32_t top_k) {
     const int epl = (int)((E + 15) / 16);
 #define MM_EPL(n) \
-    if (epl <= n) return (const void*)&topk_rows<T, n>;
+    if (epl <= n) return top_k <= 8 ? (const void*)&topk_rows<T, n, (n < 8 ? n : 8)> : (const void*)&topk_rows<T, n, n>;
     MM_EPL(1) MM_EPL(2) MM_EPL(4) MM_EPL(8) MM_EPL(16) MM_EPL(32)
 #undef MM_EPL
     return nullptr;
@@ -305,7 +314,7 @@ hipError_t launch_topk(const TopkArgs& a, bool grad, hipStream_t s, Launched* L)
     L->kernel = grad ? MM_KERNEL_TOPK_GRAD : MM_KERNEL_TOPK;
     const bool rows = !grad && a.dtype != 0 && a.n_experts <= 512 && a.top_k <= 16;
     L->variant = rows ? 16 : kWave;
-    const void* fn = rows            ? (a.dtype == 1 ? pick_rows<TF16>(a.n_experts) : pick_rows<TBF16>(a.n_experts))
+    const void* fn = rows            ? (a.dtype == 1 ? pick_rows<TF16>(a.n_experts, a.top_k) : pick_rows<TBF16>(a.n_experts, a.top_k))
                      : a.dtype == 0   ? pick<TF32>(grad, a.n_experts)
                      : a.dtype == 1 ? pick<TF16>(grad, a.n_experts)
                                     : pick<TBF16>(grad, a.n_experts);
