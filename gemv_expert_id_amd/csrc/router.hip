@@ -11,7 +11,7 @@
 // expert's complement and every key is unique. Each lane sorts its own
 // keys with an odd-even merge network; a round takes the largest head of the
 // 16 lanes and the lane that owns it moves its list up. Bound by vector issue:
-// 16384 x 256 bf16, top 8, in 8.5 us (650 instructions for four tokens; one wave a
+// 16384 x 256 bf16, top 8, in 6.5 us (560 instructions for four tokens; one wave a
 // token 16.1 us; the logits alone would take 1.8 us).
 //
 // topk (the rest): one wave a token; a round takes the wave's largest key,

@@ -147,7 +147,7 @@ def test_position_and_offsets_go_together(name, lib):
     ("q4_gemv", "group", 0, UNSUPPORTED), ("q4_gemv", "k", 96 + 16, INVALID), ("q4_gemv", "k", 0, INVALID),
     ("q4_gemv", "n", 0, INVALID), ("q4_gemv", "gated", 2, INVALID), ("q4_gemv", "n_experts", 2, INVALID),
     ("q4_gemv", "top_k", 2, INVALID), ("q4_gemv", "input_layout", 1, INVALID), ("q4_gemv", "ldx", 63, INVALID),
-    ("q4_gemv", "ldy", 23, INVALID), ("q4_gemv", "n", (1 << 24) + 1, INVALID),
+    ("q4_gemv", "ldy", 23, INVALID), ("q4_gemv", "ldx", 1 << 25, INVALID), ("q4_gemv", "k", 1 << 25, INVALID), ("q4_gemv", "n", (1 << 24) + 1, INVALID),
     ("q4_direct", "input_layout", 2, INVALID), ("q4_sorted", "input_layout", 1, INVALID),
     ("q4_sorted", "n_experts", 1025, UNSUPPORTED), ("q4_direct", "m", 1 << 31, INVALID),
 ])
