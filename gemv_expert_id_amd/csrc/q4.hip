@@ -6,10 +6,13 @@
 // codes are the B operand of v_mfma_f32_16x16x32 (column = row of W), the
 // activations the A operand (row = token):
 //   - A code becomes an operand by placing its four bits in the mantissa of
-//     16.0, which is 16 + q, exact in f16 and bf16: one shift and one
-//     and-or for two codes, no conversion. The accumulator starts at -16 times
-//     the group's sum of x and so ends at q . x (the 16 taken back after the
-//     instructions instead, by a coefficient b - 16 s, had 1.5 times the error).
+//     1.0, which is 1 + q / 16, exact in f16 and bf16: one shift and one
+//     and-or for two codes, no conversion. The accumulator starts at minus the
+//     group's sum of x and so ends at q . x / 16 (the 1 taken back after the
+//     instructions instead, by a coefficient b - 16 s, had 1.5 times the error);
+//     outputs are multiplied by 16. On the way the accumulator stays within the
+//     group's sum of |x|, which is below 2^127 for every |x| < 2^120 and group
+//     (in the mantissa of 16.0 the same sums passed 2^128 from |x| = 2^116 on).
 //     The sum is taken where x is staged, or, for 16 tokens of 16 bits, by the
 //     same instruction with a constant operand (staging 31 -> 10 instructions
 //     an octet). Scales enter in f32 after a group's instructions, so no weight
@@ -58,17 +61,17 @@ struct __attribute__((packed, aligned(sizeof(S)))) QChunk {
 
 // Operand format of the codes and the activations.
 struct CoreF16 {
-    static constexpr uint32_t kSixteen = 0x4C004C00u;
-    static constexpr uint32_t kMinusSixteen = 0xCC00CC00u;
-    static constexpr int kShift = 6;  // the code's place in the mantissa of 16.0
+    static constexpr uint32_t kOne = 0x3C003C00u;
+    static constexpr uint32_t kMinusOne = 0xBC00BC00u;
+    static constexpr int kShift = 6;  // the code's place in the mantissa of 1.0
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
     }
 };
 struct CoreBF16 {
-    static constexpr uint32_t kSixteen = 0x41804180u;
-    static constexpr uint32_t kMinusSixteen = 0xC180C180u;
+    static constexpr uint32_t kOne = 0x3F803F80u;
+    static constexpr uint32_t kMinusOne = 0xBF80BF80u;
     static constexpr int kShift = 3;
     static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -78,17 +81,17 @@ struct CoreBF16 {
 template <class T> struct CoreOf { using type = CoreBF16; };
 template <> struct CoreOf<TF16> { using type = CoreF16; };
 
-// Eight codes (nibble i = element i) to 16 + q in the order 0 4 1 5 2 6 3 7.
-// The mask is a scalar, the 16.0s a vector register: as literals they would not
+// Eight codes (nibble i = element i) to 1 + q / 16 in the order 0 4 1 5 2 6 3 7.
+// The mask is a scalar, the 1.0s a vector register: as literals they would not
 // fit one and-or.
 template <class C>
-__device__ __forceinline__ u32x4 codes16(uint32_t w, uint32_t mask, uint32_t sixteen) {
+__device__ __forceinline__ u32x4 codes16(uint32_t w, uint32_t mask, uint32_t one) {
     u32x4 r;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int sh = 4 * p - C::kShift;
         const uint32_t t = sh >= 0 ? w >> (sh >= 0 ? sh : 0) : w << (sh < 0 ? -sh : 0);
-        r[p] = (t & mask) | sixteen;
+        r[p] = (t & mask) | one;
     }
     return r;
 }
@@ -266,7 +269,7 @@ struct Tiles {
     static constexpr int XR = PARTS == 3 ? 2 : 1;           // 16-byte loads of an octet
     struct Stage {
         u32x4 x[PARTS][ROWS][PITCH];
-        // -16 times each token's sum of a group; MI = 1: a token's groups together.
+        // Minus each token's sum of a group; MI = 1: a token's groups together.
         // f32: of the upper parts, and of the rest.
         __attribute__((aligned(16))) float sum[SUMS][MI == 1 ? VT : NV][MI == 1 ? NV : VT];
     };
@@ -279,8 +282,8 @@ struct Tiles {
     const uint8_t* codes[NT];      // first row of each tile, the same for the wave
     const uint16_t *sc[NT], *bi[NT];
     uint32_t coff[NT], goff[NT];   // this lane's row and chunk from there
-    f32x4 out[NT];                 // MI = 1: out[t][0] alone
-    uint32_t k, groups, mask, sixteen;
+    f32x4 out[NT];                 // sixteenths of the sums; MI = 1: out[t][0] alone
+    uint32_t k, groups, mask, one;
     int c, xrow;
 
     // j[t]: first row of tile t; rows past `end` repeat the last and are not stored.
@@ -307,8 +310,8 @@ struct Tiles {
         xrow = tok < (int)cnt ? tok : (int)cnt - 1;
         if (MASKED && (r16 & 3) != c) xrow = VT;
         mask = 0x000F000Fu << C::kShift;
-        sixteen = C::kSixteen;
-        asm volatile("" : "+s"(mask), "+v"(sixteen));
+        one = C::kOne;
+        asm volatile("" : "+s"(mask), "+v"(one));
     }
 
     // Scales first, codes by step: a step is computed as soon as its own have arrived.
@@ -382,7 +385,7 @@ struct Tiles {
 #pragma unroll
         for (int h = 0; h < SUMS; ++h) {
             const float sum = group_sum<GROUP>(f[h]);
-            if (o % (GROUP / 8) == 0) xs.sum[h][MI == 1 ? v : g][MI == 1 ? g : v] = -16.f * sum;
+            if (o % (GROUP / 8) == 0) xs.sum[h][MI == 1 ? v : g][MI == 1 ? g : v] = -sum;
         }
     }
 
@@ -419,7 +422,7 @@ struct Tiles {
 #pragma unroll
                     for (int p = 0; p < PARTS; ++p) av[p][j] = xs.x[p][xrow][i * (QStep / 8) + oct];
                 }
-                // -16 sum(x) of each group (MI = 1) or token: by parts, and whole.
+                // -sum(x) of each group (MI = 1) or token: by parts, and whole.
                 float sums[SUMS][4], sum[4];
                 if constexpr (STAGED_SUMS) {
 #pragma unroll
@@ -428,10 +431,10 @@ struct Tiles {
                         for (int v = 0; v < (MI == 1 ? GPS : 4); ++v)
                             sums[h][v] = MI == 1 ? xs.sum[h][c][i * GPS + v] : xs.sum[h][i * GPS + gp][4 * c + v];
                 } else {
-                    const u32x4 m16 = {C::kMinusSixteen, C::kMinusSixteen, C::kMinusSixteen, C::kMinusSixteen};
+                    const u32x4 m1 = {C::kMinusOne, C::kMinusOne, C::kMinusOne, C::kMinusOne};
                     f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) d = C::mma(av[0][j], m16, d);
+                    for (int j = 0; j < PER; ++j) d = C::mma(av[0][j], m1, d);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) sums[0][v] = d[v];
                 }
@@ -452,7 +455,7 @@ struct Tiles {
                     }
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
-                        const u32x4 bq = codes16<C>(cw[t][gp * PER + j], mask, sixteen);
+                        const u32x4 bq = codes16<C>(cw[t][gp * PER + j], mask, one);
                         acc[0] = C::mma(av[0][j], bq, acc[0]);
 #pragma unroll
                         for (int p = 1; p < PARTS; ++p) acc[SUMS - 1] = C::mma(av[p][j], bq, acc[SUMS - 1]);
@@ -469,7 +472,7 @@ struct Tiles {
                         const int gi = i * GPS + gp + h;
                         const float sv = widen(ST{}, (uint16_t)(q.s[t][gi / 2] >> (16 * (gi & 1))));
                         const float bv = widen(ST{}, (uint16_t)(q.b[t][gi / 2] >> (16 * (gi & 1))));
-                        const float b16 = bv * -0.0625f;  // of -16 sum(x)
+                        const float b16 = bv * -0.0625f;  // of -sum(x), in sixteenths
                         if constexpr (MI == 1) {
                             const float dv = GROUP == 64 ? d[2 * h] + d[2 * h + 1] : d[h];
                             out[t][0] = __builtin_fmaf(b16, sum[h], __builtin_fmaf(sv, dv, out[t][0]));
@@ -485,8 +488,9 @@ struct Tiles {
     }
 };
 
-// silu(g) u of the gated form.
-__device__ __forceinline__ float gate(float g, float u) { return g / (1.f + expf(-g)) * u; }
+// An output from its sum in sixteenths: W . x, or silu(G . x) (U . x).
+__device__ __forceinline__ float output(float y) { return 16.f * y; }
+__device__ __forceinline__ float output(float g, float u) { return 16.f * g / (1.f + expf(-16.f * g)) * (16.f * u); }
 
 // Waves on a SIMD that leave q4_split its registers: a spill would wait for every
 // load under way.
@@ -596,7 +600,7 @@ __global__ __launch_bounds__(W* kWave, split_waves(T::code == 0, GROUP, MI, GATE
 #pragma unroll
             for (int w = 1; w < W; ++w) sum[h] += join[w][h * TN + t][v][j];
         }
-        y[(int64_t)v * a.ldy + col] = narrow(T{}, GATED ? gate(sum[0], sum[1]) : sum[0]);
+        y[(int64_t)v * a.ldy + col] = narrow(T{}, GATED ? output(sum[0], sum[1]) : output(sum[0]));
     }
 }
 
@@ -671,7 +675,7 @@ __global__ __launch_bounds__(W* kWave, T::code == 0 || GROUP == 32 ? 3 : 4) void
         for (int v = 0; v < 4; ++v)
             if (4 * z.c + v < (int)cnt)
                 y[(int64_t)(4 * z.c + v) * a.ldy + col] =
-                    narrow(T{}, GATED ? gate(z.out[t][v], z.out[NT - TN + t][v]) : z.out[t][v]);
+                    narrow(T{}, GATED ? output(z.out[t][v], z.out[NT - TN + t][v]) : output(z.out[t][v]));
     }
 }
 

@@ -518,8 +518,9 @@ mm_status mm_id_combine_grad(const mm_sort_params *params, mm_buf dout, mm_buf y
  * rounded, f32 activations are used to their full 24 bits, and the result is
  * rounded once to the dtype. n_experts matrices lie one after the other in
  * each of the three buffers. Activations must be finite and below 2^120 in
- * magnitude: with others the row's results are unspecified (other rows are not
- * affected).
+ * magnitude, and the sum over a row's groups of |s * (q . x)| + |b * sum(x)|
+ * below 2^128: with others the row's results are unspecified (other rows are
+ * not affected).
  */
 typedef struct {
     mm_dtype dtype;          /* x and y: f32, f16 or bf16 */
