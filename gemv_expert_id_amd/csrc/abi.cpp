@@ -17,6 +17,7 @@
 
 #include "../../include/mm.h"
 #include "kernels.hpp"
+#include "sort_rule.hpp"
 
 static_assert(MM_ID_GROUPED_MAX_EXPERTS == (unsigned)mmk::MM_GROUPED_MAX_E, "expert limit");
 
@@ -958,7 +959,7 @@ mm_status mm_id_sort(const mm_sort_params* params, mm_buf x, mm_buf ids, mm_buf 
     if ((st = resolve("sort")) != MM_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     mmk::Launched L;
-    const int launches = mmk::sort_launches(a);
+    const int launches = mmk::sort_launches(a.m, a.top_k);
     if (launches == 2) {
         ++g_launches;
         if ((st = finish(mmk::launch_sort_plan(a, s, &L), s, "sort")) != MM_OK) return st;

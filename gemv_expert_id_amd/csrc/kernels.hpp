@@ -129,8 +129,7 @@ struct SortArgs {
     int32_t dtype;
 };
 hipError_t launch_sort_plan(const SortArgs& a, hipStream_t s, Launched* L);
-hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s, Launched* L);
-int sort_launches(const SortArgs& a);  // 1: launch_sort_rows alone; 2: the plan first
+hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s, Launched* L);  // the plan first, by sort_launches
 hipError_t launch_combine(const SortArgs& a, hipStream_t s, Launched* L);
 hipError_t launch_combine_grad(const SortArgs& a, hipStream_t s, Launched* L);
 

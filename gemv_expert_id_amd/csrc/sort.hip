@@ -18,6 +18,7 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "sort_rule.hpp"
 
 namespace mmk {
 
@@ -186,7 +187,7 @@ __device__ __forceinline__ u32x4 repack(const float* f) {
     return v;
 }
 
-constexpr int KU = 8;  // slots handled together
+constexpr int KU = kSortSlots;  // slots handled together
 
 // A storage type's bits as they are moved.
 template <class T>
@@ -219,8 +220,10 @@ __device__ __forceinline__ void put(void* base, int64_t row, uint32_t j, uint32_
 }
 
 // xs[position[t * top_k + s]] = x[t], zeros past the rows that have an expert.
-// A block takes a token and one piece of its row; the rows are moved as bits.
-// Bound by memory: 4096 x 8 bf16 rows of 2048 in 27 us, 5.6 TB/s.
+// A block takes a token, one piece of its row and up to kSlots of its slots; the
+// rows are moved as bits. Bound by memory: 4096 x 8 bf16 rows of 2048 in 27 us,
+// 5.6 TB/s.
+constexpr uint32_t kSlots = 64;
 template <class S>
 __global__ __launch_bounds__(CThreads) void sort_copy(SortArgs a) {
     constexpr int CH = 16 / sizeof(S);
@@ -229,15 +232,18 @@ __global__ __launch_bounds__(CThreads) void sort_copy(SortArgs a) {
     const uint32_t live = a.offsets[a.n_experts];
     for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
         const u32x4 v = get<S>(a.tokens, t * a.ld_tokens, j, a.width);
-        for (uint32_t s = 0; s < a.top_k; ++s) {
-            const uint32_t i = a.position[t * a.top_k + s];
-            put<S>(a.rows_w, (int64_t)i * a.ld_rows, j, a.width, i < live ? v : u32x4{0, 0, 0, 0});
+        for (uint32_t s0 = blockIdx.z * kSlots; s0 < a.top_k; s0 += gridDim.z * kSlots) {
+            const uint32_t s1 = s0 + kSlots < a.top_k ? s0 + kSlots : a.top_k;
+            for (uint32_t s = s0; s < s1; ++s) {
+                const uint32_t i = a.position[t * a.top_k + s];
+                put<S>(a.rows_w, (int64_t)i * a.ld_rows, j, a.width, i < live ? v : u32x4{0, 0, 0, 0});
+            }
         }
     }
 }
 
 // The whole sort in one launch, for few rows: block 0 counts the offsets, block
-// t + 1 the places of token t's slots. 4 x 8 rows of 2048 bf16: 4.8 us, one memory
+// t + 1 the places of token t's slots, KU at a time. 4 x 8 rows of 2048 bf16: 4.8 us, one memory
 // round trip and a count; 512 x 8 rows of 2048 f32: 9.7 us, 3.9 TB/s.
 template <class S>
 __global__ __launch_bounds__(SThreads) void sort_small(SortArgs a) {
@@ -437,13 +443,6 @@ dim3 row_grid(int64_t blocks, uint32_t width, int dtype, uint32_t threads) {
 
 }  // namespace
 
-// The sort in one launch: each of its m blocks reads all m * top_k ids, which
-// costs less than a second launch up to about this many reads (one launch
-// against two: 512 x 8 rows 7.9 and 8.9 us, 1024 x 2 6.9 and 6.9, 640 x 8 10.1 and
-// 8.6, 2048 x 2 14.9 and 8.1, in a graph, rows of 512 bf16).
-constexpr int64_t kSmallReads = 1 << 21;
-int sort_launches(const SortArgs& a) { return (int64_t)a.m * a.m <= kSmallReads / a.top_k ? 1 : 2; }
-
 hipError_t launch_sort_plan(const SortArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_SORT_PLAN;
     void* args[] = {const_cast<SortArgs*>(&a)};
@@ -452,14 +451,15 @@ hipError_t launch_sort_plan(const SortArgs& a, hipStream_t s, Launched* L) {
 
 hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_SORT_ROWS;
-    const bool small = sort_launches(a) == 1;
+    const bool small = sort_launches(a.m, a.top_k) == 1;
     L->variant = small ? 1 : 0;
     const uint32_t threads = small ? SThreads : CThreads;
     const void* fn = small ? (a.dtype == 0 ? (const void*)&sort_small<uint32_t> : (const void*)&sort_small<uint16_t>)
                            : (a.dtype == 0 ? (const void*)&sort_copy<uint32_t> : (const void*)&sort_copy<uint16_t>);
+    dim3 grid = row_grid(small ? (int64_t)a.m + 1 : (int64_t)a.m, a.width, a.dtype, threads);
+    if (!small) grid.z = a.top_k <= 4096 * kSlots ? (a.top_k + kSlots - 1) / kSlots : 4096;
     void* args[] = {const_cast<SortArgs*>(&a)};
-    return hipLaunchKernel(fn, row_grid(small ? (int64_t)a.m + 1 : (int64_t)a.m, a.width, a.dtype, threads),
-                           dim3(threads), args, 0, s);
+    return hipLaunchKernel(fn, grid, dim3(threads), args, 0, s);
 }
 
 namespace {

@@ -456,8 +456,9 @@ typedef struct {
  *   position[r] = place of routed row r                  (u32 [m*top_k])
  *   xs[i][:]    = x[order[i] / top_k][:], or +0 for i >= offsets[n_experts]
  * Ids may repeat within a token. x is dtype [m, width], xs dtype
- * [m*top_k, width]. One launch while m*m*top_k <= 2^21, two beyond: if the HIP
- * runtime refuses the second, offsets, order and position are still written.
+ * [m*top_k, width]. One launch while top_k <= 16 and m*m*top_k*ceil(top_k/8)
+ * <= 2^21, two beyond: if the HIP runtime refuses the second, offsets, order and
+ * position are still written.
  */
 mm_status mm_id_sort(const mm_sort_params *params, mm_buf x, mm_buf ids, mm_buf xs,
                      mm_buf offsets, mm_buf order, mm_buf position, void *stream,
