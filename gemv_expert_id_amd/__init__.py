@@ -50,6 +50,7 @@ EXPORTS = [
     "mm_id_combine_grad", "mm_q4_gemv", "mm_q4_id_direct", "mm_q4_id_sorted",
 ]
 MM_TOPK_MAX_EXPERTS, MM_TOPK_MAX_SLOTS = 1024, 64
+MM_SORT_MAX_SLOTS = 65536
 MM_ID_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 

@@ -621,6 +621,8 @@ mm_status sort_plan(const mm_sort_params* p, mmk::SortArgs* a, SortSizes* z) {
     if (p->n_experts > MM_TOPK_MAX_EXPERTS)
         return fail(MM_ERR_UNSUPPORTED, "sorted rows: at most %u experts (got %u)", MM_TOPK_MAX_EXPERTS,
                     p->n_experts);
+    if (p->top_k > MM_SORT_MAX_SLOTS)
+        return fail(MM_ERR_UNSUPPORTED, "sorted rows: at most %u slots (got %u)", MM_SORT_MAX_SLOTS, p->top_k);
     const uint64_t R = (uint64_t)p->m * p->top_k;
     if (R >= (1ull << 31) || p->width > (1u << 24))
         return fail(MM_ERR_INVALID_ARGUMENT, "sorted rows: m*top_k must be below 2^31 and width at most 2^24");

@@ -396,6 +396,11 @@ mm_status mm_id_prefill_noalloc(const mm_id_params *params, mm_dtype weight_dtyp
 #define MM_TOPK_MAX_EXPERTS 1024u
 #define MM_TOPK_MAX_SLOTS 64u
 
+/* Largest slots per token of the sorted-row calls. mm_id_combine and
+ * mm_id_sort_grad add a token's rows one after the other, at 0.2 to 0.5 us each:
+ * tens of milliseconds for one token of this many. */
+#define MM_SORT_MAX_SLOTS 65536u
+
 typedef struct {
     mm_dtype dtype;          /* logits (and dlogits): f32, f16 or bf16 */
     uint32_t m;              /* tokens */
@@ -438,7 +443,8 @@ mm_status mm_topk_grad(const mm_topk_params *params, mm_buf logits, mm_buf ids, 
 
 typedef struct {
     mm_dtype dtype;          /* token rows and expert rows: f32, f16 or bf16 */
-    uint32_t m, top_k;       /* tokens, slots per token; m*top_k < 2^31 */
+    uint32_t m, top_k;       /* tokens, slots per token (<= MM_SORT_MAX_SLOTS);
+                                m*top_k < 2^31 */
     uint32_t n_experts;      /* <= MM_TOPK_MAX_EXPERTS */
     uint32_t width;          /* elements of a row */
     uint32_t reserved;       /* 0 */
