@@ -247,12 +247,16 @@ __global__ __launch_bounds__(RThreads) void topk_grad(TopkArgs a) {
             g = a.dweights[t * a.top_k + lane];
         }
         float val[EPL];
+        bool nan = false;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const uint32_t e = lane + j * kWave;
             val[j] = e < E ? widen(T{}, row[e]) : -INFINITY;
+            nan |= val[j] != val[j];
             slot[e] = 0;
         }
+        // A NaN makes the token's weights NaN whether it was chosen or not.
+        const bool any_nan = __ballot(nan) != 0;
         wave_lds_fence();
         if (id < E) slot[id] = lane + 1;
         wave_lds_fence();
@@ -276,7 +280,7 @@ __global__ __launch_bounds__(RThreads) void topk_grad(TopkArgs a) {
             total += p[j];
             dot += ge[j] * p[j];
         }
-        const float inv = 1.f / wave_add(total);
+        const float inv = any_nan ? __uint_as_float(0x7FC00000u) : 1.f / wave_add(total);
         dot = wave_add(dot) * inv;
         S* out = static_cast<S*>(a.dlogits) + t * a.ld;
 #pragma unroll

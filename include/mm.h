@@ -434,7 +434,9 @@ mm_status mm_topk(const mm_topk_params *params, mm_buf logits, mm_buf ids, mm_bu
  * elsewhere):
  *   dlogits[t][e] = p[e] * (g[e] - sum_e' g[e'] * p[e'])
  * Slots whose id is outside the expert count are skipped, whatever their
- * gradient holds; a token without any gets a row of +0. dlogits is written
+ * gradient holds; a token without any gets a row of +0. In other tokens a NaN
+ * logit makes the gradients NaN as it does the weights: those of all experts
+ * that are not masked (renormalize = 0), or of the chosen (1). dlogits is written
  * whole. The ids of one token must be distinct, as mm_topk gives them. Buffers:
  * logits and dlogits dtype [m, n_experts], ids u32 and dweights f32 [m, top_k].
  */
