@@ -528,8 +528,9 @@ mm_status mm_id_combine_grad(const mm_sort_params *params, mm_buf dout, mm_buf y
  * rounded once to the dtype. n_experts matrices lie one after the other in
  * each of the three buffers. Activations must be finite and below 2^120 in
  * magnitude, and the sum over a row's groups of |s * (q . x)| + |b * sum(x)|
- * below 2^128: with others the row's results are unspecified (other rows are
- * not affected).
+ * below 2^128. A NaN or an infinity among a row's activations makes all its
+ * results NaN; with other values beyond those bounds they are unspecified. No
+ * other row is affected.
  */
 typedef struct {
     mm_dtype dtype;          /* x and y: f32, f16 or bf16 */

@@ -53,3 +53,25 @@ def test_q4_of_large_activations(dt, gated, form, group):
     assert float(want.abs().max()) < torch.finfo(TORCH[dt]).max
     got = run_q4(dt, 2, (codes, scales, biases), group, x, n, gated, form)
     q4_check(got, dt, want, err, "y")
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dt,gated,form", [(dt, gated, form) for dt in (0, 1, 2) for gated in (0, 1) for form in FORMS
+                                           if form != "split2" or (dt and not gated)])
+def test_q4_of_rows_that_are_not_finite(dt, gated, form, group, bad):
+    """One activation that is not finite makes its row's outputs NaN and no other's; its place in the row does not matter."""
+    m, n = FORMS[form][0], FORMS[form][1 + gated]
+    k = 9 * group
+    case = q4_case(1, n * (1 + gated), k, group, 1, group)
+    case[1][:, ::7] = 0.0  # also where a scale is 0
+    x = torch.randn(m, k, generator=gen(k)).to(TORCH[dt])
+    clean = run_q4(dt, 1, case, group, x, n, gated, form)
+    assert bool(torch.isfinite(clean).all())
+    for row, at in ((1, 0), (m - 1, k - 1), (0, k // 2 + 1)):
+        z = x.clone()
+        z[row, at] = float(bad)
+        got = run_q4(dt, 1, case, group, z, n, gated, form)
+        assert bool(torch.isnan(got[row]).all())
+        keep = [i for i in range(m) if i != row]
+        assert torch.equal(got[keep], clean[keep])
