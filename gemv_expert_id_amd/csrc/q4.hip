@@ -10,18 +10,19 @@
 //     and-or for two codes, no conversion. The accumulator starts at minus the
 //     group's sum of x and so ends at q . x / 16 (the 1 taken back after the
 //     instructions instead, by a coefficient b - 16 s, had 1.5 times the error);
-//     outputs are multiplied by 16. On the way the accumulator stays within the
-//     group's sum of |x|, which is below 2^127 for every |x| < 2^120 and group
-//     (in the mantissa of 16.0 the same sums passed 2^128 from |x| = 2^116 on).
+//     outputs are multiplied by 16. The accumulator stays below 2^128 on the way
+//     for every group and |x| < 2^120 (in the mantissa of 16.0 the same sums
+//     passed 2^128 from |x| = 2^116 on).
 //     The sum is taken where x is staged, or, for 16 tokens of 16 bits, by the
 //     same instruction with a constant operand (staging 31 -> 10 instructions
 //     an octet). Scales enter in f32 after a group's instructions, so no weight
 //     is ever rounded.
-//   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact). The upper
-//     parts have an accumulator and a sum of their own: their products and sums
-//     are short enough to be nearly exact in f32, and the lower parts' roundings
-//     are small (error against 64 bits 2e-7 of the result; with one accumulator
-//     and one sum 5e-7 to 1.5e-6).
+//   - f32 activations are three bf16 parts (8 + 8 + 8 bits, exact down to
+//     2^-133). The upper parts have an accumulator and a sum of their own: their
+//     products and sums are short enough to be nearly exact in f32, and the lower
+//     parts' roundings are small (error against 64 bits 4e-8 to 4e-7 of the result
+//     in norm, by k and group; 2e-7 where one accumulator and one sum had 5e-7 to
+//     1.5e-6).
 //   - A sum must not leave its group. The four lane groups of an instruction
 //     hold the step's four 32-element chunks. With up to 4 tokens (MI = 1) the A
 //     operand has 16 rows for 4 tokens: row 4v + g holds token v in lane group g
@@ -38,9 +39,9 @@
 // the current one.
 //
 // Measured (kernel alone): one token, 11008 x 4096 f16, groups of 128: 8.3 us, 2.9
-// TB/s; one token's eight gated experts of 1408 x 2048, bf16, groups of 32: 10.1 us,
-// 2.9 TB/s; both a launch, one or two memory round trips and 2 to 3 us of vector
-// issue. 512 f32 rows over 64 experts of 2048 x 1408, groups of 64: 46 us, 2.4 TB/s,
+// TB/s; one token's eight gated experts of 1408 x 2048, bf16, groups of 32: 10.3 us,
+// 2.8 TB/s; both a launch, one or two memory round trips and 2 to 3 us of vector
+// issue. 512 f32 rows over 64 experts of 2048 x 1408, groups of 64: 47 us, 2.4 TB/s,
 // bound by vector issue (19 us) and matrix instructions (8 us) between barriers. A
 // stream of the same bytes in this access pattern reaches 5.1 TB/s.
 #include <type_traits>

@@ -105,8 +105,9 @@ typedef enum {
     MM_KERNEL_GEMM_PANEL = 13,       /* NT, k in {32, 64, 128}: 64- or 128-row A panel in LDS, B tiles streamed */
     MM_KERNEL_TOPK = 14,             /* router */
     MM_KERNEL_TOPK_GRAD = 15,        /* router gradient */
-    MM_KERNEL_SORT_PLAN = 16,        /* offsets, order and position */
-    MM_KERNEL_SORT_ROWS = 17,      /* sorted rows (with the plan, when in one launch) */
+    MM_KERNEL_SORT_PLAN = 16,        /* offsets, order and position: the first of two launches of
+                                        mm_id_sort, whose receipt reports the second */
+    MM_KERNEL_SORT_ROWS = 17,        /* sorted rows (with the plan, when in one launch) */
     MM_KERNEL_COMBINE = 18,          /* weighted sum of expert rows (and mm_id_sort_grad) */
     MM_KERNEL_COMBINE_GRAD = 19,     /* its gradients */
     MM_KERNEL_Q4 = 20                /* 4-bit weights on MFMA */
@@ -524,8 +525,8 @@ mm_status mm_id_combine_grad(const mm_sort_params *params, mm_buf dout, mm_buf y
  * N = n, or 2n for the gated form, whose first n rows G and last n rows U give
  *   y[r][j] = silu(G[j] . x) * (U[j] . x),   silu(a) = a / (1 + exp(-a)).
  * Otherwise y[r][j] = W[j] . x. Sums are f32; nothing of the weights is
- * rounded, f32 activations are used to their full 24 bits, and the result is
- * rounded once to the dtype. n_experts matrices lie one after the other in
+ * rounded, f32 activations are used to their full 24 bits (but for bits below
+ * 2^-133, the smallest bf16 number), and the result is rounded once to the dtype. n_experts matrices lie one after the other in
  * each of the three buffers. Activations must be finite and below 2^120 in
  * magnitude, and the sum over a row's groups of |s * (q . x)| + |b * sum(x)|
  * below 2^128. A NaN or an infinity among a row's activations makes all its
