@@ -24,13 +24,16 @@ MM_ROUTE_GEMV, MM_ROUTE_GEMM, MM_ROUTE_ID_DIRECT = 0, 1, 2
 MM_ROUTE_ID_MAP, MM_ROUTE_ID_GROUPED, MM_ROUTE_ID_PREFILL = 3, 4, 5
 MM_ROUTE_GEMV_WIDE = 6
 MM_ROUTE_TOPK, MM_ROUTE_SORT, MM_ROUTE_COMBINE, MM_ROUTE_Q4 = 7, 8, 9, 10
+MM_ROUTE_GATED, MM_ROUTE_I8 = 11, 12
+MM_GATE_NONE, MM_GATE_SILU, MM_GATE_GELU = 0, 1, 2
 # mm_kernel: kernel family reported in receipts
 (MM_KERNEL_GEMV_ROWS, MM_KERNEL_GEMV_ROWS_ELEM, MM_KERNEL_GEMV_COLS, MM_KERNEL_GEMM_TILED,
  MM_KERNEL_GEMM_LARGE, MM_KERNEL_GEMM_F32, MM_KERNEL_ID_DIRECT_FAST, MM_KERNEL_ID_DIRECT,
  MM_KERNEL_ID_MAP, MM_KERNEL_ID_GROUPED_MFMA, MM_KERNEL_ID_GROUPED_FMA,
  MM_KERNEL_GEMV_WIDE, MM_KERNEL_GEMM_F32_SMALL, MM_KERNEL_GEMM_PANEL, MM_KERNEL_TOPK,
  MM_KERNEL_TOPK_GRAD, MM_KERNEL_SORT_PLAN, MM_KERNEL_SORT_ROWS, MM_KERNEL_COMBINE,
- MM_KERNEL_COMBINE_GRAD, MM_KERNEL_Q4) = range(21)
+ MM_KERNEL_COMBINE_GRAD, MM_KERNEL_Q4, MM_KERNEL_GATED, MM_KERNEL_GATED_GRAD,
+ MM_KERNEL_I8_QUANT, MM_KERNEL_I8) = range(25)
 MM_ID_SCHEMA_VERSION = 5
 MM_ID_GROUPED_MAX_EXPERTS = 1024
 
@@ -48,9 +51,11 @@ EXPORTS = [
     "mm_test_inject_resolve_failure", "mm_test_launch_count", "mm_id_prefill_noalloc",
     "mm_topk", "mm_topk_grad", "mm_id_sort", "mm_id_sort_grad", "mm_id_combine",
     "mm_id_combine_grad", "mm_q4_gemv", "mm_q4_id_direct", "mm_q4_id_sorted",
+    "mm_gated", "mm_gated_grad", "mm_i8_quant", "mm_i8_gemm",
 ]
 MM_TOPK_MAX_EXPERTS, MM_TOPK_MAX_SLOTS = 1024, 64
 MM_SORT_MAX_SLOTS = 65536
+MM_I8_MAX_K = 131056
 MM_ID_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -117,6 +122,24 @@ class Q4Params(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
+class GatedParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("gate", ctypes.c_uint32), ("m", ctypes.c_uint32),
+                ("n", ctypes.c_uint32), ("k", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldpre", ctypes.c_int64),
+                ("ldh", ctypes.c_int64)]
+
+
+class QuantParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("m", ctypes.c_uint32), ("k", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("ldx", ctypes.c_int64), ("ldq", ctypes.c_int64)]
+
+
+class I8Params(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("gate", ctypes.c_uint32), ("m", ctypes.c_uint32),
+                ("n", ctypes.c_uint32), ("k", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
 class DeviceCaps(ctypes.Structure):
     _fields_ = [("arch", ctypes.c_char * 64), ("cu_count", ctypes.c_int32),
                 ("max_clock_mhz", ctypes.c_int32), ("l2_bytes", ctypes.c_int32),
@@ -173,7 +196,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                  ("mm_id_combine", SortParams, 6),
                                  ("mm_id_combine_grad", SortParams, 7),
                                  ("mm_q4_gemv", Q4Params, 5), ("mm_q4_id_direct", Q4Params, 6),
-                                 ("mm_q4_id_sorted", Q4Params, 6)):
+                                 ("mm_q4_id_sorted", Q4Params, 6),
+                                 ("mm_gated", GatedParams, 4), ("mm_gated_grad", GatedParams, 7),
+                                 ("mm_i8_quant", QuantParams, 3), ("mm_i8_gemm", I8Params, 5)):
         fn = getattr(lib, name)
         fn.argtypes = [P(params)] + [Buf] * n_bufs + [vp, P(Receipt)]
         fn.restype = st
@@ -399,6 +424,53 @@ def mm_q4_id_sorted(params: Q4Params, codes: Buf, scales: Buf, biases: Buf, x: B
     """Rows sorted by expert (mm_id_sort) through 4-bit weights."""
     r = Receipt()
     _raise(load().mm_q4_id_sorted(params, codes, scales, biases, x, offsets, y, _stream(stream), r))
+    return r
+
+
+def gated_params(dtype: int, m: int, n: int, k: int, *, gate: int = MM_GATE_SILU, ldx: int = 0,
+                 ldw: int = 0, ldpre: int = 0, ldh: int = 0) -> GatedParams:
+    return GatedParams(dtype, gate, m, n, k, 0, ldx, ldw, ldpre, ldh)
+
+
+def quant_params(dtype: int, m: int, k: int, *, ldx: int = 0, ldq: int = 0) -> QuantParams:
+    return QuantParams(dtype, m, k, 0, ldx, ldq)
+
+
+def i8_params(dtype: int, m: int, n: int, k: int, *, gate: int = MM_GATE_NONE, ldx: int = 0,
+              ldw: int = 0, ldy: int = 0) -> I8Params:
+    return I8Params(dtype, gate, m, n, k, 0, ldx, ldw, ldy)
+
+
+def mm_gated(params: GatedParams, x: Buf, w: Buf, h: Buf, pre: Optional[Buf] = None,
+             stream=None) -> Receipt:
+    """h = act(x . gate^T) * (x . up^T); pre, if given, gets both projections."""
+    r = Receipt()
+    _raise(load().mm_gated(params, x, w, h, pre or Buf(None, 0), _stream(stream), r))
+    return r
+
+
+def mm_gated_grad(params: GatedParams, x: Buf, w: Buf, pre: Optional[Buf], dh: Buf, dpre: Buf,
+                  dx: Optional[Buf], dw: Optional[Buf], stream=None) -> Receipt:
+    """Gradients of mm_gated; without pre the projections are computed again."""
+    r = Receipt()
+    none = Buf(None, 0)
+    _raise(load().mm_gated_grad(params, x, w, pre or none, dh, dpre, dx or none, dw or none,
+                                _stream(stream), r))
+    return r
+
+
+def mm_i8_quant(params: QuantParams, x: Buf, q: Buf, scales: Buf, stream=None) -> Receipt:
+    """Rows to 8-bit codes with a scale for each row."""
+    r = Receipt()
+    _raise(load().mm_i8_quant(params, x, q, scales, _stream(stream), r))
+    return r
+
+
+def mm_i8_gemm(params: I8Params, x: Buf, x_scales: Buf, w: Buf, w_scales: Buf, y: Buf,
+               stream=None) -> Receipt:
+    """Product of 8-bit codes with scales for each token and channel, plain or gated."""
+    r = Receipt()
+    _raise(load().mm_i8_gemm(params, x, x_scales, w, w_scales, y, _stream(stream), r))
     return r
 
 

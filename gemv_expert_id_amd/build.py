@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmm.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["gemv.hip", "skinny.hip", "gemm.hip", "mmid.hip", "router.hip", "sort.hip", "q4.hip",
-           "abi.cpp"]
+           "gated.hip", "i8.hip", "abi.cpp"]
 ARCH = "gfx950"
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

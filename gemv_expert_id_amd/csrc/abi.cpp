@@ -717,6 +717,57 @@ mm_status run_q4(mmk::Q4Mode mode, const mm_q4_params* p, mm_buf codes, mm_buf s
                    [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_q4(a, s, L); });
 }
 
+// ---------------------------------------------------------------------------
+// Feed-forward block
+// ---------------------------------------------------------------------------
+// Extents of the gated calls, in bytes.
+struct GatedSizes {
+    uint64_t es, x, w, pre, h;
+};
+mm_status gated_plan(const mm_gated_params* p, mmk::FfnArgs* a, GatedSizes* z, int64_t* ldx, int64_t* ldw) {
+    if (!p) return fail(MM_ERR_INVALID_ARGUMENT, "gated: null params");
+    if (!valid_dtype(p->dtype))
+        return fail(MM_ERR_UNSUPPORTED, "gated: dtype %d is not f32, f16 or bf16", (int)p->dtype);
+    if (p->gate != MM_GATE_SILU && p->gate != MM_GATE_GELU)
+        return fail(MM_ERR_INVALID_ARGUMENT, "gated: gate %u is not SiLU or GELU", p->gate);
+    if (!p->m || !p->n || !p->k) return fail(MM_ERR_INVALID_ARGUMENT, "gated: m, n and k must be nonzero");
+    if (p->reserved) return fail(MM_ERR_INVALID_ARGUMENT, "gated: reserved must be 0");
+    if (p->m >= (1u << 31) || p->n > (1u << 24) || p->k > (1u << 24))
+        return fail(MM_ERR_INVALID_ARGUMENT, "gated: m must be below 2^31, n and k at most 2^24");
+    *a = mmk::FfnArgs{};
+    z->es = elt_size(p->dtype);
+    *ldx = p->ldx;
+    *ldw = p->ldw;
+    a->ldy = p->ldh;
+    a->ldpre = p->ldpre;
+    mm_status st;
+    if ((st = rows_extent("gated x", p->m, p->k, ldx, z->es, &z->x)) != MM_OK) return st;
+    if ((st = rows_extent("gated w", 2ull * p->n, p->k, ldw, z->es, &z->w)) != MM_OK) return st;
+    if ((st = rows_extent("gated pre", p->m, 2ull * p->n, &a->ldpre, z->es, &z->pre)) != MM_OK) return st;
+    if ((st = rows_extent("gated h", p->m, p->n, &a->ldy, z->es, &z->h)) != MM_OK) return st;
+    a->m = p->m;
+    a->n = p->n;
+    a->k = p->k;
+    a->ldx = *ldx * (int64_t)z->es;
+    a->ldw = *ldw * (int64_t)z->es;
+    a->dtype = (int)p->dtype;
+    a->gate = (int)p->gate;
+    return MM_OK;
+}
+
+// One product C = op(A) . op(B) of rows, on the route that mm_gemm takes.
+GemmPlan rows_product(int dt, int64_t m, int64_t n, int64_t k, bool ta, const void* a, int64_t lda,
+                      const void* b, int64_t ldb, void* c, int64_t ldc) {
+    return GemmPlan{dt, 1, m, n, k, lda, ldb, ldc, 0, 0, 0, ta, false,
+                    static_cast<const char*>(a), static_cast<const char*>(b), static_cast<char*>(c)};
+}
+hipError_t launch_product(const GemmPlan& p, hipStream_t s, mmk::Launched* L) {
+    if (p.m == 1 || p.n == 1) return mmk::launch_gemv(gemv_args(p), s, L);
+    mmk::GemmArgs g{p.a, p.b, p.c, p.m, p.n, p.k, p.lda, p.ldb, p.ldc, p.sa, p.sb, p.sc,
+                    p.batch, p.dt, p.ta, p.tb, p.alpha, p.beta};
+    return mmk::launch_gemm(g, s, L);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1064,6 +1115,156 @@ mm_status mm_q4_id_direct(const mm_q4_params* params, mm_buf codes, mm_buf scale
 mm_status mm_q4_id_sorted(const mm_q4_params* params, mm_buf codes, mm_buf scales, mm_buf biases,
                           mm_buf x, mm_buf offsets, mm_buf y, void* stream, mm_receipt* receipt) {
     return run_q4(mmk::Q4_SORTED, params, codes, scales, biases, x, offsets, y, stream, receipt);
+}
+
+mm_status mm_gated(const mm_gated_params* params, mm_buf x, mm_buf w, mm_buf h, mm_buf pre, void* stream,
+                   mm_receipt* receipt) {
+    mmk::FfnArgs a;
+    GatedSizes z;
+    int64_t ldx, ldw;
+    mm_status st = gated_plan(params, &a, &z, &ldx, &ldw);
+    if (st != MM_OK) return st;
+    Operand ops[] = {{"gated x", x, z.x, z.es, false},
+                     {"gated w", w, z.w, z.es, false},
+                     {"gated h", h, z.h, z.es, true},
+                     {pre.ptr ? "gated pre" : nullptr, pre, z.pre, z.es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.x = x.ptr;
+    a.w = w.ptr;
+    a.y = h.ptr;
+    a.pre_w = pre.ptr;
+    return run_one("gated", MM_ROUTE_GATED, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_gated(a, s, L); });
+}
+
+mm_status mm_gated_grad(const mm_gated_params* params, mm_buf x, mm_buf w, mm_buf pre, mm_buf dh, mm_buf dpre,
+                        mm_buf dx, mm_buf dw, void* stream, mm_receipt* receipt) {
+    mmk::FfnArgs a;
+    GatedSizes z;
+    int64_t ldx, ldw;
+    mm_status st = gated_plan(params, &a, &z, &ldx, &ldw);
+    if (st != MM_OK) return st;
+    // dpre may be pre itself: each element is read, then written, by one lane.
+    const bool in_place = pre.ptr != nullptr && pre.ptr == dpre.ptr;
+    Operand ops[] = {{"gated gradient x", x, z.x, z.es, false},
+                     {"gated gradient w", w, z.w, z.es, false},
+                     {pre.ptr && !in_place ? "gated gradient pre" : nullptr, pre, z.pre, z.es, false},
+                     {"gated gradient dh", dh, z.h, z.es, false},
+                     {"gated gradient dpre", dpre, z.pre, z.es, true},
+                     {dx.ptr ? "gated gradient dx" : nullptr, dx, z.x, z.es, true},
+                     {dw.ptr ? "gated gradient dw" : nullptr, dw, z.w, z.es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    if (in_place) {
+        Range same;
+        if ((st = check_buf("gated gradient pre", pre, 0, z.pre, z.es, &same)) != MM_OK) return st;
+    }
+    a.x = x.ptr;
+    a.w = w.ptr;
+    a.pre = pre.ptr;
+    a.dh = dh.ptr;
+    a.pre_w = dpre.ptr;
+    if ((st = resolve("gated_grad")) != MM_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    mmk::Launched L;
+    uint32_t launches = 0;
+    const auto enqueue = [&](hipError_t err) {
+        ++launches;
+        return finish(err, s, "gated_grad");
+    };
+    ++g_launches;
+    if ((st = enqueue(pre.ptr ? mmk::launch_gated_grad(a, s, &L) : mmk::launch_gated_again(a, s, &L))) != MM_OK)
+        return st;
+    const int64_t n2 = 2 * a.n;
+    if (dx.ptr) {  // dx [m, k] = dpre [m, 2n] . w [2n, k]
+        ++g_launches;
+        const GemmPlan p = rows_product(a.dtype, a.m, a.k, n2, false, dpre.ptr, a.ldpre, w.ptr, ldw, dx.ptr, ldx);
+        if ((st = enqueue(launch_product(p, s, &L))) != MM_OK) return st;
+    }
+    if (dw.ptr) {  // dw [2n, k] = dpre [m, 2n]^T . x [m, k]
+        ++g_launches;
+        const GemmPlan p = rows_product(a.dtype, n2, a.k, a.m, true, dpre.ptr, a.ldpre, x.ptr, ldx, dw.ptr, ldw);
+        if ((st = enqueue(launch_product(p, s, &L))) != MM_OK) return st;
+    }
+    set_receipt(receipt, MM_ROUTE_GATED, (uint32_t)a.dtype, launches, L);
+    return ok();
+}
+
+mm_status mm_i8_quant(const mm_quant_params* params, mm_buf x, mm_buf q, mm_buf scales, void* stream,
+                      mm_receipt* receipt) {
+    const mm_quant_params* p = params;
+    if (!p) return fail(MM_ERR_INVALID_ARGUMENT, "i8 codes: null params");
+    if (!valid_dtype(p->dtype))
+        return fail(MM_ERR_UNSUPPORTED, "i8 codes: dtype %d is not f32, f16 or bf16", (int)p->dtype);
+    if (!p->m || !p->k) return fail(MM_ERR_INVALID_ARGUMENT, "i8 codes: m and k must be nonzero");
+    if (p->reserved) return fail(MM_ERR_INVALID_ARGUMENT, "i8 codes: reserved must be 0");
+    if (p->m >= (1u << 31) || p->k > (1u << 24))
+        return fail(MM_ERR_INVALID_ARGUMENT, "i8 codes: m must be below 2^31 and k at most 2^24");
+    mmk::QuantArgs a{};
+    a.ldx = p->ldx;
+    a.ldq = p->ldq;
+    const uint64_t es = elt_size(p->dtype);
+    uint64_t xbytes, qbytes;
+    mm_status st;
+    if ((st = rows_extent("i8 codes: x", p->m, p->k, &a.ldx, es, &xbytes)) != MM_OK) return st;
+    if ((st = rows_extent("i8 codes: q", p->m, p->k, &a.ldq, 1, &qbytes)) != MM_OK) return st;
+    Operand ops[] = {{"i8 codes: x", x, xbytes, es, false},
+                     {"i8 codes: q", q, qbytes, 1, true},
+                     {"i8 codes: scales", scales, (uint64_t)p->m * 4, 4, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.x = x.ptr;
+    a.q = static_cast<int8_t*>(q.ptr);
+    a.scales = static_cast<float*>(scales.ptr);
+    a.m = p->m;
+    a.k = p->k;
+    a.dtype = (int)p->dtype;
+    return run_one("i8_quant", MM_ROUTE_I8, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_i8_quant(a, s, L); });
+}
+
+mm_status mm_i8_gemm(const mm_i8_params* params, mm_buf x, mm_buf x_scales, mm_buf w, mm_buf w_scales, mm_buf y,
+                     void* stream, mm_receipt* receipt) {
+    const mm_i8_params* p = params;
+    if (!p) return fail(MM_ERR_INVALID_ARGUMENT, "i8: null params");
+    if (!valid_dtype(p->dtype))
+        return fail(MM_ERR_UNSUPPORTED, "i8: dtype %d is not f32, f16 or bf16", (int)p->dtype);
+    if (p->gate > MM_GATE_GELU) return fail(MM_ERR_INVALID_ARGUMENT, "i8: unknown gate %u", p->gate);
+    if (!p->m || !p->n || !p->k) return fail(MM_ERR_INVALID_ARGUMENT, "i8: m, n and k must be nonzero");
+    if (p->reserved) return fail(MM_ERR_INVALID_ARGUMENT, "i8: reserved must be 0");
+    if (p->m >= (1u << 31) || p->n > (1u << 24))
+        return fail(MM_ERR_INVALID_ARGUMENT, "i8: m must be below 2^31 and n at most 2^24");
+    if (p->k % 16 || p->k > MM_I8_MAX_K)
+        return fail(MM_ERR_INVALID_ARGUMENT, "i8: k %u is not a multiple of 16 up to %u", p->k, MM_I8_MAX_K);
+    const uint64_t N = (uint64_t)p->n * (p->gate ? 2 : 1), es = elt_size(p->dtype);
+    mmk::FfnArgs a{};
+    a.ldx = p->ldx;
+    a.ldw = p->ldw;
+    a.ldy = p->ldy;
+    uint64_t xbytes, wbytes, ybytes;
+    mm_status st;
+    if ((st = rows_extent("i8 x", p->m, p->k, &a.ldx, 1, &xbytes)) != MM_OK) return st;
+    if ((st = rows_extent("i8 w", N, p->k, &a.ldw, 1, &wbytes)) != MM_OK) return st;
+    if ((st = rows_extent("i8 y", p->m, p->n, &a.ldy, es, &ybytes)) != MM_OK) return st;
+    if (a.ldx % 16 || a.ldw % 16 || a.ldx >= (1 << 24) || a.ldw >= (1 << 24))
+        return fail(MM_ERR_INVALID_ARGUMENT, "i8: pitches of codes (%lld, %lld) must be multiples of 16 below 2^24",
+                    (long long)a.ldx, (long long)a.ldw);
+    Operand ops[] = {{"i8 x", x, xbytes, 16, false},
+                     {"i8 x scales", x_scales, (uint64_t)p->m * 4, 4, false},
+                     {"i8 w", w, wbytes, 16, false},
+                     {"i8 w scales", w_scales, N * 4, 4, false},
+                     {"i8 y", y, ybytes, es, true}};
+    if ((st = check_operands(ops)) != MM_OK) return st;
+    a.x = x.ptr;
+    a.w = w.ptr;
+    a.y = y.ptr;
+    a.sx = static_cast<const float*>(x_scales.ptr);
+    a.sw = static_cast<const float*>(w_scales.ptr);
+    a.m = p->m;
+    a.n = p->n;
+    a.k = p->k;
+    a.dtype = (int)p->dtype;
+    a.gate = (int)p->gate;
+    return run_one("i8", MM_ROUTE_I8, a.dtype, stream, receipt,
+                   [&](hipStream_t s, mmk::Launched* L) { return mmk::launch_i8(a, s, L); });
 }
 
 mm_status mm_capabilities(int device, mm_device_caps* out) {

@@ -1,0 +1,95 @@
+// Gated feed-forward block: h = act(x G^T) * (x U^T), and the gradients of its
+// pre-activations (mm.h, "Feed-forward block").
+#include "ffn_tile.hpp"
+
+namespace mmk {
+
+namespace {
+
+// dpre from saved pre-activations, element by element: 16 bytes of the gate's
+// half, of the up projection's and of dh in, 16 bytes of each half out. Bound by
+// memory. A block takes 2^sh chunks of a row by 256 / 2^sh rows. In place (pre ==
+// dpre) every element is read before the same lane writes it.
+template <class T>
+__global__ __launch_bounds__(256) void gated_grad(FfnArgs a, int sh) {
+    using S = typename T::store_t;
+    constexpr int V = T::Elems16;
+    using U16 = Unaligned16<S>;
+    const int64_t c = (int64_t)blockIdx.x * (1 << sh) + (threadIdx.x & ((1 << sh) - 1));
+    const int64_t col = c * V;
+    if (col >= a.n) return;
+    const int valid = (int)(a.n - col < V ? a.n - col : V);
+    const int64_t rows = 256 >> sh;
+    for (int64_t r = blockIdx.y * rows + (threadIdx.x >> sh); r < a.m; r += gridDim.y * rows) {
+        const S* g = static_cast<const S*>(a.pre) + r * a.ldpre + col;
+        const S* u = g + a.n;
+        const S* d = static_cast<const S*>(a.dh) + r * a.ldy + col;
+        S* dg = static_cast<S*>(a.pre_w) + r * a.ldpre + col;
+        S* du = dg + a.n;
+        S gs[V], us[V], ds[V];
+        if (valid == V) {
+            *reinterpret_cast<U16*>(gs) = *reinterpret_cast<const U16*>(g);
+            *reinterpret_cast<U16*>(us) = *reinterpret_cast<const U16*>(u);
+            *reinterpret_cast<U16*>(ds) = *reinterpret_cast<const U16*>(d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                gs[i] = i < valid ? g[i] : S(0);
+                us[i] = i < valid ? u[i] : S(0);
+                ds[i] = i < valid ? d[i] : S(0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float x, y;
+            gate_grad(a.gate, widen(T{}, gs[i]), widen(T{}, us[i]), widen(T{}, ds[i]), &x, &y);
+            gs[i] = narrow(T{}, x);
+            us[i] = narrow(T{}, y);
+        }
+        if (valid == V) {
+            *reinterpret_cast<U16*>(dg) = *reinterpret_cast<const U16*>(gs);
+            *reinterpret_cast<U16*>(du) = *reinterpret_cast<const U16*>(us);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < valid) {
+                    dg[i] = gs[i];
+                    du[i] = us[i];
+                }
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L) {
+    L->kernel = MM_KERNEL_GATED;
+    return a.dtype == 0   ? run_ffn_tile<GatedOut<TF32>>(a, s)
+           : a.dtype == 1 ? run_ffn_tile<GatedOut<TF16>>(a, s)
+                          : run_ffn_tile<GatedOut<TBF16>>(a, s);
+}
+
+hipError_t launch_gated_again(const FfnArgs& a, hipStream_t s, Launched* L) {
+    L->kernel = MM_KERNEL_GATED_GRAD;
+    return a.dtype == 0   ? run_ffn_tile<GradOut<TF32>>(a, s)
+           : a.dtype == 1 ? run_ffn_tile<GradOut<TF16>>(a, s)
+                          : run_ffn_tile<GradOut<TBF16>>(a, s);
+}
+
+hipError_t launch_gated_grad(const FfnArgs& a, hipStream_t s, Launched* L) {
+    const int v = a.dtype == 0 ? 4 : 8;
+    const int64_t chunks = (a.n + v - 1) / v;
+    int sh = 0;
+    while (sh < 8 && (1 << sh) < chunks) ++sh;
+    const int64_t rows = 256 >> sh, gx = (chunks + (1 << sh) - 1) >> sh;
+    const int64_t gy = (a.m + rows - 1) / rows;
+    const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
+    const void* fn = a.dtype == 0   ? (const void*)&gated_grad<TF32>
+                     : a.dtype == 1 ? (const void*)&gated_grad<TF16>
+                                    : (const void*)&gated_grad<TBF16>;
+    void* args[] = {const_cast<FfnArgs*>(&a), &sh};
+    L->kernel = MM_KERNEL_GATED_GRAD;
+    return hipLaunchKernel(fn, grid, dim3(256), args, 0, s);
+}
+
+}  // namespace mmk

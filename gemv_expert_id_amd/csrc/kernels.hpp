@@ -152,6 +152,37 @@ struct Q4Args {
 };
 hipError_t launch_q4(const Q4Args& a, hipStream_t s, Launched* L);
 
+// Feed-forward products: sums of x [m, k] with the rows of w, [n, k] or, gated,
+// [2n, k], and what becomes of them. Each launcher reads the fields it needs.
+struct FfnArgs {
+    const void* x;
+    const void* w;
+    void* y;               // h, or the 8-bit product's output
+    const void* dh;        // gradient: [m, n], pitch ldy
+    const void* pre;       // gradient: [m, 2n]
+    void* pre_w;           // forward: pre-activations or null; gradient: theirs
+    const float* sx;       // codes: scale of each token
+    const float* sw;       // codes: scale of each row of w
+    int64_t m, n, k;
+    int64_t ldx, ldw;      // bytes
+    int64_t ldy, ldpre;    // elements
+    int32_t dtype, gate;
+};
+hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L);        // y and pre_w
+hipError_t launch_gated_again(const FfnArgs& a, hipStream_t s, Launched* L);  // pre_w from x, w, dh
+hipError_t launch_gated_grad(const FfnArgs& a, hipStream_t s, Launched* L);   // pre_w from pre, dh
+hipError_t launch_i8(const FfnArgs& a, hipStream_t s, Launched* L);
+
+// Rows of x to 8-bit codes and a scale each.
+struct QuantArgs {
+    const void* x;
+    int8_t* q;
+    float* scales;
+    int64_t m, k, ldx, ldq;
+    int32_t dtype;
+};
+hipError_t launch_i8_quant(const QuantArgs& a, hipStream_t s, Launched* L);
+
 // Library-held scratch for the allocation-free prefill call: its size, and
 // its device address on the GPU of stream `s` (looked up once per GPU).
 constexpr uint64_t kStaticScratchBytes = MM_ID_NOALLOC_SCRATCH_BYTES;

@@ -20,8 +20,8 @@
  *   that returns an error other than MM_ERR_DEVICE has enqueued nothing.
  *   MM_ERR_DEVICE means the HIP runtime refused a launch after validation;
  *   a call that makes two launches (mm_id with the grouped route; mm_id_sort
- *   of many rows) may then leave its first launch, the map pass or
- *   the sort's plan, enqueued (see mm_id, mm_id_sort).
+ *   of many rows; mm_gated_grad) may then leave its first launch, the map pass or
+ *   the sort's plan, enqueued (see mm_id, mm_id_sort, mm_gated_grad).
  * - Asynchrony: on MM_OK the work is enqueued on `stream` (a hipStream_t; 0 =
  *   the null stream) and results are valid once the stream has reached that
  *   point. Stream order is the only ordering: a map launch followed by a
@@ -83,7 +83,9 @@ typedef enum {
     MM_ROUTE_TOPK = 7,       /* router, and its gradient */
     MM_ROUTE_SORT = 8,       /* rows in expert order, and the gradient */
     MM_ROUTE_COMBINE = 9,    /* expert rows back to tokens, and the gradient */
-    MM_ROUTE_Q4 = 10         /* products with 4-bit weights */
+    MM_ROUTE_Q4 = 10,        /* products with 4-bit weights */
+    MM_ROUTE_GATED = 11,     /* gated feed-forward block, and its gradients */
+    MM_ROUTE_I8 = 12         /* 8-bit codes, and their products */
 } mm_route;
 
 /* Kernel family of a launch (reported in receipts; the choice depends on
@@ -110,7 +112,12 @@ typedef enum {
     MM_KERNEL_SORT_ROWS = 17,        /* sorted rows (with the plan, when in one launch) */
     MM_KERNEL_COMBINE = 18,          /* weighted sum of expert rows (and mm_id_sort_grad) */
     MM_KERNEL_COMBINE_GRAD = 19,     /* its gradients */
-    MM_KERNEL_Q4 = 20                /* 4-bit weights on MFMA */
+    MM_KERNEL_Q4 = 20,               /* 4-bit weights on MFMA */
+    MM_KERNEL_GATED = 21,            /* both projections and the gate */
+    MM_KERNEL_GATED_GRAD = 22,       /* gradients of the pre-activations; a call that also makes
+                                        products reports the kernel of the last one */
+    MM_KERNEL_I8_QUANT = 23,         /* rows to 8-bit codes */
+    MM_KERNEL_I8 = 24                /* products of 8-bit codes */
 } mm_kernel;
 
 typedef struct {
@@ -566,6 +573,103 @@ mm_status mm_q4_id_sorted(const mm_q4_params *params, mm_buf codes, mm_buf scale
                           mm_buf x, mm_buf offsets, mm_buf y, void *stream, mm_receipt *receipt);
 
 /* ------------------------------------------------------------------------ */
+/* Feed-forward block                                                        */
+/* ------------------------------------------------------------------------ */
+/*
+ * The dense layer that the products above serve: both projections, the gate and
+ * their product in one call, its gradients, and the same product over 8-bit
+ * codes. Conventions as for the mixture-of-experts operators: every dimension
+ * >= 1, pitches (ld*) in elements with 0 = tight, buffers aligned to their
+ * element unless stated, outputs overlapping no input and no other output unless
+ * stated, no scratch of the library's own, no global atomics, every call
+ * capturable into a graph.
+ *
+ * A gated matrix has 2n rows: n of the gate projection, then n of the up
+ * projection, as in mm_q4_*. With G and U a token's sums over them,
+ *   h = act(G) * U,   act(a) = a * sigmoid(z(a)),
+ *   z(a) = a                                    MM_GATE_SILU
+ *   z(a) = 2 sqrt(2/pi) (a + 0.044715 a^3)      MM_GATE_GELU (tanh form)
+ */
+typedef enum { MM_GATE_NONE = 0, MM_GATE_SILU = 1, MM_GATE_GELU = 2 } mm_gate;
+
+typedef struct {
+    mm_dtype dtype;          /* every tensor: f32, f16 or bf16 */
+    uint32_t gate;           /* MM_GATE_SILU or MM_GATE_GELU */
+    uint32_t m, n, k;        /* tokens (below 2^31), outputs and inputs (at most 2^24) */
+    uint32_t reserved;       /* 0 */
+    int64_t ldx;             /* x and dx [m, k] */
+    int64_t ldw;             /* w and dw [2n, k] */
+    int64_t ldpre;           /* pre and dpre [m, 2n] */
+    int64_t ldh;             /* h and dh [m, n] */
+} mm_gated_params;
+
+/*
+ * Forward: [G U] = x . w^T in f32, h = act(G) * U from the f32 sums, rounded
+ * once. pre is optional ({NULL, 0}): [G U] rounded to the dtype, for the
+ * backward pass.
+ */
+mm_status mm_gated(const mm_gated_params *params, mm_buf x, mm_buf w, mm_buf h, mm_buf pre,
+                   void *stream, mm_receipt *receipt);
+
+/*
+ * Gradients, with dh the gradient of h:
+ *   dpre = [dh * U * act'(G), dh * act(G)]   in f32, rounded once
+ *   dx   = dpre . w        (of the rounded dpre, in f32, rounded once)
+ *   dw   = dpre^T . x
+ * G and U come from pre as mm_gated left it or, without pre ({NULL, 0}), from x
+ * and w again, unrounded. dpre is always written, and is the operand of both
+ * products; it may be the same buffer as pre. dx and dw are optional. One launch
+ * for dpre and one for each product; if the HIP runtime refuses a later one, what
+ * was enqueued before it is still written.
+ */
+mm_status mm_gated_grad(const mm_gated_params *params, mm_buf x, mm_buf w, mm_buf pre, mm_buf dh,
+                        mm_buf dpre, mm_buf dx, mm_buf dw, void *stream, mm_receipt *receipt);
+
+typedef struct {
+    mm_dtype dtype;          /* x: f32, f16 or bf16 */
+    uint32_t m, k;           /* rows (below 2^31), elements of a row (at most 2^24) */
+    uint32_t reserved;       /* 0 */
+    int64_t ldx, ldq;        /* row pitches of x and of the codes */
+} mm_quant_params;
+
+/*
+ * Rows to 8-bit codes, for activations (a scale for each token) as for weights
+ * (a scale for each channel):
+ *   scales[i] = max(max_p |x[i][p]| / 127, 2^-126)           (f32)
+ *   q[i][p]   = x[i][p] / scales[i] to the nearest whole number, ties to even (int8)
+ * exactly: -127 <= q <= 127, and the error is at most half a scale. A row that
+ * holds a NaN has a NaN scale, one that holds an infinity and no NaN an infinite
+ * one, and codes 0, so that every product of it is NaN. Bytes between rows are
+ * left as they were.
+ */
+mm_status mm_i8_quant(const mm_quant_params *params, mm_buf x, mm_buf q, mm_buf scales,
+                      void *stream, mm_receipt *receipt);
+
+/* Largest contraction of mm_i8_gemm: sums of products of codes fit 32 bits. */
+#define MM_I8_MAX_K 131056u
+
+typedef struct {
+    mm_dtype dtype;          /* y: f32, f16 or bf16 */
+    uint32_t gate;           /* MM_GATE_NONE, or the gated form */
+    uint32_t m, n, k;        /* tokens (below 2^31), outputs (at most 2^24), inputs
+                                (a multiple of 16, at most MM_I8_MAX_K) */
+    uint32_t reserved;       /* 0 */
+    int64_t ldx, ldw;        /* pitches of the codes: multiples of 16, below 2^24 */
+    int64_t ldy;
+} mm_i8_params;
+
+/*
+ * Product of 8-bit codes with scales for each token and each channel (row of w):
+ *   y[i][j] = sum_p x[i][p] * w[j][p] * w_scales[j] * x_scales[i]
+ * or act(G) * U of two such sums, gated. The sum is exact, in 32-bit integers (any
+ * codes, -128 too); its product with the channel's scale, then the token's, is
+ * f32, and y is rounded once. x int8 [m, k], x_scales f32 [m], w int8 [n, k] or,
+ * gated, [2n, k], w_scales f32 of as many; codes 16-byte aligned.
+ */
+mm_status mm_i8_gemm(const mm_i8_params *params, mm_buf x, mm_buf x_scales, mm_buf w,
+                     mm_buf w_scales, mm_buf y, void *stream, mm_receipt *receipt);
+
+/* ------------------------------------------------------------------------ */
 /* Device and library information                                            */
 /* ------------------------------------------------------------------------ */
 
@@ -606,7 +710,8 @@ const char *mm_last_error(void);
 
 /* Make the next launch-resolution step on this thread fail for the kernel
  * family `name` ("gemv", "gemv_wide", "gemm", "id_direct", "id_map",
- * "id_grouped", "topk", "topk_grad", "sort", "combine", "combine_grad", "q4"),
+ * "id_grouped", "topk", "topk_grad", "sort", "combine", "combine_grad", "q4",
+ * "gated", "gated_grad", "i8_quant", "i8"),
  * before anything is enqueued, like the pipeline-lookup failure injected in
  * mlx-native's `grouped_pipeline_resolution_failure_does_not_mutate_encoder`.
  * NULL clears it. */

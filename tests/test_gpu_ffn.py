@@ -1,0 +1,321 @@
+"""GPU tests of the feed-forward block's operators against the 64-bit definitions
+in ffn_ref.py, with the error bounds derived there plus half a step of the output's
+type. Whole numbers have to be equal. Memory around every operand holds NaN (or a
+code that would show), memory around every output a sentinel that must survive."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import ffn_ref as ref
+import gemv_expert_id_amd as mm
+from ffn_ref import TORCH, rounding
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+DTYPES = [0, 1, 2]
+GATES = [ref.SILU, ref.GELU]
+
+
+def stream():
+    return torch.cuda.current_stream()
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def randn(seed, *shape, scale=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=gen(seed), device=DEV) * scale).to(dtype)
+
+
+class Rows:
+    """[rows, width] on the GPU with a pitch, `shift` elements into memory filled with `fill`."""
+
+    def __init__(self, rows, width, dtype, ld=0, shift=0, value=None, fill=None):
+        self.rows, self.width, self.ld, self.shift = rows, width, ld or width, shift
+        self.fill = fill if fill is not None else (float("nan") if dtype.is_floating_point else 99)
+        self.store = torch.full((shift + rows * self.ld + 16,), self.fill, dtype=dtype, device=DEV)
+        self.t = self.store[shift:].as_strided((rows, width), (self.ld, 1))
+        if value is not None:
+            self.t.copy_(value)
+
+    @property
+    def buf(self):
+        z = self.store.element_size()
+        return mm.Buf(self.store.data_ptr() + self.shift * z, ((self.rows - 1) * self.ld + self.width) * z)
+
+    def untouched(self):
+        """Everything outside the tensor still holds the fill."""
+        probe = self.store.clone()
+        probe[self.shift:].as_strided((self.rows, self.width), (self.ld, 1)).fill_(self.fill)
+        same = probe.isnan() if self.fill != self.fill else probe == self.fill
+        assert bool(same.all()), "written outside the output"
+
+
+def near(got, want, bound, what):
+    assert got.shape == want.shape
+    err = (got.double() - want).abs()
+    bad = ~(err <= bound)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((err / bound)[bad].max()):.3g} of its bound"
+
+
+# ---- the gated block -------------------------------------------------------------
+
+
+def gated_operands(dt, m, n, k, pad, shift):
+    t = TORCH[dt]
+    x = Rows(m, k, t, k + pad, shift, randn(m + n, m, k))
+    w = Rows(2 * n, k, t, k + pad, shift, randn(n + k, 2 * n, k, scale=1.5 / k ** 0.5))
+    return x, w
+
+
+def check_gated(dt, m, n, k, gate=ref.SILU, saved=True, pad=0, shift=0):
+    t = TORCH[dt]
+    x, w = gated_operands(dt, m, n, k, pad, shift)
+    h = Rows(m, n, t, n + pad, shift)
+    pre = Rows(m, 2 * n, t, 2 * n + pad, shift) if saved else None
+    p = mm.gated_params(dt, m, n, k, gate=gate, ldx=x.ld, ldw=w.ld, ldpre=pre.ld if saved else 0, ldh=h.ld)
+    rec = mm.mm_gated(p, x.buf, w.buf, h.buf, pre.buf if saved else None, stream=stream())
+    assert rec.kernel == mm.MM_KERNEL_GATED and rec.route == mm.MM_ROUTE_GATED and rec.dispatch_count == 1
+    want, wpre, e, epre = ref.gated(x.t, w.t, gate)
+    near(h.t, want, e + rounding(dt, want.abs() + e), "h")
+    h.untouched()
+    if saved:
+        near(pre.t, wpre, epre + rounding(dt, wpre.abs() + epre), "pre")
+        pre.untouched()
+    return rec
+
+
+def check_grad(dt, m, n, k, gate=ref.SILU, saved=True, pad=0, shift=0, want=("dx", "dw"), in_place=False):
+    t = TORCH[dt]
+    x, w = gated_operands(dt, m, n, k, pad, shift)
+    dh = Rows(m, n, t, n + pad, shift, randn(7, m, n))
+    _, pre, _, e = ref.gated(x.t, w.t, gate)
+    dpre = Rows(m, 2 * n, t, 2 * n + pad, shift)
+    held = None
+    if saved:
+        held = dpre if in_place else Rows(m, 2 * n, t, 2 * n + pad, shift)
+        held.t.copy_(pre)
+        pre, e = held.t.double().clone(), torch.zeros_like(pre)
+    dx = Rows(m, k, t, k + pad, shift) if "dx" in want else None
+    dw = Rows(2 * n, k, t, k + pad, shift) if "dw" in want else None
+    p = mm.gated_params(dt, m, n, k, gate=gate, ldx=x.ld, ldw=w.ld, ldpre=dpre.ld, ldh=dh.ld)
+    rec = mm.mm_gated_grad(p, x.buf, w.buf, held.buf if saved else None, dh.buf, dpre.buf,
+                           dx.buf if dx else None, dw.buf if dw else None, stream=stream())
+    assert rec.route == mm.MM_ROUTE_GATED and rec.dispatch_count == 1 + len(want)
+    wd, ed = ref.gated_grad(pre, e, dh.t, gate)
+    near(dpre.t, wd, ed + rounding(dt, wd.abs() + ed), "dpre")
+    dpre.untouched()
+    if dx:  # of the rounded dpre
+        v, ev = ref.products(dpre.t, w.t.t())
+        near(dx.t, v, ev + rounding(dt, v.abs() + ev), "dx")
+        dx.untouched()
+    if dw:
+        v, ev = ref.products(dpre.t.t(), x.t.t())
+        near(dw.t, v, ev + rounding(dt, v.abs() + ev), "dw")
+        dw.untouched()
+    return rec
+
+
+SIZES = [(1, 1, 1), (1, 64, 64), (2, 3, 5), (5, 17, 24), (16, 16, 32), (17, 33, 40), (33, 130, 72), (64, 64, 128),
+         (65, 127, 264), (129, 65, 200), (130, 192, 513), (300, 257, 96)]
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_gated(dt, m, n, k):
+    check_gated(dt, m, n, k, gate=GATES[(m + n) % 2], saved=n % 2 == 1)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("pad,shift", [(1, 0), (0, 1), (3, 5), (8, 8)])
+@pytest.mark.parametrize("m", [3, 70])
+def test_gated_pitches_and_starts(dt, pad, shift, m):
+    check_gated(dt, m, 50, 88, gate=ref.GELU, pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("saved", [False, True])
+def test_gated_grad(dt, m, n, k, saved):
+    check_grad(dt, m, n, k, gate=GATES[(m + n) % 2], saved=saved)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("pad,shift", [(1, 0), (0, 1), (3, 5), (8, 8)])
+@pytest.mark.parametrize("saved", [False, True])
+def test_gated_grad_pitches_and_starts(dt, pad, shift, saved):
+    check_grad(dt, 37, 50, 88, gate=ref.GELU, saved=saved, pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("want", [(), ("dx",), ("dw",)])
+@pytest.mark.parametrize("saved", [False, True])
+def test_gated_grad_parts(want, saved):
+    check_grad(2, 40, 48, 64, saved=saved, want=want)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_gated_grad_in_place(dt):
+    check_grad(dt, 41, 50, 64, in_place=True)
+    check_grad(dt, 41, 51, 64, in_place=True, pad=3, shift=1)
+
+
+@pytest.mark.parametrize("gate", GATES)
+def test_gradients_against_differences(gate):
+    """f32 gradients against differences of the 64-bit forward; the difference's own error is step^2."""
+    m, n, k = 4, 6, 8
+    x, w, dh = randn(1, m, k), randn(2, 2 * n, k, scale=0.5), randn(3, m, n)
+    dpre, dx, dw = (torch.empty(*s, device=DEV) for s in ((m, 2 * n), (m, k), (2 * n, k)))
+    mm.mm_gated_grad(mm.gated_params(0, m, n, k, gate=gate), mm.buf(x), mm.buf(w), None, mm.buf(dh), mm.buf(dpre),
+                     mm.buf(dx), mm.buf(dw), stream=stream())
+    f = lambda x, w: float((ref.gated(x, w, gate)[0] * dh.double()).sum())  # noqa: E731
+    step = 1e-5
+    for t, grad in ((x.double(), dx), (w.double(), dw)):
+        for i in range(0, t.numel(), 5):
+            up, down = t.clone(), t.clone()
+            up.view(-1)[i] += step
+            down.view(-1)[i] -= step
+            pair = (up, down) if grad is dw else (up, down)
+            diff = (f(x.double(), pair[0]) - f(x.double(), pair[1]) if grad is dw else
+                    f(pair[0], w.double()) - f(pair[1], w.double())) / (2 * step)
+            assert abs(diff - float(grad.view(-1)[i])) < 2e-5
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("gate", GATES)
+def test_far_pre_activations(dt, gate):
+    """Gates far on both sides, zeros, and values whose cubes leave f32: no NaN, h and gradients as defined."""
+    t = TORCH[dt]
+    big = 3e4 if dt == 1 else 1e18
+    g = torch.tensor([0.0, -0.0, 1.0, -1.0, 30.0, -30.0, 80.0, -80.0, 1000.0, -1000.0, big, -big], device=DEV)
+    n = g.numel()
+    pre = torch.cat((g, torch.ones(n, device=DEV))).to(t)[None].contiguous()
+    dh = torch.full((1, n), 0.5, dtype=t, device=DEV)
+    x, w = torch.ones(1, 1, dtype=t, device=DEV), pre.t().contiguous()
+    p = mm.gated_params(dt, 1, n, 1, gate=gate)
+    h, dpre = torch.empty(1, n, dtype=t, device=DEV), torch.empty(1, 2 * n, dtype=t, device=DEV)
+    mm.mm_gated(p, mm.buf(x), mm.buf(w), mm.buf(h), None, stream=stream())
+    want, _, e, _ = ref.gated(x, w, gate)
+    near(h, want, e + rounding(dt, want.abs() + e), "h")
+    wd, ed = ref.gated_grad(pre.double(), torch.zeros(1, 2 * n, dtype=torch.float64, device=DEV), dh, gate)
+    for saved in (mm.buf(pre), None):
+        mm.mm_gated_grad(p, mm.buf(x), mm.buf(w), saved, mm.buf(dh), mm.buf(dpre), None, None, stream=stream())
+        # x w here is one product of numbers with few bits: exact
+        near(dpre, wd, ed + rounding(dt, wd.abs() + ed), "dpre")
+
+
+# ---- codes -----------------------------------------------------------------------
+
+
+def check_quant(dt, m, k, ldx=0, ldq=0, shift=0, value=None):
+    x = Rows(m, k, TORCH[dt], ldx, shift, randn(m * 31 + k, m, k) if value is None else value)
+    q, s = Rows(m, k, torch.int8, ldq, shift), Rows(m, 1, torch.float32, 0, shift % 4)
+    rec = mm.mm_i8_quant(mm.quant_params(dt, m, k, ldx=x.ld, ldq=q.ld), x.buf, q.buf, s.buf, stream=stream())
+    assert rec.kernel == mm.MM_KERNEL_I8_QUANT and rec.route == mm.MM_ROUTE_I8 and rec.dispatch_count == 1
+    wq, ws = ref.quantise(x.t)
+    assert torch.equal(s.t[:, 0], ws)
+    assert torch.equal(q.t, wq), f"{int((q.t != wq).sum())} codes differ"
+    q.untouched()
+    s.untouched()
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,k", [(1, 1), (1, 7), (3, 16), (2, 255), (5, 256), (4, 1000), (7, 2048), (2, 4097), (1, 8192),
+                                 (3, 11008), (2, 16385), (1, 40000), (1, 100003), (600, 64), (2100, 33), (1500, 520)])
+def test_quant(dt, m, k):
+    check_quant(dt, m, k)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("ldx,ldq,shift", [(1030, 1031, 0), (1024, 1024, 1), (1025, 1040, 3), (1032, 1024, 8), (1024, 1025, 0)])
+@pytest.mark.parametrize("m", [3, 1100])
+def test_quant_pitches_and_starts(dt, ldx, ldq, shift, m):
+    check_quant(dt, m, 1023 if ldx == 1025 else 1024, ldx, ldq, shift)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_quant_ties_and_every_value(dt):
+    """Exact halves of a scale, zero rows, rows of tiny numbers; in 16 bits every finite value."""
+    half = torch.arange(-254, 255, device=DEV).float() / 2
+    rows = [half * f for f in (1.0, 0.25, 2.0 ** -8, 0.0)]
+    if dt != 1:
+        rows += [half * 2.0 ** -120, half * 2.0 ** -128, half * 2.0 ** -133]
+    check_quant(dt, len(rows), 509, value=torch.stack(rows))
+    if dt:
+        bits = torch.arange(-32768, 32768, dtype=torch.int32, device=DEV).to(torch.int16).view(TORCH[dt])
+        v = bits[torch.isfinite(bits)]
+        check_quant(dt, 1, v.numel(), value=v[None])
+        v = v[v.abs() < 100]
+        check_quant(dt, 1, v.numel(), value=v[None])
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("k", [40, 5000, 70000])
+def test_quant_rows_that_are_not_finite(dt, k):
+    x = randn(5, 6, k, dtype=TORCH[dt])
+    x[1, k // 2] = float("nan")
+    x[2, k - 1] = float("inf")
+    x[3, 0] = float("-inf")
+    x[4, 1], x[4, k - 2] = float("inf"), float("nan")
+    q, s = torch.full((6, k), 99, dtype=torch.int8, device=DEV), torch.zeros(6, device=DEV)
+    mm.mm_i8_quant(mm.quant_params(dt, 6, k), mm.buf(x), mm.buf(q), mm.buf(s), stream=stream())
+    wq, ws = ref.quantise(x[[0, 5]])
+    assert torch.equal(q[[0, 5]], wq) and torch.equal(s[[0, 5]], ws)
+    assert not q[1:5].any()
+    assert bool(s[[1, 4]].isnan().all()) and bool(torch.isposinf(s[[2, 3]]).all())
+    w, ws, y = torch.ones(3, 48, dtype=torch.int8, device=DEV), torch.ones(3, device=DEV), torch.zeros(6, 3, device=DEV)
+    qx = torch.zeros(6, 48, dtype=torch.int8, device=DEV)
+    qx[:, :40] = q[:, :40]
+    mm.mm_i8_gemm(mm.i8_params(0, 6, 3, 48), mm.buf(qx), mm.buf(s), mm.buf(w), mm.buf(ws), mm.buf(y), stream=stream())
+    assert bool(y[1:5].isnan().all()) and bool(torch.isfinite(y[[0, 5]]).all())
+
+
+def codes(seed, m, k, low=-127):
+    return torch.randint(low, 128, (m, k), generator=gen(seed), device=DEV, dtype=torch.int8)
+
+
+def check_i8(dt, m, n, k, gate=ref.NONE, pad=0, ypad=0, shift=0, low=-127):
+    rows = n * (1 + (gate > 0))
+    x = Rows(m, k, torch.int8, k + pad, shift, codes(m + k, m, k, low))
+    w = Rows(rows, k, torch.int8, k + pad, shift, codes(n + k, rows, k, low))
+    s = Rows(m, 1, torch.float32, 0, shift % 4, torch.rand(m, 1, generator=gen(1), device=DEV) * 0.02 + 1e-3)
+    ws = Rows(rows, 1, torch.float32, 0, shift % 3, (torch.rand(rows, 1, generator=gen(2), device=DEV) + 0.1) / (40 * k ** 0.5))
+    y = Rows(m, n, TORCH[dt], n + ypad, shift % 16)
+    p = mm.i8_params(dt, m, n, k, gate=gate, ldx=x.ld, ldw=w.ld, ldy=y.ld)
+    rec = mm.mm_i8_gemm(p, x.buf, s.buf, w.buf, ws.buf, y.buf, stream=stream())
+    assert rec.kernel == mm.MM_KERNEL_I8 and rec.route == mm.MM_ROUTE_I8 and rec.dispatch_count == 1
+    want, e = ref.i8(x.t, s.t[:, 0], w.t, ws.t[:, 0], gate)
+    near(y.t, want, e + rounding(dt, want.abs() + e), "y")
+    y.untouched()
+    return rec
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (1, 64, 64), (1, 100, 4096), (2, 3, 48), (4, 300, 1040), (5, 17, 80), (8, 33, 2048),
+                                   (16, 16, 128), (17, 33, 144), (33, 130, 208), (64, 64, 1024), (65, 127, 272),
+                                   (129, 65, 4112), (130, 192, 528), (300, 257, 96)])
+@pytest.mark.parametrize("gate", [ref.NONE, ref.SILU])
+def test_i8(dt, m, n, k, gate):
+    check_i8(dt, m, n, k, gate=gate)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("pad,ypad,shift", [(16, 1, 0), (0, 0, 16), (48, 3, 32), (16, 8, 48)])
+@pytest.mark.parametrize("m", [1, 3, 70, 200])
+@pytest.mark.parametrize("gate", [ref.NONE, ref.GELU])
+def test_i8_pitches_and_starts(dt, pad, ypad, shift, m, gate):
+    check_i8(dt, m, 50, 176, gate=gate, pad=pad, ypad=ypad, shift=shift)
+
+
+@pytest.mark.parametrize("m,n", [(1, 33), (9, 40), (70, 130)])
+def test_i8_largest_sums(m, n):
+    """The longest contraction with every code -128: sums of almost 2^31, exact."""
+    k = mm.MM_I8_MAX_K
+    x, w = (torch.full((r, k), -128, dtype=torch.int8, device=DEV) for r in (m, n))
+    s, ws, y = torch.ones(m, device=DEV), torch.ones(n, device=DEV), torch.empty(m, n, device=DEV)
+    mm.mm_i8_gemm(mm.i8_params(0, m, n, k), mm.buf(x), mm.buf(s), mm.buf(w), mm.buf(ws), mm.buf(y), stream=stream())
+    assert bool((y == float(k * 16384)).all())  # 8191 * 2^18: 13 bits
+    check_i8(0, m, n, k, low=-128)
+    check_i8(2, m, n, 4096, gate=ref.SILU, low=-128)
