@@ -1,6 +1,6 @@
 // Gated feed-forward block: h = act(x G^T) * (x U^T), and the gradients of its
 // pre-activations (mm.h, "Feed-forward block").
-#include "ffn_tile.hpp"
+#include "ffn_pipe.hpp"
 
 namespace mmk {
 
@@ -64,16 +64,16 @@ __global__ __launch_bounds__(256) void gated_grad(FfnArgs a, int sh) {
 
 hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_GATED;
-    return a.dtype == 0   ? run_ffn_tile<GatedOut<TF32>>(a, s)
-           : a.dtype == 1 ? run_ffn_tile<GatedOut<TF16>>(a, s)
-                          : run_ffn_tile<GatedOut<TBF16>>(a, s);
+    return a.dtype == 0   ? run_ffn<GatedOut<TF32>>(a, s, L)
+           : a.dtype == 1 ? run_ffn<GatedOut<TF16>>(a, s, L)
+                          : run_ffn<GatedOut<TBF16>>(a, s, L);
 }
 
 hipError_t launch_gated_again(const FfnArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_GATED_GRAD;
-    return a.dtype == 0   ? run_ffn_tile<GradOut<TF32>>(a, s)
-           : a.dtype == 1 ? run_ffn_tile<GradOut<TF16>>(a, s)
-                          : run_ffn_tile<GradOut<TBF16>>(a, s);
+    return a.dtype == 0   ? run_ffn<GradOut<TF32>>(a, s, L)
+           : a.dtype == 1 ? run_ffn<GradOut<TF16>>(a, s, L)
+                          : run_ffn<GradOut<TBF16>>(a, s, L);
 }
 
 hipError_t launch_gated_grad(const FfnArgs& a, hipStream_t s, Launched* L) {

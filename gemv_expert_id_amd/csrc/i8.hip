@@ -1,6 +1,6 @@
 // Rows to 8-bit codes with a scale each, and products of codes (mm.h,
 // "Feed-forward block").
-#include "ffn_tile.hpp"
+#include "ffn_pipe.hpp"
 
 namespace mmk {
 
@@ -68,8 +68,8 @@ __global__ __launch_bounds__(256) void i8_quant(QuantArgs a) {
 }
 
 template <class T>
-hipError_t run_i8(const FfnArgs& a, hipStream_t s) {
-    return a.gate ? run_ffn_tile<CodesOut<T, true>>(a, s) : run_ffn_tile<CodesOut<T, false>>(a, s);
+hipError_t run_i8(const FfnArgs& a, hipStream_t s, Launched* L) {
+    return a.gate ? run_ffn<CodesOut<T, true>>(a, s, L) : run_ffn<CodesOut<T, false>>(a, s, L);
 }
 
 }  // namespace
@@ -86,7 +86,7 @@ hipError_t launch_i8_quant(const QuantArgs& a, hipStream_t s, Launched* L) {
 
 hipError_t launch_i8(const FfnArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_I8;
-    return a.dtype == 0 ? run_i8<TF32>(a, s) : a.dtype == 1 ? run_i8<TF16>(a, s) : run_i8<TBF16>(a, s);
+    return a.dtype == 0 ? run_i8<TF32>(a, s, L) : a.dtype == 1 ? run_i8<TF16>(a, s, L) : run_i8<TBF16>(a, s, L);
 }
 
 }  // namespace mmk

@@ -149,7 +149,13 @@ typedef struct {
                                  MM_KERNEL_SORT_ROWS 1 when the plan was made
                                  in the same launch; for MM_KERNEL_Q4 the
                                  tokens of a tile (4 or 16) plus 256 times the
-                                 outputs of a block; 0 for every other family */
+                                 outputs of a block; for MM_KERNEL_GATED,
+                                 MM_KERNEL_I8 and a recomputing MM_KERNEL_GATED_GRAD
+                                 0 for the form that takes any alignment, 16-token
+                                 fragments (1 to 4) plus 256 times the waves that
+                                 split the contraction (1, 2 or 4) for few tokens,
+                                 tile edge (128 or 256) plus LDS regions (2 or 4)
+                                 for many; 0 for every other family */
 } mm_receipt;
 
 /* ------------------------------------------------------------------------ */

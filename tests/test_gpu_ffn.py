@@ -319,3 +319,39 @@ def test_i8_largest_sums(m, n):
     assert bool((y == float(k * 16384)).all())  # 8191 * 2^18: 13 bits
     check_i8(0, m, n, k, low=-128)
     check_i8(2, m, n, 4096, gate=ref.SILU, low=-128)
+
+
+# ---- the forms a product takes, by its size ------------------------------------------
+
+
+FORMS = [  # m, n, k of a gated product in 16 bits, and the receipt's variant
+    (1, 8209, 520, 1 + 256), (16, 8209, 1032, 1 + 256), (17, 8209, 264, 2 + 256), (48, 8209, 520, 3 + 256),
+    (64, 8209, 264, 4 + 256), (1, 4105, 2056, 1 + 512), (20, 4105, 520, 2 + 512), (33, 4105, 264, 3 + 512),
+    (61, 4105, 1544, 4 + 512), (1, 70, 4104, 1 + 1024), (30, 257, 2048, 2 + 1024), (40, 33, 1032, 3 + 1024),
+    (64, 100, 8, 4 + 1024), (65, 100, 1032, 128 + 4), (200, 257, 72, 128 + 4), (1100, 1985, 200, 128 + 2),
+    (1200, 1950, 1032, 128 + 2), (3500, 1795, 200, 256 + 2), (3329, 1985, 1096, 256 + 2),
+]
+
+
+@pytest.mark.parametrize("dt", [1, 2])
+@pytest.mark.parametrize("m,n,k,variant", FORMS)
+def test_gated_forms(dt, m, n, k, variant):
+    assert check_gated(dt, m, n, k, gate=GATES[m % 2], saved=n % 2 == 1, pad=8).variant == variant
+
+
+@pytest.mark.parametrize("m,n,k,variant", FORMS)
+def test_i8_forms(m, n, k, variant):
+    k = k // 8 * 16
+    assert check_i8(m % 3, m, n, k, gate=GATES[m % 2], pad=16).variant == variant
+    assert check_i8(m % 3, m, 2 * n, k, pad=16).variant == variant
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 4105, 264), (64, 8209, 72), (40, 70, 1032), (200, 257, 68), (1100, 1985, 200)])
+def test_gated_forms_f32(m, n, k):
+    check_gated(0, m, n, k, gate=GATES[m % 2], pad=4)
+    check_grad(0, m, n, k, gate=GATES[m % 2], saved=False, want=())
+
+
+@pytest.mark.parametrize("m,n,k,variant", [f for f in FORMS if f[2] != 1032])
+def test_gradient_forms(m, n, k, variant):
+    assert check_grad(1, m, n, k, gate=GATES[m % 2], saved=False, want=()).variant == variant
