@@ -755,7 +755,7 @@ mm_status gated_plan(const mm_gated_params* p, mmk::FfnArgs* a, GatedSizes* z, i
     return MM_OK;
 }
 
-// One product C = op(A) . op(B) of rows, on the route that mm_gemm takes.
+// One product C = op(A) . op(B) of rows.
 GemmPlan rows_product(int dt, int64_t m, int64_t n, int64_t k, bool ta, const void* a, int64_t lda,
                       const void* b, int64_t ldb, void* c, int64_t ldc) {
     return GemmPlan{dt, 1, m, n, k, lda, ldb, ldc, 0, 0, 0, ta, false,
@@ -765,7 +765,7 @@ hipError_t launch_product(const GemmPlan& p, hipStream_t s, mmk::Launched* L) {
     if (p.m == 1 || p.n == 1) return mmk::launch_gemv(gemv_args(p), s, L);
     mmk::GemmArgs g{p.a, p.b, p.c, p.m, p.n, p.k, p.lda, p.ldb, p.ldc, p.sa, p.sb, p.sc,
                     p.batch, p.dt, p.ta, p.tb, p.alpha, p.beta};
-    return mmk::launch_gemm(g, s, L);
+    return mmk::launch_gated_product(g, s, L);
 }
 
 }  // namespace

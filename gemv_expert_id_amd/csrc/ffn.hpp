@@ -2,12 +2,13 @@
 // types, one 64-byte step of 16 x 16 matrix instructions, and what becomes of a
 // lane's four neighbouring sums.
 //
-// Every type is handled by its bytes: a fragment is 16 rows of 64 bytes, lane l
-// holding the 16 bytes at chunk l / 16 of row l % 16, in both operands. The
-// order of the contraction inside a step is free as long as both share it, so
-// f32 runs four 16x16x4 instructions, one for each component of the lanes'
-// chunks; f16 and bf16 one 16x16x32, 8-bit codes one 16x16x64.
+// Types are handled by their bytes: a fragment is 16 rows of 64 bytes, lane l
+// holding the 16 bytes at chunk l / 16 of row l % 16, in both operands; f16 and bf16
+// take one 16x16x32 instruction for it, 8-bit codes one 16x16x64. (The order of the
+// contraction inside a step is free as long as both operands share it.)
 #pragma once
+
+#include <type_traits>
 
 #include "common.hpp"
 #include "gate.hpp"
@@ -28,12 +29,7 @@ template <> struct AccOf<TI8> { using type = i32x4; };
 
 template <class E>
 __device__ __forceinline__ typename AccOf<E>::type step_mma(u32x4 w, u32x4 x, typename AccOf<E>::type acc) {
-    if constexpr (E::code == 0) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[q]), __uint_as_float(x[q]), acc, 0, 0, 0);
-        return acc;
-    } else if constexpr (E::code == 1) {
+    if constexpr (E::code == 1) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, x),
                                                       acc, 0, 0, 0);
     } else if constexpr (E::code == 2) {

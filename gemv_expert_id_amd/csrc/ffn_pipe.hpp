@@ -121,9 +121,13 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
                                                      col * ldw + st * TStage, 0, 0);
         }
     };
-    Acc acc[FM];
+    // f32 sums run in four chains, one for each component of the lanes' chunks.
+    constexpr int CH = E::code == 0 ? 4 : 1;
+    Acc chain[FM][CH];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) acc[i] = Acc{0, 0, 0, 0};
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int q = 0; q < CH; ++q) chain[i][q] = Acc{0, 0, 0, 0};
     auto compute = [&](auto S_) {
         const char* base = thin_stage<Z::BYTES, decltype(S_)::value>();
 #pragma unroll
@@ -133,7 +137,14 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const u32x4 xf = *reinterpret_cast<const u32x4*>(base + (i * 16 + lr) * TStage + at);
-                acc[i] = step_mma<E>(wf, xf, acc[i]);
+                if constexpr (E::code == 0) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        chain[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            __uint_as_float(wf[q]), __uint_as_float(xf[q]), chain[i][q], 0, 0, 0);
+                } else {
+                    chain[i][0] = step_mma<E>(wf, xf, chain[i][0]);
+                }
             }
         }
     };
@@ -149,6 +160,12 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
         });
     }
     __builtin_amdgcn_s_waitcnt(ffn_wait(0));  // no load into LDS outlives its wave
+    Acc acc[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        acc[i] = chain[i][0];
+        if constexpr (E::code == 0) acc[i] = (acc[i] + chain[i][1]) + (chain[i][2] + chain[i][3]);
+    }
     if constexpr (KS > 1) {
         __syncthreads();
         Acc* part = reinterpret_cast<Acc*>(thin_stage<Z::BYTES, 0>());
@@ -209,8 +226,7 @@ __global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(Ffn
     constexpr bool G = Out::kGated;
     constexpr int BM = Z::BM, WT = Z::WT, HF = TF / 2, LD = Z::LOADS, LPP = 2 * LD;
     constexpr int WO = G ? BM / 2 : BM;                      // outputs of a tile
-    constexpr int MULT = E::code == 0 ? 4 : 1;               // instructions of a 64-byte step
-    constexpr int MPR = HF * TF / LD * MULT;                 // matrix instructions between loads
+    constexpr int MPR = HF * TF / LD;                        // matrix instructions between loads
     extern __shared__ __attribute__((aligned(1024))) char pipe_lds[];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -307,12 +323,12 @@ __global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(Ffn
         rdw(S1{}, w1);
         mma(1, x1, w0);
         __builtin_amdgcn_sched_group_barrier(0x100, HF + TF, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, HF * TF * MULT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, HF * TF, 0);
         __builtin_amdgcn_sched_barrier(0);
         rdx(S1{}, 1, x1);
         mma(0, x0, w1);
         __builtin_amdgcn_sched_group_barrier(0x100, HF, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, HF * TF * MULT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, HF * TF, 0);
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(ffn_wait((NREG - 2) * LPP));  // pair p + 1 has landed
         __builtin_amdgcn_s_barrier();                            // region R has been read
@@ -395,7 +411,9 @@ hipError_t run_ffn_thin(const FfnArgs& a, int fm, int ks, hipStream_t s) {
 template <class Out>
 hipError_t run_ffn(const FfnArgs& a, hipStream_t s, Launched* L) {
     using E = typename Out::E;
-    if (!ffn_chunked(a, sizeof(typename E::store_t))) return run_ffn_tile<Out>(a, s);
+    if constexpr (E::code != 3) {  // codes always are
+        if (!ffn_chunked(a, sizeof(typename E::store_t)) || (E::code == 0 && a.m > 64)) return run_ffn_tile<Out>(a, s);
+    }
     const int64_t rows = Out::kGated ? 2 * a.n : a.n;
     if (a.m <= 64) {
         const int fm = (int)((a.m + 15) / 16);
@@ -403,20 +421,21 @@ hipError_t run_ffn(const FfnArgs& a, hipStream_t s, Launched* L) {
         L->variant = fm + 256 * ks;
         return run_ffn_thin<Out>(a, fm, ks, s);
     }
-    const int64_t big = ((a.m + 255) / 256) * ((rows + 255) / 256);
     if constexpr (E::code != 0) {
+        const int64_t big = ((a.m + 255) / 256) * ((rows + 255) / 256);
         if (big >= 192) {
             L->variant = 256 + 2;
             return run_ffn_pipe<Out, 8, 2>(a, s);
         }
+        const int64_t mid = ((a.m + 127) / 128) * ((rows + 127) / 128);
+        if (mid > 256) {
+            L->variant = 128 + 2;
+            return run_ffn_pipe<Out, 4, 2>(a, s);
+        }
+        L->variant = 128 + 4;
+        return run_ffn_pipe<Out, 4, 4>(a, s);
     }
-    const int64_t mid = ((a.m + 127) / 128) * ((rows + 127) / 128);
-    if (mid > 256) {
-        L->variant = 128 + 2;
-        return run_ffn_pipe<Out, 4, 2>(a, s);
-    }
-    L->variant = 128 + 4;
-    return run_ffn_pipe<Out, 4, 4>(a, s);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace mmk

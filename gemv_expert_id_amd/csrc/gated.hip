@@ -14,7 +14,7 @@ template <class T>
 __global__ __launch_bounds__(256) void gated_grad(FfnArgs a, int sh) {
     using S = typename T::store_t;
     constexpr int V = T::Elems16;
-    using U16 = Unaligned16<S>;
+    using U16 = Pack<S, V>;
     const int64_t c = (int64_t)blockIdx.x * (1 << sh) + (threadIdx.x & ((1 << sh) - 1));
     const int64_t col = c * V;
     if (col >= a.n) return;
@@ -60,7 +60,37 @@ __global__ __launch_bounds__(256) void gated_grad(FfnArgs a, int sh) {
     }
 }
 
+template <class T>
+hipError_t tile_product(const GemmArgs& g, hipStream_t s) {
+    FfnArgs o{};
+    o.y = g.C;
+    o.ldy = g.ldc;
+    o.n = g.n;
+    const TileArgs t{g.A, g.B, g.m, g.n, g.k, g.lda, g.ldb, 0};
+    return g.ta ? run_ffn_tile<PlainOut<T>, false, false>(t, o, s) : run_ffn_tile<PlainOut<T>, true, false>(t, o, s);
+}
+
 }  // namespace
+
+// dpre . w (both as stored: NN) or dpre^T . x (TN). 16-bit products that the pipelined
+// GEMM takes go to it; a contraction over the tokens need not be a multiple of its
+// step there.
+hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
+    const auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+    const int64_t span_a = g.ta ? (g.k + 127) * g.lda + g.m : (g.m - 1) * g.lda + g.k;
+    const int64_t span_b = (g.k + 127) * g.ldb + g.n;
+    const bool piped = g.dtype != 0 && al16(g.A) && al16(g.B) && g.lda % 8 == 0 && g.ldb % 8 == 0 &&
+                       (reinterpret_cast<uintptr_t>(g.C) & 7) == 0 && g.ldc % 4 == 0 && g.lda < (1 << 22) &&
+                       g.ldb < (1 << 22) && span_a < (1ll << 30) && span_b < (1ll << 30) &&
+                       (g.ta || (g.k % 128 == 0 && g.k >= 256));
+    if (piped) {
+        GemmArgs q = g;
+        q.ragged_k = 1;
+        return launch_gemm(q, s, L);
+    }
+    L->kernel = MM_KERNEL_GATED_GRAD;
+    return g.dtype == 0 ? tile_product<TF32>(g, s) : g.dtype == 1 ? tile_product<TF16>(g, s) : tile_product<TBF16>(g, s);
+}
 
 hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_GATED;

@@ -782,7 +782,11 @@ __global__ __launch_bounds__(LThreads, TF == 8 ? 1 : 2) void gemm_mfma_large(Gem
     const int wm = w >> 1, wn = w & 1;
     int64_t m0, n0;
     if (!pipelined_tile<BM, RAG>(a, m0, n0)) return;
-    const int nk = (int)(a.k / LBK);  // a multiple of LSTAGES, at least 2 * LSTAGES
+    // A multiple of LSTAGES, at least 2 * LSTAGES. With both operands K-strided k
+    // may end inside the last ones (ragged_k): rows from k on lie past both
+    // resources' ranges and read as zeros.
+    const int nk_k = KA || KB ? (int)(a.k / LBK) : (int)((a.k + LSTAGES * LBK - 1) / (LSTAGES * LBK)) * LSTAGES;
+    const int nk = nk_k < 2 * LSTAGES ? 2 * LSTAGES : nk_k;
     const int lda = (int)a.lda, ldb = (int)a.ldb;
 
     // DMA lane mapping, K-contiguous operand (A [m,k], B [n,k]): instruction
@@ -1472,8 +1476,9 @@ hipError_t launch_gemm(const GemmArgs& a, hipStream_t s, Launched* L) {
     // 256 x 256 from 192 tiles on, 128 x 128 at 128 tiles and below, and
     // 128 x 128 ahead of the 128 x 128 register-staged kernel at every
     // measured shape.
-    const bool pipelined = vec && a.k % (LSTAGES * LBK) == 0 &&
-                           a.k >= 2 * LSTAGES * LBK && a.lda < (1 << 22) && a.ldb < (1 << 22) &&
+    const bool any_k = a.ragged_k && a.ta && !a.tb;
+    const bool pipelined = vec && (any_k || (a.k % (LSTAGES * LBK) == 0 && a.k >= 2 * LSTAGES * LBK)) &&
+                           a.lda < (1 << 22) && a.ldb < (1 << 22) &&
                            a.ldc % 4 == 0 && (reinterpret_cast<uintptr_t>(a.C) & 7) == 0 && a.sc % 4 == 0;
     // m or n need not be multiples of the tile edge (edge tiles are cut at
     // the operands' extents and masked at the store).

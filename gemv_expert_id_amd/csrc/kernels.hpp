@@ -68,6 +68,7 @@ struct GemmArgs {
     int32_t dtype;
     int32_t ta, tb;
     float alpha, beta;   // C = alpha * op(A) op(B) + beta * C_old (beta == 0: C_old unread)
+    int32_t ragged_k = 0;  // TN, 16-byte rows: the pipelined kernel at any k (zeros past it)
 };
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t s, Launched* L);
 
@@ -171,6 +172,7 @@ struct FfnArgs {
 hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L);        // y and pre_w
 hipError_t launch_gated_again(const FfnArgs& a, hipStream_t s, Launched* L);  // pre_w from x, w, dh
 hipError_t launch_gated_grad(const FfnArgs& a, hipStream_t s, Launched* L);   // pre_w from pre, dh
+hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L);  // NN or TN
 hipError_t launch_i8(const FfnArgs& a, hipStream_t s, Launched* L);
 
 // Rows of x to 8-bit codes and a scale each.

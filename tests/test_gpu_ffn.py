@@ -355,3 +355,20 @@ def test_gated_forms_f32(m, n, k):
 @pytest.mark.parametrize("m,n,k,variant", [f for f in FORMS if f[2] != 1032])
 def test_gradient_forms(m, n, k, variant):
     assert check_grad(1, m, n, k, gate=GATES[m % 2], saved=False, want=()).variant == variant
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 64, 96), (2, 128, 256), (37, 64, 96), (129, 128, 512), (300, 260, 264), (511, 192, 2040),
+                                   (1025, 516, 72), (2, 4096, 2048), (700, 1024, 1032)])
+def test_gradient_products(dt, m, n, k):
+    """Rows of whole 16-byte pieces; contractions over tokens of any count."""
+    check_grad(dt, m, n, k, gate=GATES[m % 2], pad=8)
+    check_grad(dt, m, n, k, gate=GATES[m % 2], pad=0)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1100, 1985, 33), (1203, 1950, 129), (33, 1985, 1100), (1985, 70, 1985)])
+def test_any_alignment_large_tiles(dt, m, n, k):
+    check_gated(dt, m, n, k, pad=1)
+    check_grad(dt, m, n, k, pad=1, saved=False)
+    check_grad(dt, m, n, k, gate=ref.GELU)
