@@ -732,8 +732,8 @@ mm_status gated_plan(const mm_gated_params* p, mmk::FfnArgs* a, GatedSizes* z, i
         return fail(MM_ERR_INVALID_ARGUMENT, "gated: gate %u is not SiLU or GELU", p->gate);
     if (!p->m || !p->n || !p->k) return fail(MM_ERR_INVALID_ARGUMENT, "gated: m, n and k must be nonzero");
     if (p->reserved) return fail(MM_ERR_INVALID_ARGUMENT, "gated: reserved must be 0");
-    if (p->m >= (1u << 31) || p->n > (1u << 24) || p->k > (1u << 24))
-        return fail(MM_ERR_INVALID_ARGUMENT, "gated: m must be below 2^31, n and k at most 2^24");
+    if (p->m > (1u << 24) || p->n > (1u << 24) || p->k > (1u << 24) || (uint64_t)p->m * p->n > (1ull << 36))
+        return fail(MM_ERR_INVALID_ARGUMENT, "gated: m, n and k must be at most 2^24, m*n at most 2^36");
     *a = mmk::FfnArgs{};
     z->es = elt_size(p->dtype);
     *ldx = p->ldx;
@@ -1230,8 +1230,8 @@ mm_status mm_i8_gemm(const mm_i8_params* params, mm_buf x, mm_buf x_scales, mm_b
     if (p->gate > MM_GATE_GELU) return fail(MM_ERR_INVALID_ARGUMENT, "i8: unknown gate %u", p->gate);
     if (!p->m || !p->n || !p->k) return fail(MM_ERR_INVALID_ARGUMENT, "i8: m, n and k must be nonzero");
     if (p->reserved) return fail(MM_ERR_INVALID_ARGUMENT, "i8: reserved must be 0");
-    if (p->m >= (1u << 31) || p->n > (1u << 24))
-        return fail(MM_ERR_INVALID_ARGUMENT, "i8: m must be below 2^31 and n at most 2^24");
+    if (p->m > (1u << 24) || p->n > (1u << 24) || (uint64_t)p->m * p->n > (1ull << 36))
+        return fail(MM_ERR_INVALID_ARGUMENT, "i8: m and n must be at most 2^24, m*n at most 2^36");
     if (p->k % 16 || p->k > MM_I8_MAX_K)
         return fail(MM_ERR_INVALID_ARGUMENT, "i8: k %u is not a multiple of 16 up to %u", p->k, MM_I8_MAX_K);
     const uint64_t N = (uint64_t)p->n * (p->gate ? 2 : 1), es = elt_size(p->dtype);
@@ -1244,8 +1244,8 @@ mm_status mm_i8_gemm(const mm_i8_params* params, mm_buf x, mm_buf x_scales, mm_b
     if ((st = rows_extent("i8 x", p->m, p->k, &a.ldx, 1, &xbytes)) != MM_OK) return st;
     if ((st = rows_extent("i8 w", N, p->k, &a.ldw, 1, &wbytes)) != MM_OK) return st;
     if ((st = rows_extent("i8 y", p->m, p->n, &a.ldy, es, &ybytes)) != MM_OK) return st;
-    if (a.ldx % 16 || a.ldw % 16 || a.ldx >= (1 << 24) || a.ldw >= (1 << 24))
-        return fail(MM_ERR_INVALID_ARGUMENT, "i8: pitches of codes (%lld, %lld) must be multiples of 16 below 2^24",
+    if (a.ldx % 16 || a.ldw % 16 || a.ldx >= (1 << 22) || a.ldw >= (1 << 22))
+        return fail(MM_ERR_INVALID_ARGUMENT, "i8: pitches of codes (%lld, %lld) must be multiples of 16 below 2^22",
                     (long long)a.ldx, (long long)a.ldw);
     Operand ops[] = {{"i8 x", x, xbytes, 16, false},
                      {"i8 x scales", x_scales, (uint64_t)p->m * 4, 4, false},

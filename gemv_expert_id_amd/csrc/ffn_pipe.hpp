@@ -40,31 +40,29 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 #define MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
 // ---------------------------------------------------------------------------
-// Few tokens: 16 FM tokens by 64 / KS rows of W, the contraction in stages of
-// 256 bytes.
+// Few tokens: 16 FM tokens by 16 rows of W, the contraction in stages of 256 bytes.
 //
 // W is read once, 256 contiguous bytes of a row at a time, and the tokens' pieces
-// with it (from L2). A stage is four steps of matrix instructions. KS = 1: the four
-// waves take 16 rows each and all four steps; KS = 2 and 4: 32 or 16 rows, the waves
-// split the steps and are joined through LDS at the end, for the rows that would
-// leave CUs idle otherwise. Chunk c of LDS row r lies at slot c ^ (r & 15), so the
-// 16 rows of a fragment read cover all banks.
+// with it (from L2). A stage is four steps of matrix instructions, one for each
+// wave; the waves' sums are joined through LDS at the end. So narrow a tile keeps
+// many blocks in flight: one token through 22016 x 4096 takes 36.1 us in bf16 (5.0
+// TB/s), 41.6 with 64 rows a block and unsplit steps; through 1024 x 8192, 10.3 and
+// 16.9. Chunk c of LDS row r lies at slot c ^ (r & 15), so the 16 rows of a fragment
+// read cover all banks.
 //
 // Gated, a fragment's 16 rows are eight of the gate and the same eight of the up
 // projection: the two sums of an output end 32 lanes apart.
 // ---------------------------------------------------------------------------
 constexpr int TStage = 256;  // bytes of k a stage
 constexpr int TRing = 4;     // stages in LDS
+constexpr int TRows = 16;    // rows of W
+constexpr int TWaves = 4;    // one for each 64-byte step of a stage
 
-template <int FM, int KS>
+template <int FM>
 struct ThinShape {
-    static constexpr int XR = 16 * FM;           // tokens
-    static constexpr int WN = 4 / KS;            // waves along W's rows
-    static constexpr int WR = 16 * WN;           // rows of W
-    static constexpr int XI = FM, WI = WR / 16;  // loads of a wave and stage
-    static constexpr int LOADS = XI + WI;
-    static constexpr int BYTES = (XR + WR) * TStage;
-    static constexpr int STEPS = 4 / KS;  // steps of a wave and stage
+    static constexpr int XR = 16 * FM;    // tokens
+    static constexpr int LOADS = FM + 1;  // of a wave and stage
+    static constexpr int BYTES = (XR + TRows) * TStage;
 };
 
 // Stage S of the ring: arrays of their own, so that the compiler sees that reads of
@@ -75,16 +73,16 @@ __device__ __forceinline__ char* thin_stage() {
     return st;
 }
 
-template <class Out, int FM, int KS>
-__global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
+template <class Out, int FM>
+__global__ __launch_bounds__(64 * TWaves) void ffn_thin(FfnArgs a, int tiles_m) {
     using E = typename Out::E;
     using Acc = typename AccOf<E>::type;
-    using Z = ThinShape<FM, KS>;
+    using Z = ThinShape<FM>;
     constexpr bool G = Out::kGated;
-    constexpr int WO = G ? Z::WR / 2 : Z::WR;  // outputs
+    constexpr int WO = G ? TRows / 2 : TRows;  // outputs
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wn = w % Z::WN, ks = w / Z::WN, lr = lane & 15, lq = lane >> 4;
+    const int lr = lane & 15, lq = lane >> 4;
     // Token tiles of the same rows of W follow each other on one XCD.
     const int64_t tiles = (int64_t)tiles_m * ((a.n + WO - 1) / WO);
     const int64_t per_xcd = (tiles + 7) / 8;
@@ -105,21 +103,17 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
     auto issue = [&](auto S_, int st) {
         char* base = thin_stage<Z::BYTES, decltype(S_)::value>();
 #pragma unroll
-        for (int j = 0; j < Z::XI; ++j) {
-            const int row = (w * Z::XI + j) * 4, c = c0 ^ (row & 12);
+        for (int j = 0; j < FM; ++j) {
+            const int row = (w * FM + j) * 4, c = c0 ^ (row & 12);
             const uint32_t at = st * 16 + c < chunks ? (uint32_t)(r4 * ldx + c * 16) : kPastEnd;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MM_LDS(base + row * TStage), 16, at,
                                                      row * ldx + st * TStage, 0, 0);
         }
-#pragma unroll
-        for (int j = 0; j < Z::WI; ++j) {
-            const int row = (w * Z::WI + j) * 4, c = c0 ^ (row & 12);
-            const uint32_t at = st * 16 + c < chunks ? (uint32_t)(r4 * ldw + c * 16) : kPastEnd;
-            const bool up = G && (row & 8);
-            const int col = G ? (row >> 4) * 8 + (row & 7) : row;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : rw, MM_LDS(base + (Z::XR + row) * TStage), 16, at,
-                                                     col * ldw + st * TStage, 0, 0);
-        }
+        const int row = w * 4, c = c0 ^ row;
+        const uint32_t at = st * 16 + c < chunks ? (uint32_t)(r4 * ldw + c * 16) : kPastEnd;
+        const bool up = G && w >= 2;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : rw, MM_LDS(base + (Z::XR + row) * TStage), 16, at,
+                                                 (G ? row & 7 : row) * ldw + st * TStage, 0, 0);
     };
     // f32 sums run in four chains, one for each component of the lanes' chunks.
     constexpr int CH = E::code == 0 ? 4 : 1;
@@ -130,21 +124,18 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
         for (int q = 0; q < CH; ++q) chain[i][q] = Acc{0, 0, 0, 0};
     auto compute = [&](auto S_) {
         const char* base = thin_stage<Z::BYTES, decltype(S_)::value>();
+        const int at = ((4 * w + lq) ^ lr) * 16;
+        const u32x4 wf = *reinterpret_cast<const u32x4*>(base + (Z::XR + lr) * TStage + at);
 #pragma unroll
-        for (int s = 0; s < Z::STEPS; ++s) {
-            const int at = ((4 * (ks * Z::STEPS + s) + lq) ^ lr) * 16;
-            const u32x4 wf = *reinterpret_cast<const u32x4*>(base + (Z::XR + wn * 16 + lr) * TStage + at);
+        for (int i = 0; i < FM; ++i) {
+            const u32x4 xf = *reinterpret_cast<const u32x4*>(base + (i * 16 + lr) * TStage + at);
+            if constexpr (E::code == 0) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const u32x4 xf = *reinterpret_cast<const u32x4*>(base + (i * 16 + lr) * TStage + at);
-                if constexpr (E::code == 0) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        chain[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            __uint_as_float(wf[q]), __uint_as_float(xf[q]), chain[i][q], 0, 0, 0);
-                } else {
-                    chain[i][0] = step_mma<E>(wf, xf, chain[i][0]);
-                }
+                for (int q = 0; q < 4; ++q)
+                    chain[i][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                        __uint_as_float(wf[q]), __uint_as_float(xf[q]), chain[i][q], 0, 0, 0);
+            } else {
+                chain[i][0] = step_mma<E>(wf, xf, chain[i][0]);
             }
         }
     };
@@ -166,21 +157,19 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
         acc[i] = chain[i][0];
         if constexpr (E::code == 0) acc[i] = (acc[i] + chain[i][1]) + (chain[i][2] + chain[i][3]);
     }
-    if constexpr (KS > 1) {
-        __syncthreads();
-        Acc* part = reinterpret_cast<Acc*>(thin_stage<Z::BYTES, 0>());
-        static_assert((KS - 1) * Z::WN * FM * 64 * 16 <= Z::BYTES, "partial sums fit a stage");
-        if (ks > 0) {
+    __syncthreads();
+    Acc* part = reinterpret_cast<Acc*>(thin_stage<Z::BYTES, 0>());
+    static_assert((TWaves - 1) * FM * 64 * 16 <= Z::BYTES, "partial sums fit a stage");
+    if (w > 0) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) part[(((ks - 1) * Z::WN + wn) * FM + i) * 64 + lane] = acc[i];
-        }
-        __syncthreads();
-        if (ks > 0) return;
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int q = 1; q < KS; ++q) acc[i] += part[(((q - 1) * Z::WN + wn) * FM + i) * 64 + lane];
+        for (int i = 0; i < FM; ++i) part[((w - 1) * FM + i) * 64 + lane] = acc[i];
     }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int q = 1; q < TWaves; ++q) acc[i] += part[((q - 1) * FM + i) * 64 + lane];
     const Out out{a};
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -189,48 +178,51 @@ __global__ __launch_bounds__(256) void ffn_thin(FfnArgs a, int tiles_m) {
             Acc u;
 #pragma unroll
             for (int q = 0; q < 4; ++q) u[q] = __shfl_xor(acc[i][q], 32, kWave);
-            if (lq < 2 && row < a.m) out.pair(row, n0 + wn * 8 + 4 * lq, acc[i], u);
+            if (lq < 2 && row < a.m) out.pair(row, n0 + 4 * lq, acc[i], u);
         } else {
-            if (row < a.m) out.one(row, n0 + wn * 16 + 4 * lq, acc[i]);
+            if (row < a.m) out.one(row, n0 + 4 * lq, acc[i]);
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 32 TF tokens by 32 TF rows of W, 4 waves of 16 TF x 16 TF each, the
-// contraction in pairs of 64-byte steps, as in the paired-stage GEMM.
+// Many tokens: WM x WN waves of 16 FM tokens x 16 FN rows of W each, the
+// contraction in pairs of 64-byte steps.
 //
 // A region of LDS holds 128 bytes of every row of a tile (chunk c of row r at slot
 // c ^ (r & 7)); a load covers 8 rows. Of a pair's two steps, the second's barrier
 // frees its region for the pair NREG later, whose loads go out between the matrix
-// instructions of the next two half steps. Gated, a wave's 16 TF rows of W are half
-// gate, half up projection, so an output's two sums end in one lane.
+// instructions of the next two half steps. Gated, a wave's rows of W are half gate,
+// half up projection, so an output's two sums end in one lane.
 // ---------------------------------------------------------------------------
-template <int TF, int NREG>
+template <int WM_, int WN_, int FM_, int FN_, int NREG_>
 struct PipeShape {
-    static constexpr int BM = 32 * TF;             // tile edge
-    static constexpr int WT = 16 * TF;             // wave tile edge
-    static constexpr int OP = BM * 128;            // bytes of an operand and region
-    static constexpr int REGION = 2 * OP;
-    static constexpr int LOADS = BM / 32;          // loads of a wave, operand and pair
+    static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_, NREG = NREG_;
+    static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;   // tile: tokens, rows of W
+    static constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;  // loads of a wave and pair
+    static_assert(XI * 8 * WAVES == BM && WI * 8 * WAVES == BN, "whole loads");
+    static constexpr int LOADS = XI + WI, HALF = LOADS / 2;      // sent out in two halves
+    static constexpr int REGION = (BM + BN) * 128;
     static constexpr size_t LDS = (size_t)NREG * REGION;
+    static constexpr int BLOCKS = 160 * 1024 / LDS >= 2 ? 2 : 1;  // of a CU, at least
 };
 
 constexpr int PipeGroup = 4;  // tile-rows of a group: neighbours in time share W through L2
 
-template <class Out, int TF, int NREG>
-__global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(FfnArgs a) {
+template <class Out, class Z>
+__global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe(FfnArgs a) {
     using E = typename Out::E;
     using Acc = typename AccOf<E>::type;
-    using Z = PipeShape<TF, NREG>;
     constexpr bool G = Out::kGated;
-    constexpr int BM = Z::BM, WT = Z::WT, HF = TF / 2, LD = Z::LOADS, LPP = 2 * LD;
-    constexpr int WO = G ? BM / 2 : BM;                      // outputs of a tile
-    constexpr int MPR = HF * TF / LD;                        // matrix instructions between loads
+    constexpr int BM = Z::BM, BN = Z::BN, FM = Z::FM, FN = Z::FN, HF = FM / 2, NREG = Z::NREG;
+    constexpr int TM = 16 * FM, TN = 16 * FN;        // wave tile
+    constexpr int WO = G ? BN / 2 : BN;              // outputs of a tile
+    constexpr int LPP = Z::LOADS, LA = Z::HALF, LB = LPP - LA;
     extern __shared__ __attribute__((aligned(1024))) char pipe_lds[];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = w >> 1, wn = w & 1, lr = lane & 15, lq = lane >> 4;
+    const int wm = w / Z::WN, wn = w % Z::WN, lr = lane & 15, lq = lane >> 4;
 
     // Groups of tile-rows, column by column inside a group, a contiguous run on each XCD.
     const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + WO - 1) / WO, tiles = tiles_m * tiles_n;
@@ -246,67 +238,69 @@ __global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(Ffn
     const int chunks = (int)(bytes / 16);
     const int pairs = ((chunks + 7) / 8 + NREG - 1) / NREG * NREG;
     const int ldx = (int)a.ldx, ldw = (int)a.ldw;
-    // This wave loads rows w BM / 4 .. of both operands; gated, waves 0 and 2 the
-    // gate's rows of wave columns 0 and 1, waves 1 and 3 the up projection's.
-    constexpr int WL = BM / 4;
-    const int64_t xat = m0 + w * WL, wat = G ? n0 + (w >> 1) * WL : n0 + w * WL;
-    const int64_t xrows = a.m - xat < WL ? a.m - xat : WL, wrows = a.n - wat < WL ? a.n - wat : WL;
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, xrows > 0 ? xat : 0, a.ldx, xrows, bytes);
-    const __amdgpu_buffer_rsrc_t rw =
-        rows_rsrc(a.w, wrows > 0 ? wat + (G && (w & 1) ? a.n : 0) : 0, a.ldw, wrows, bytes);
+    const int64_t xrows = a.m - m0 < BM ? a.m - m0 : BM, wrows = a.n - n0 < WO ? a.n - n0 : WO;
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, m0, a.ldx, xrows, bytes);
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w, n0, a.ldw, wrows, bytes);
+    const __amdgpu_buffer_rsrc_t ru = rows_rsrc(a.w, n0 + (G ? a.n : 0), a.ldw, wrows, bytes);
     const int dch = (lane & 7) ^ (lane >> 3);
     const int vox = (lane >> 3) * ldx + dch * 16, vow = (lane >> 3) * ldw + dch * 16;
 
-    // Load q (operand q % 2, its load q / 2) of pair p into region R.
+    // Load q of pair p into region R: rows of x first, then of W.
     auto dma = [&](auto R_, int p, auto Q_) {
-        constexpr int R = decltype(R_)::value, q = decltype(Q_)::value, j = q / 2;
+        constexpr int R = decltype(R_)::value, q = decltype(Q_)::value;
         const bool live = p * 8 + dch < chunks;
-        char* at = pipe_lds + R * Z::REGION + (q % 2) * Z::OP + (w * WL + j * 8) * 128;
-        if constexpr (q % 2 == 0)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MM_LDS(at), 16, live ? (uint32_t)vox : kPastEnd,
-                                                     j * 8 * ldx + p * 128, 0, 0);
-        else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, MM_LDS(at), 16, live ? (uint32_t)vow : kPastEnd,
-                                                     j * 8 * ldw + p * 128, 0, 0);
+        char* region = pipe_lds + R * Z::REGION;
+        if constexpr (q < Z::XI) {
+            const int row = (w * Z::XI + q) * 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MM_LDS(region + row * 128), 16, live ? (uint32_t)vox : kPastEnd,
+                                                     row * ldx + p * 128, 0, 0);
+        } else {
+            const int row = (w * Z::WI + q - Z::XI) * 8;
+            const bool up = G && row % TN >= TN / 2;
+            const int col = G ? row / TN * (TN / 2) + row % (TN / 2) : row;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : rw, MM_LDS(region + (BM + row) * 128), 16,
+                                                     live ? (uint32_t)vow : kPastEnd, col * ldw + p * 128, 0, 0);
+        }
     };
-    Acc acc[TF][TF];
+    Acc acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < TF; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < TF; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+        for (int j = 0; j < FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
     const int f0 = lr * 128 + ((lq ^ (lr & 7)) << 4), f1 = lr * 128 + (((4 + lq) ^ (lr & 7)) << 4);
     // Step S (region S / 2, half S % 2): x fragments of half hh of the wave's rows, all of W's.
     auto rdx = [&](auto S_, int hh, u32x4 (&f)[HF]) {
         constexpr int s = decltype(S_)::value;
-        const char* p = pipe_lds + (s / 2) * Z::REGION + (wm * WT + hh * (WT / 2)) * 128 + (s % 2 ? f1 : f0);
+        const char* p = pipe_lds + (s / 2) * Z::REGION + (wm * TM + hh * (TM / 2)) * 128 + (s % 2 ? f1 : f0);
 #pragma unroll
         for (int i = 0; i < HF; ++i) f[i] = *reinterpret_cast<const u32x4*>(p + i * 16 * 128);
     };
-    auto rdw = [&](auto S_, u32x4 (&f)[TF]) {
+    auto rdw = [&](auto S_, u32x4 (&f)[FN]) {
         constexpr int s = decltype(S_)::value;
-        const char* p = pipe_lds + (s / 2) * Z::REGION + Z::OP + wn * WT * 128 + (s % 2 ? f1 : f0);
+        const char* p = pipe_lds + (s / 2) * Z::REGION + (BM + wn * TN) * 128 + (s % 2 ? f1 : f0);
 #pragma unroll
-        for (int j = 0; j < TF; ++j) f[j] = *reinterpret_cast<const u32x4*>(p + j * 16 * 128);
+        for (int j = 0; j < FN; ++j) f[j] = *reinterpret_cast<const u32x4*>(p + j * 16 * 128);
     };
-    auto mma = [&](int hh, const u32x4 (&fx)[HF], const u32x4 (&fw)[TF]) {
+    auto mma = [&](int hh, const u32x4 (&fx)[HF], const u32x4 (&fw)[FN]) {
 #pragma unroll
         for (int i = 0; i < HF; ++i)
 #pragma unroll
-            for (int j = 0; j < TF; ++j) acc[hh * HF + i][j] = step_mma<E>(fw[j], fx[i], acc[hh * HF + i][j]);
+            for (int j = 0; j < FN; ++j) acc[hh * HF + i][j] = step_mma<E>(fw[j], fx[i], acc[hh * HF + i][j]);
     };
-    // Fragment reads first, then a load after every MPR matrix instructions.
-    auto weave = [&](auto READS) {
+    // Fragment reads first, then the loads spread over the matrix instructions.
+    auto weave = [&](auto READS, auto LOADS_) {
+        constexpr int n = decltype(LOADS_)::value, all = HF * FN;
         __builtin_amdgcn_sched_group_barrier(0x100, decltype(READS)::value, 0);
-#pragma unroll
-        for (int q = 0; q < LD; ++q) {
-            __builtin_amdgcn_sched_group_barrier(0x008, MPR, 0);
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        }
+        ffn_for<(n > 0 ? n : 1)>([&](auto Q_) {
+            constexpr int q = decltype(Q_)::value, d = n > 0 ? n : 1;
+            __builtin_amdgcn_sched_group_barrier(0x008, all * (q + 1) / d - all * q / d, 0);
+            if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        });
         __builtin_amdgcn_sched_barrier(0);
     };
-    u32x4 x0[HF], x1[HF], w0[TF], w1[TF];
+    u32x4 x0[HF], x1[HF], w0[FN], w1[FN];
     // Both steps of pair p, in region R. The first half of step 0 sends out the
-    // second half of pair p + NREG - 1, the second half of step 1 the first half of
+    // rest of pair p + NREG - 1, the second half of step 1 the first loads of
     // pair p + NREG.
     auto pair = [&](auto R_, int p) {
         constexpr int R = decltype(R_)::value, RP = (R + NREG - 1) % NREG, RN = (R + 1) % NREG;
@@ -314,34 +308,30 @@ __global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(Ffn
         using S1 = std::integral_constant<int, 2 * R + 1>;
         using SN = std::integral_constant<int, 2 * RN>;
         rdx(S0{}, 1, x1);
-        ffn_for<LD>([&](auto Q_) {
-            dma(std::integral_constant<int, RP>{}, p + NREG - 1, std::integral_constant<int, LD + decltype(Q_)::value>{});
+        ffn_for<LB>([&](auto Q_) {
+            dma(std::integral_constant<int, RP>{}, p + NREG - 1, std::integral_constant<int, LA + decltype(Q_)::value>{});
         });
         mma(0, x0, w0);
-        weave(std::integral_constant<int, HF>{});
+        weave(std::integral_constant<int, HF>{}, std::integral_constant<int, LB>{});
         rdx(S1{}, 0, x0);
         rdw(S1{}, w1);
         mma(1, x1, w0);
-        __builtin_amdgcn_sched_group_barrier(0x100, HF + TF, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, HF * TF, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        weave(std::integral_constant<int, HF + FN>{}, std::integral_constant<int, 0>{});
         rdx(S1{}, 1, x1);
         mma(0, x0, w1);
-        __builtin_amdgcn_sched_group_barrier(0x100, HF, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, HF * TF, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        weave(std::integral_constant<int, HF>{}, std::integral_constant<int, 0>{});
         __builtin_amdgcn_s_waitcnt(ffn_wait((NREG - 2) * LPP));  // pair p + 1 has landed
         __builtin_amdgcn_s_barrier();                            // region R has been read
         rdx(SN{}, 0, x0);
         rdw(SN{}, w0);
-        ffn_for<LD>([&](auto Q_) { dma(R_, p + NREG, Q_); });
+        ffn_for<LA>([&](auto Q_) { dma(R_, p + NREG, Q_); });
         mma(1, x1, w1);
-        weave(std::integral_constant<int, HF + TF>{});
+        weave(std::integral_constant<int, HF + FN>{}, std::integral_constant<int, LA>{});
     };
-    // Pairs 0 .. NREG - 2 whole, and the first half of the next.
+    // Pairs 0 .. NREG - 2 whole, and the first loads of the next.
     ffn_for<NREG - 1>([&](auto R_) { ffn_for<LPP>([&](auto Q_) { dma(R_, decltype(R_)::value, Q_); }); });
-    ffn_for<LD>([&](auto Q_) { dma(std::integral_constant<int, NREG - 1>{}, NREG - 1, Q_); });
-    __builtin_amdgcn_s_waitcnt(ffn_wait((NREG - 2) * LPP + LD));
+    ffn_for<LA>([&](auto Q_) { dma(std::integral_constant<int, NREG - 1>{}, NREG - 1, Q_); });
+    __builtin_amdgcn_s_waitcnt(ffn_wait((NREG - 2) * LPP + LA));
     __builtin_amdgcn_s_barrier();
     rdx(std::integral_constant<int, 0>{}, 0, x0);
     rdw(std::integral_constant<int, 0>{}, w0);
@@ -350,16 +340,16 @@ __global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(Ffn
 
     const Out out{a};
 #pragma unroll
-    for (int i = 0; i < TF; ++i) {
-        const int64_t row = m0 + wm * WT + i * 16 + lr;
+    for (int i = 0; i < FM; ++i) {
+        const int64_t row = m0 + wm * TM + i * 16 + lr;
         if (row >= a.m) continue;
         if constexpr (G) {
 #pragma unroll
-            for (int j = 0; j < HF; ++j)
-                out.pair(row, n0 + wn * (WT / 2) + j * 16 + 4 * lq, acc[i][j], acc[i][j + HF]);
+            for (int j = 0; j < FN / 2; ++j)
+                out.pair(row, n0 + wn * (TN / 2) + j * 16 + 4 * lq, acc[i][j], acc[i][j + FN / 2]);
         } else {
 #pragma unroll
-            for (int j = 0; j < TF; ++j) out.one(row, n0 + wn * WT + j * 16 + 4 * lq, acc[i][j]);
+            for (int j = 0; j < FN; ++j) out.one(row, n0 + wn * TN + j * 16 + 4 * lq, acc[i][j]);
         }
     }
 }
@@ -372,68 +362,83 @@ __global__ __launch_bounds__(256, TF == 8 || NREG > 2 ? 1 : 2) void ffn_pipe(Ffn
 inline bool ffn_chunked(const FfnArgs& a, int es) {
     const auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     return al16(a.x) && al16(a.w) && a.ldx % 16 == 0 && a.ldw % 16 == 0 && a.k * es % 16 == 0 &&
-           a.ldx < (1 << 24) && a.ldw < (1 << 24);
+           a.ldx < (1 << 22) && a.ldw < (1 << 22);
 }
 
-template <class Out, int FM, int KS>
+template <class Out, int FM>
 hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
-    using Z = ThinShape<FM, KS>;
-    constexpr int WO = Out::kGated ? Z::WR / 2 : Z::WR;
-    int tiles_m = (int)((a.m + Z::XR - 1) / Z::XR);
+    constexpr int XR = ThinShape<FM>::XR, WO = Out::kGated ? TRows / 2 : TRows;
+    int tiles_m = (int)((a.m + XR - 1) / XR);
     const int64_t tiles = (int64_t)tiles_m * ((a.n + WO - 1) / WO);
     void* args[] = {const_cast<FfnArgs*>(&a), &tiles_m};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_thin<Out, FM, KS>),
-                           dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), args, 0, s);
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_thin<Out, FM>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                           dim3(64 * TWaves), args, 0, s);
 }
 
-template <class Out, int TF, int NREG>
+template <class Out, class Z>
 hipError_t run_ffn_pipe(const FfnArgs& a, hipStream_t s) {
-    using Z = PipeShape<TF, NREG>;
-    constexpr int WO = Out::kGated ? Z::BM / 2 : Z::BM;
+    constexpr int WO = Out::kGated ? Z::BN / 2 : Z::BN;
     const int64_t tiles = (a.m + Z::BM - 1) / Z::BM * ((a.n + WO - 1) / WO);
     void* args[] = {const_cast<FfnArgs*>(&a)};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe<Out, TF, NREG>),
-                           dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), args, Z::LDS, s);
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe<Out, Z>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                           dim3(Z::THREADS), args, Z::LDS, s);
 }
 
-template <class Out>
-hipError_t run_ffn_thin(const FfnArgs& a, int fm, int ks, hipStream_t s) {
-#define MM_THIN(F, K) \
-    if (fm == F && ks == K) return run_ffn_thin<Out, F, K>(a, s);
-    MM_THIN(1, 1) MM_THIN(2, 1) MM_THIN(3, 1) MM_THIN(4, 1)
-    MM_THIN(1, 2) MM_THIN(2, 2) MM_THIN(3, 2) MM_THIN(4, 2)
-    MM_THIN(1, 4) MM_THIN(2, 4) MM_THIN(3, 4) MM_THIN(4, 4)
-#undef MM_THIN
-    return hipErrorInvalidValue;
+// The pipelined forms: tokens and rows of W of a tile, tiles at a time on the 256
+// CUs, and what a round of them costs in us, for each 128 bytes of k and at its
+// start. From 150 products of 1 to 8192 tokens in bf16 and codes, each in every form;
+// the form with the lowest sum of rounds is within 3% of the fastest one in the
+// mean. Both sides of some borders (us): 48 tokens by 22016 x 4096 bf16, 64 x 128
+// tiles 44.2, 64 x 64 49.7, 128 x 128 45.5; 512 by 2816 x 2048 codes, 64 x 128 9.3,
+// 64 x 64 10.2, 128 x 128 13.2; 1024 by 22016 x 4096 bf16, 256 x 128 179, 256 x 256
+// 214; 2048 by the same, 349 and 323; 32 by 1152 x 1792 bf16, 32 x 16 6.1, 64 x 64 7.8.
+struct FfnForm {
+    int tokens, rows, at_a_time;
+    float pair_us, round_us;
+};
+constexpr FfnForm kFfnForms[] = {
+    {16, 16, 768, 0.183f, 2.02f},  {32, 16, 512, 0.257f, 0.60f},   {64, 64, 256, 0.300f, 1.93f},
+    {64, 128, 256, 0.320f, 2.26f}, {128, 128, 256, 0.607f, 2.15f}, {256, 128, 256, 0.956f, 3.35f},
+    {256, 256, 256, 1.593f, 7.15f},
+};
+inline int ffn_form(int64_t m, int64_t rows, int64_t bytes) {
+    const float pairs = (float)((bytes + 127) / 128);
+    int best = -1;
+    float least = 0.f;
+    for (int i = m > 16 ? 1 : 0; i < (int)(sizeof kFfnForms / sizeof *kFfnForms); ++i) {
+        const FfnForm& f = kFfnForms[i];
+        const int64_t tiles = ((m + f.tokens - 1) / f.tokens) * ((rows + f.rows - 1) / f.rows);
+        const float us = (float)((tiles + f.at_a_time - 1) / f.at_a_time) * (pairs * f.pair_us + f.round_us);
+        if ((best < 0 || us < least) && tiles < (1 << 22)) {  // (a grid holds fewer than 2^32 threads)
+            best = i;
+            least = us;
+        }
+    }
+    return best < 0 ? (int)(sizeof kFfnForms / sizeof *kFfnForms) - 1 : best;
 }
 
-// The form for a product, reported as the receipt's variant.
+// A product in the form that suits its size; the receipt's variant names it.
 template <class Out>
 hipError_t run_ffn(const FfnArgs& a, hipStream_t s, Launched* L) {
     using E = typename Out::E;
-    if constexpr (E::code != 3) {  // codes always are
-        if (!ffn_chunked(a, sizeof(typename E::store_t)) || (E::code == 0 && a.m > 64)) return run_ffn_tile<Out>(a, s);
+    constexpr int es = sizeof(typename E::store_t);
+    const bool thin_f32 = a.m <= 64;  // f32 beyond: six bf16 products instead of f32 instructions
+    if constexpr (E::code != 3) {     // codes always are
+        if (!ffn_chunked(a, es) || (E::code == 0 && !thin_f32)) return run_ffn_tile<Out>(a, s);
     }
     const int64_t rows = Out::kGated ? 2 * a.n : a.n;
-    if (a.m <= 64) {
-        const int fm = (int)((a.m + 15) / 16);
-        const int ks = rows > 64 * 255 ? 1 : rows > 32 * 255 ? 2 : 4;
-        L->variant = fm + 256 * ks;
-        return run_ffn_thin<Out>(a, fm, ks, s);
-    }
+    const int form = E::code == 0 ? (a.m > 16) : ffn_form(a.m, rows, a.k * es);
+    L->variant = kFfnForms[form].tokens + 4096 * kFfnForms[form].rows;
+    if (form == 0) return run_ffn_thin<Out, 1>(a, s);
+    if (form == 1) return run_ffn_thin<Out, 2>(a, s);
     if constexpr (E::code != 0) {
-        const int64_t big = ((a.m + 255) / 256) * ((rows + 255) / 256);
-        if (big >= 192) {
-            L->variant = 256 + 2;
-            return run_ffn_pipe<Out, 8, 2>(a, s);
+        switch (form) {
+            case 2: return run_ffn_pipe<Out, PipeShape<2, 2, 2, 2, 4>>(a, s);
+            case 3: return run_ffn_pipe<Out, PipeShape<2, 4, 2, 2, 4>>(a, s);
+            case 4: return run_ffn_pipe<Out, PipeShape<2, 4, 4, 2, 4>>(a, s);
+            case 5: return run_ffn_pipe<Out, PipeShape<4, 2, 4, 4, 3>>(a, s);
+            default: return run_ffn_pipe<Out, PipeShape<2, 4, 8, 4, 2>>(a, s);
         }
-        const int64_t mid = ((a.m + 127) / 128) * ((rows + 127) / 128);
-        if (mid > 256) {
-            L->variant = 128 + 2;
-            return run_ffn_pipe<Out, 4, 2>(a, s);
-        }
-        L->variant = 128 + 4;
-        return run_ffn_pipe<Out, 4, 4>(a, s);
     }
     return hipErrorInvalidValue;
 }

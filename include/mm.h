@@ -151,11 +151,8 @@ typedef struct {
                                  tokens of a tile (4 or 16) plus 256 times the
                                  outputs of a block; for MM_KERNEL_GATED,
                                  MM_KERNEL_I8 and a recomputing MM_KERNEL_GATED_GRAD
-                                 0 for the form that takes any alignment, 16-token
-                                 fragments (1 to 4) plus 256 times the waves that
-                                 split the contraction (1, 2 or 4) for few tokens,
-                                 tile edge (128 or 256) plus LDS regions (2 or 4)
-                                 for many; 0 for every other family */
+                                 tokens of a tile plus 4096 times its rows of w, 0 for
+                                 the form that takes any alignment; 0 for every other family */
 } mm_receipt;
 
 /* ------------------------------------------------------------------------ */
@@ -601,7 +598,7 @@ typedef enum { MM_GATE_NONE = 0, MM_GATE_SILU = 1, MM_GATE_GELU = 2 } mm_gate;
 typedef struct {
     mm_dtype dtype;          /* every tensor: f32, f16 or bf16 */
     uint32_t gate;           /* MM_GATE_SILU or MM_GATE_GELU */
-    uint32_t m, n, k;        /* tokens (below 2^31), outputs and inputs (at most 2^24) */
+    uint32_t m, n, k;        /* tokens, outputs, inputs (each at most 2^24, m*n at most 2^36) */
     uint32_t reserved;       /* 0 */
     int64_t ldx;             /* x and dx [m, k] */
     int64_t ldw;             /* w and dw [2n, k] */
@@ -657,10 +654,10 @@ mm_status mm_i8_quant(const mm_quant_params *params, mm_buf x, mm_buf q, mm_buf 
 typedef struct {
     mm_dtype dtype;          /* y: f32, f16 or bf16 */
     uint32_t gate;           /* MM_GATE_NONE, or the gated form */
-    uint32_t m, n, k;        /* tokens (below 2^31), outputs (at most 2^24), inputs
+    uint32_t m, n, k;        /* tokens, outputs (each at most 2^24, m*n at most 2^36), inputs
                                 (a multiple of 16, at most MM_I8_MAX_K) */
     uint32_t reserved;       /* 0 */
-    int64_t ldx, ldw;        /* pitches of the codes: multiples of 16, below 2^24 */
+    int64_t ldx, ldw;        /* pitches of the codes: multiples of 16, below 2^22 */
     int64_t ldy;
 } mm_i8_params;
 

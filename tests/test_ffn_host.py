@@ -143,6 +143,7 @@ def test_gradient_in_place_of_the_pre_activations(lib):
     *[(n, "dtype", 3, UNSUPPORTED) for n in CALLS],
     *[(n, "reserved", 1, INVALID) for n in CALLS],
     *[(n, "m", 1 << 31, INVALID) for n in CALLS],
+    *[(n, "m", (1 << 24) + 1, INVALID) for n in CALLS if n != "quant"],
     *[(n, "n", (1 << 24) + 1, INVALID) for n in CALLS if n != "quant"],
     *[(n, "ldx", v, INVALID) for n in CALLS for v in (-48, 1, 1 << 62)],
     ("gated", "gate", 0, INVALID), ("gated", "gate", 3, INVALID), ("gated_grad", "gate", 0, INVALID),
@@ -154,6 +155,12 @@ def test_gradient_in_place_of_the_pre_activations(lib):
 def test_bad_fields(name, field, value, status):
     fn, p, bufs, _, _ = CALLS[name]
     _fails(status, fn, _copy(p, **{field: value}), *[_at(i) for i in range(len(bufs))])
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n != "quant"])
+def test_largest_outputs(name):
+    fn, p, bufs, _, _ = CALLS[name]
+    _fails(INVALID, fn, _copy(p, m=(1 << 18) + 1, n=1 << 18), *[_at(i, BIG) for i in range(len(bufs))])
 
 
 @pytest.mark.parametrize("name", CALLS)
