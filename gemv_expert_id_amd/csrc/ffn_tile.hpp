@@ -9,22 +9,20 @@
 // accumulator of their own, so the small ones are not rounded away. 16-bit operands
 // are one part.
 //
-// Block = 4 waves (2 x 2), tile 32 F x 32 F, 32 elements of k at a step, staged
-// through registers: the next step is fetched before the current one is multiplied.
-// A contiguous operand is fetched in 16-byte pieces at any address, a strided one in
-// blocks of F k-rows by 4 columns, which registers transpose on the way to LDS.
-// Rows and columns past the end repeat the last one (their sums are not stored);
-// elements of k past the end are zeros in both operands. LDS rows are 80 bytes
-// apart: the 16 rows that a fragment read covers start in distinct banks.
+// A group of 4 waves (2 x 2) computes a tile of 32 FM x 32 FN, each wave SUB steps of
+// 32 elements of k an iteration; a block has KS groups, which take different steps
+// and are joined through LDS at the end (few tiles: more loads in flight). Operands
+// are staged through registers: the next iteration's are fetched before the current
+// one is multiplied, in 16-byte pieces at any address, along k or along the rows. LDS
+// keeps a contiguous operand by rows, padded by 16 bytes so that the 16 rows of a
+// fragment read start in distinct banks, and a strided one by k, as it comes; its
+// fragments take two transposing reads each. Rows past the end repeat the last one
+// (their sums are not stored); elements of k past the end are zeros in both operands.
 #pragma once
 
 #include "ffn.hpp"
 
 namespace mmk {
-
-constexpr int AStep = 32;     // elements of k at a step
-constexpr int APitch = 80;    // bytes between LDS rows (64 of them used)
-constexpr int AThreads = 256;
 
 template <class S, int N>
 struct __attribute__((packed, aligned(sizeof(S)))) Pack {
@@ -63,103 +61,118 @@ __device__ __forceinline__ void parts_of(const typename T::store_t (&e)[N], uint
     }
 }
 
-// One operand's share of a thread: R = 32 F rows by 32 elements of k.
-template <class T, int F, bool KC>
+// Transposing LDS read (ds_read_b64_tr_b16): in each group of 16 lanes, lane j gets
+// element j % 4 of the four 16-bit elements at the addresses of lanes j / 4, j / 4 + 4,
+// j / 4 + 8 and j / 4 + 12.
+__device__ __forceinline__ u32x2 read_transposed(const char* p) {
+    typedef short v4i16 __attribute__((ext_vector_type(4)));
+    const v4i16 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4i16*)(const_cast<char*>(p)));
+    return __builtin_bit_cast(u32x2, v);
+}
+
+// One operand's share of a thread: R rows by KT elements of k, spread over NT threads.
+template <class T, int R, int KT, int NT, bool KC>
 struct TileOperand {
     using S = typename T::store_t;
-    static constexpr int R = 32 * F;
-    static constexpr int V = KC ? T::Elems16 : 4;              // elements of a load
-    static constexpr int N = KC ? R * AStep / V / AThreads : F;  // loads
-    static constexpr int PLANE = R * APitch;                   // bytes of one part in LDS
+    static constexpr int P = kParts<T>;
+    static constexpr int V = T::Elems16;                     // elements of a piece
+    static constexpr int PITCH = KC ? KT * 2 + 16 : R * 2;   // bytes between LDS rows (of k, strided)
+    static constexpr int PLANE = KC ? R * PITCH : KT * PITCH;  // bytes of one part
+    static constexpr int C = KC ? KT / V : R / V;            // pieces of a row
+    static constexpr int ALL = R * KT / V;                   // pieces
+    static constexpr int N = ALL > NT ? ALL / NT : 1;        // of a thread (of the first ALL, if fewer)
+    static_assert(N * NT == ALL || N == 1, "whole pieces");
     Pack<S, V> v[N];
-    const S* p[KC ? N : 4];  // row starts; or the four columns (p[0] alone while they are neighbours)
+    const S* p[KC ? N : V];  // row starts; or the columns (p[0] alone while they are neighbours)
     int64_t ld;
     bool split;  // strided: the columns are fetched one by one
 
+    static __device__ __forceinline__ int piece(int i) { return (int)threadIdx.x + i * NT; }
+    // Strided: 16-byte chunk swizzle of k-row r, by which the 16 k-rows of a
+    // transposing read cover all banks twice.
+    static __device__ __forceinline__ int swizzle(int r) {
+        if constexpr (R >= 128) return 2 * ((r & 3) + 4 * ((r >> 3) & 1));
+        else if constexpr (R == 64) return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1));
+        else return 2 * ((r >> 3) & 1);
+    }
     // `row(r)`: the operand's row that tile row r stands for, already inside it.
     template <class Row>
     __device__ __forceinline__ void init(const void* base, int64_t pitch, Row row) {
         const S* s = static_cast<const S*>(base);
         ld = pitch;
-        const int tid = threadIdx.x;
         if constexpr (KC) {
-            constexpr int C = AStep / V;  // pieces of a row
 #pragma unroll
-            for (int i = 0; i < N; ++i) p[i] = s + row((tid + i * AThreads) / C) * ld + (tid % C) * V;
+            for (int i = 0; i < N; ++i) p[i] = s + row(piece(i) / C) * ld + (piece(i) % C) * V;
         } else {
-            const int c = tid % (R / 4) * 4, k0 = tid / (R / 4) * F;
+            static_assert(NT % C == 0, "a thread's pieces share their columns");
+            const int64_t first = row(piece(0) % C * V);
+            split = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = s + k0 * ld + row(c + i);
-            split = p[3] != p[0] + 3;
+            for (int e = 0; e < V; ++e) {
+                const int64_t r = row(piece(0) % C * V + e);
+                split |= r != first + e;
+                p[e] = s + r;
+            }
         }
     }
-    // Elements k0 .. k0 + 31; TAIL: those from K on are zeros.
+    // Elements k0 .. k0 + KT - 1; TAIL: those from K on are zeros.
     template <bool TAIL>
     __device__ __forceinline__ void fetch(int64_t k0, int64_t K) {
-        const int tid = threadIdx.x;
-        if constexpr (KC) {
-            const int64_t left = K - k0 - (tid % (AStep / V)) * V;
+        if (ALL < NT && (int)threadIdx.x >= ALL) return;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N; ++i) {
+            if constexpr (KC) {
+                const int64_t left = K - k0 - piece(i) % C * V;
                 if (!TAIL || left >= V) {
                     v[i] = *reinterpret_cast<const Pack<S, V>*>(p[i] + k0);
                 } else {
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[i].v[e] = e < left ? p[i][k0 + e] : S(0);
                 }
-            }
-        } else {
-            const int64_t left = K - k0 - tid / (R / 4) * F;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (TAIL && i >= left) {
+            } else {
+                const int64_t at = k0 + piece(i) / C;
+                if (TAIL && at >= K) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) v[i].v[e] = S(0);
                 } else if (!split) {
-                    v[i] = *reinterpret_cast<const Pack<S, V>*>(p[0] + (k0 + i) * ld);
+                    v[i] = *reinterpret_cast<const Pack<S, V>*>(p[0] + at * ld);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) v[i].v[e] = p[e][(k0 + i) * ld];
+                    for (int e = 0; e < V; ++e) v[i].v[e] = p[e][at * ld];
                 }
             }
         }
     }
     __device__ __forceinline__ void store(char* lds) const {
-        const int tid = threadIdx.x;
-        constexpr int P = kParts<T>;
+        if (ALL < NT && (int)threadIdx.x >= ALL) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t w[P][V / 2];
+            parts_of<T, V>(v[i].v, w);
+            const int r = piece(i) / C, at = piece(i) % C * V * 2;
+            char* to = lds + r * PITCH + (KC ? at : (((at >> 4) ^ swizzle(r)) << 4) + (at & 15));
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                if constexpr (V == 8)
+                    *reinterpret_cast<u32x4*>(to + q * PLANE) = u32x4{w[q][0], w[q][1], w[q][2], w[q][3]};
+                else
+                    *reinterpret_cast<u32x2*>(to + q * PLANE) = u32x2{w[q][0], w[q][1]};
+            }
+        }
+    }
+    // The lane's eight elements of rows row0 .. row0 + 15 in step `step` (32 of k) of a
+    // plane: row lane % 16, elements 8 (lane / 16) of the step on.
+    static __device__ __forceinline__ u32x4 frag(const char* plane, int row0, int step) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
         if constexpr (KC) {
-            constexpr int C = AStep / V;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                uint32_t w[P][V / 2];
-                parts_of<T, V>(v[i].v, w);
-                char* at = lds + (tid + i * AThreads) / C * APitch + tid % C * V * 2;
-#pragma unroll
-                for (int q = 0; q < P; ++q) {
-                    if constexpr (V == 8)
-                        *reinterpret_cast<u32x4*>(at + q * PLANE) = u32x4{w[q][0], w[q][1], w[q][2], w[q][3]};
-                    else
-                        *reinterpret_cast<u32x2*>(at + q * PLANE) = u32x2{w[q][0], w[q][1]};
-                }
-            }
+            return *reinterpret_cast<const u32x4*>(plane + (row0 + s) * PITCH + step * 64 + g * 16);
         } else {
-            const int c = tid % (R / 4) * 4, k0 = tid / (R / 4) * F;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                S col[F];
-#pragma unroll
-                for (int i = 0; i < F; ++i) col[i] = v[i].v[e];
-                uint32_t w[P][F / 2];
-                parts_of<T, F>(col, w);
-                char* at = lds + (c + e) * APitch + k0 * 2;
-#pragma unroll
-                for (int q = 0; q < P; ++q) {
-                    if constexpr (F == 4)
-                        *reinterpret_cast<u32x2*>(at + q * PLANE) = u32x2{w[q][0], w[q][1]};
-                    else
-                        *reinterpret_cast<uint32_t*>(at + q * PLANE) = w[q][0];
-                }
-            }
+            // Lane s of group g addresses k-rows 8 g + s / 4 and + 4, columns 4 (s % 4) on.
+            const int r0 = step * 32 + 8 * g + (s >> 2), r1 = r0 + 4, c = row0 / 8 + ((s & 3) >> 1);
+            const u32x2 lo = read_transposed(plane + r0 * PITCH + ((c ^ swizzle(r0)) << 4) + 8 * (s & 1));
+            const u32x2 hi = read_transposed(plane + r1 * PITCH + ((c ^ swizzle(r1)) << 4) + 8 * (s & 1));
+            return u32x4{lo[0], lo[1], hi[0], hi[1]};
         }
     }
 };
@@ -178,38 +191,47 @@ struct PlainOut {
     }
 };
 
-template <class Out, int F, bool AK, bool BK>
-__global__ __launch_bounds__(AThreads, 2) void ffn_tile(TileArgs t, FfnArgs o) {
+template <class T, int FM_, int FN_, int SUB_, int KS_>
+struct TileShape {
+    static constexpr int FM = FM_, FN = FN_, SUB = SUB_, KS = KS_;
+    static constexpr int BM = 32 * FM, BN = 32 * FN, KT = 32 * SUB * KS, THREADS = 256 * KS;
+    static constexpr int BYTES = kParts<T> * (BM + BN) * (KT * 2 + 16);  // one LDS buffer, at most
+    // Two buffers where a CU still holds two blocks (one, where the groups split k).
+    static constexpr int BUF = 2 * BYTES * (KS > 1 ? 1 : 2) <= 160 * 1024 ? 2 : 1;
+};
+
+template <class Out, class Z, bool AK, bool BK>
+__global__ __launch_bounds__(Z::THREADS, Z::KS > 1 ? Z::KS : 2) void ffn_tile(TileArgs t, FfnArgs o) {
     using T = typename Out::E;
     using M = MmaOf<T>;
     constexpr bool G = Out::kGated;
-    constexpr int P = kParts<T>, R = 32 * F, WT = 16 * F;
-    constexpr int RO = G ? R / 2 : R;            // outputs of a tile
-    constexpr int BUF = P == 3 && F == 4 ? 1 : 2;  // LDS buffers: one lets two blocks share a CU
-    using OA = TileOperand<T, F, AK>;
-    using OB = TileOperand<T, F, BK>;
-    __shared__ __attribute__((aligned(16))) char lds[BUF][P * (OA::PLANE + OB::PLANE)];
+    constexpr int P = kParts<T>, FM = Z::FM, FN = Z::FN, TM = 16 * FM, TN = 16 * FN, KT = Z::KT, BUF = Z::BUF;
+    constexpr int RO = G ? Z::BN / 2 : Z::BN;  // outputs of a tile
+    using OA = TileOperand<T, Z::BM, KT, Z::THREADS, AK>;
+    using OB = TileOperand<T, Z::BN, KT, Z::THREADS, BK>;
+    static_assert(P * (OA::PLANE + OB::PLANE) <= Z::BYTES, "LDS buffer");
+    extern __shared__ __attribute__((aligned(16))) char tile_lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave >> 1, wn = wave & 1, lr = lane & 15, lq = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x / t.tiles_n) * R, n0 = (int64_t)(blockIdx.x % t.tiles_n) * RO;
+    const int kg = wave >> 2, wm = (wave >> 1) & 1, wn = wave & 1, lr = lane & 15, lq = lane >> 4;
+    const int64_t m0 = (int64_t)(blockIdx.x / t.tiles_n) * Z::BM, n0 = (int64_t)(blockIdx.x % t.tiles_n) * RO;
     OA a;
     OB b;
     a.init(t.a, t.lda, [&](int r) { return m0 + r < t.m ? m0 + r : t.m - 1; });
     b.init(t.b, t.ldb, [&](int r) {
         // Gated: each wave column's rows are half gate, half up projection.
-        const int64_t col = n0 + (G ? (r / WT) * (WT / 2) + r % (WT / 2) : r);
-        return (col < t.n ? col : t.n - 1) + (G && r % WT >= WT / 2 ? t.n : 0);
+        const int64_t col = n0 + (G ? (r / TN) * (TN / 2) + r % (TN / 2) : r);
+        return (col < t.n ? col : t.n - 1) + (G && r % TN >= TN / 2 ? t.n : 0);
     });
-    f32x4 acc[F][F], low[P == 3 ? F : 1][P == 3 ? F : 1];
+    f32x4 acc[FM][FN], low[P == 3 ? FM : 1][P == 3 ? FN : 1];
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
+        for (int j = 0; j < FN; ++j) {
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
             if constexpr (P == 3) low[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     auto fetch = [&](int64_t k0) {
-        if (k0 + AStep <= t.k) {
+        if (k0 + KT <= t.k) {
             a.template fetch<false>(k0, t.k);
             b.template fetch<false>(k0, t.k);
         } else {
@@ -218,79 +240,108 @@ __global__ __launch_bounds__(AThreads, 2) void ffn_tile(TileArgs t, FfnArgs o) {
         }
     };
     auto store = [&](int buf) {
-        a.store(lds[buf]);
-        b.store(lds[buf] + P * OA::PLANE);
-    };
-    auto frag = [&](const char* plane, int row0) {
-        return *reinterpret_cast<const u32x4*>(plane + (row0 + lr) * APitch + lq * 16);
+        a.store(tile_lds + buf * Z::BYTES);
+        b.store(tile_lds + buf * Z::BYTES + P * OA::PLANE);
     };
     fetch(0);
     store(0);
     __syncthreads();
-    for (int64_t k0 = 0; k0 < t.k; k0 += AStep) {
-        const int cur = BUF == 2 ? (int)((k0 / AStep) & 1) : 0;
-        const bool more = k0 + AStep < t.k;
-        if (more) fetch(k0 + AStep);
-        const char* la = lds[cur];
-        const char* lb = lds[cur] + P * OA::PLANE;
-        u32x4 fa[P][F];
+    for (int64_t k0 = 0; k0 < t.k; k0 += KT) {
+        const int cur = BUF == 2 ? (int)((k0 / KT) & 1) : 0;
+        const bool more = k0 + KT < t.k;
+        if (more) fetch(k0 + KT);
 #pragma unroll
-        for (int q = 0; q < P; ++q)
+        for (int s = 0; s < Z::SUB; ++s) {
+            const char* la = tile_lds + cur * Z::BYTES;
+            const char* lb = la + P * OA::PLANE;
+            const int step = kg * Z::SUB + s;
+            u32x4 fa[P][FM];
 #pragma unroll
-            for (int i = 0; i < F; ++i) fa[q][i] = frag(la + q * OA::PLANE, wm * WT + i * 16);
+            for (int q = 0; q < P; ++q)
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-            u32x4 fb[P];
+                for (int i = 0; i < FM; ++i) fa[q][i] = OA::frag(la + q * OA::PLANE, wm * TM + i * 16, step);
 #pragma unroll
-            for (int q = 0; q < P; ++q) fb[q] = frag(lb + q * OB::PLANE, wn * WT + j * 16);
+            for (int j = 0; j < FN; ++j) {
+                u32x4 fb[P];
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                if constexpr (P == 3) {
-                    low[i][j] = step_mma<M>(fb[2], fa[0][i], low[i][j]);
-                    low[i][j] = step_mma<M>(fb[0], fa[2][i], low[i][j]);
-                    low[i][j] = step_mma<M>(fb[1], fa[1][i], low[i][j]);
-                    low[i][j] = step_mma<M>(fb[1], fa[0][i], low[i][j]);
-                    low[i][j] = step_mma<M>(fb[0], fa[1][i], low[i][j]);
+                for (int q = 0; q < P; ++q) fb[q] = OB::frag(lb + q * OB::PLANE, wn * TN + j * 16, step);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    if constexpr (P == 3) {
+                        low[i][j] = step_mma<M>(fb[2], fa[0][i], low[i][j]);
+                        low[i][j] = step_mma<M>(fb[0], fa[2][i], low[i][j]);
+                        low[i][j] = step_mma<M>(fb[1], fa[1][i], low[i][j]);
+                        low[i][j] = step_mma<M>(fb[1], fa[0][i], low[i][j]);
+                        low[i][j] = step_mma<M>(fb[0], fa[1][i], low[i][j]);
+                    }
+                    acc[i][j] = step_mma<M>(fb[0], fa[0][i], acc[i][j]);
                 }
-                acc[i][j] = step_mma<M>(fb[0], fa[0][i], acc[i][j]);
             }
         }
         if (BUF == 1) __syncthreads();  // read by every wave
         if (more) store(BUF == 2 ? cur ^ 1 : 0);
         __syncthreads();
     }
+    if constexpr (P == 3) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] += low[i][j];
+    }
+    if constexpr (Z::KS > 1) {
+        f32x4* part = reinterpret_cast<f32x4*>(tile_lds);
+        static_assert((Z::KS - 1) * 256 * FM * FN * 16 <= Z::BUF * Z::BYTES, "partial sums fit");
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < FM * FN; ++i) part[((kg - 1) * FM * FN + i) * 256 + (threadIdx.x & 255)] = acc[i / FN][i % FN];
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int g = 1; g < Z::KS; ++g)
+#pragma unroll
+            for (int i = 0; i < FM * FN; ++i) acc[i / FN][i % FN] += part[((g - 1) * FM * FN + i) * 256 + threadIdx.x];
+    }
     const Out out{o};
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int64_t row = m0 + wm * WT + i * 16 + lr;
+    for (int i = 0; i < FM; ++i) {
+        const int64_t row = m0 + wm * TM + i * 16 + lr;
         if (row >= t.m) continue;
-        if constexpr (P == 3) {
-#pragma unroll
-            for (int j = 0; j < F; ++j) acc[i][j] += low[i][j];
-        }
         if constexpr (G) {
 #pragma unroll
-            for (int j = 0; j < F / 2; ++j)
-                out.pair(row, n0 + wn * (WT / 2) + j * 16 + 4 * lq, acc[i][j], acc[i][j + F / 2]);
+            for (int j = 0; j < FN / 2; ++j)
+                out.pair(row, n0 + wn * (TN / 2) + j * 16 + 4 * lq, acc[i][j], acc[i][j + FN / 2]);
         } else {
 #pragma unroll
-            for (int j = 0; j < F; ++j) out.one(row, n0 + wn * WT + j * 16 + 4 * lq, acc[i][j]);
+            for (int j = 0; j < FN; ++j) out.one(row, n0 + wn * TN + j * 16 + 4 * lq, acc[i][j]);
         }
     }
 }
 
-// 128 x 128 tiles when they give every CU two blocks, else 64 x 64.
-template <class Out, bool AK, bool BK>
-hipError_t run_ffn_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
-    const int64_t outs = Out::kGated ? 2 * t.n : t.n;
-    const bool big = ((t.m + 127) / 128) * ((outs + 127) / 128) >= 512;
-    const int64_t edge = big ? 128 : 64, ro = Out::kGated ? edge / 2 : edge;
-    t.tiles_n = (int32_t)((t.n + ro - 1) / ro);
-    const unsigned grid = (unsigned)((t.m + edge - 1) / edge * t.tiles_n);
-    const void* fn = big ? reinterpret_cast<const void*>(&ffn_tile<Out, 4, AK, BK>)
-                         : reinterpret_cast<const void*>(&ffn_tile<Out, 2, AK, BK>);
+template <class Out, class Z, bool AK, bool BK>
+hipError_t run_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
+    constexpr int RO = Out::kGated ? Z::BN / 2 : Z::BN;
+    t.tiles_n = (int32_t)((t.n + RO - 1) / RO);
+    const unsigned grid = (unsigned)((t.m + Z::BM - 1) / Z::BM * t.tiles_n);
     void* args[] = {&t, const_cast<FfnArgs*>(&o)};
-    return hipLaunchKernel(fn, dim3(grid), dim3(AThreads), args, 0, s);
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_tile<Out, Z, AK, BK>), dim3(grid), dim3(Z::THREADS), args,
+                           Z::BUF * Z::BYTES, s);
+}
+
+// 128 x 128 tiles when they give every CU two blocks, 64 x 64 below; four groups
+// over k when even those leave CUs without a tile, 32 tokens where there are no more.
+template <class Out, bool AK, bool BK>
+hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
+    using T = typename Out::E;
+    const int64_t outs = Out::kGated ? 2 * t.n : t.n;
+    const auto tiles = [&](int64_t bm, int64_t bn) { return ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn); };
+    if (tiles(128, 128) >= 512) return run_tile<Out, TileShape<T, 4, 4, kParts<T> == 3 ? 1 : 2, 1>, AK, BK>(t, o, s);
+    if constexpr (!Out::kGated) {
+        if (tiles(64, 64) <= 64) return run_tile<Out, TileShape<T, 1, 1, 1, 4>, AK, BK>(t, o, s);
+    }
+    if (t.m <= 32) return run_tile<Out, TileShape<T, 1, 2, 1, 4>, AK, BK>(t, o, s);
+    if (tiles(64, 64) <= 256) return run_tile<Out, TileShape<T, 2, 2, 1, 4>, AK, BK>(t, o, s);
+    return run_tile<Out, TileShape<T, 2, 2, kParts<T> == 3 ? 1 : 2, 1>, AK, BK>(t, o, s);
 }
 
 // The products with the rows of W, from a product's own arguments.
