@@ -41,6 +41,16 @@ __device__ __forceinline__ typename AccOf<E>::type step_mma(u32x4 w, u32x4 x, ty
     }
 }
 
+// Transposing LDS read (ds_read_b64_tr_b16): in each group of 16 lanes, lane j gets
+// element j % 4 of the four 16-bit elements at the addresses of lanes j / 4, j / 4 + 4,
+// j / 4 + 8 and j / 4 + 12.
+__device__ __forceinline__ u32x2 read_transposed(const char* p) {
+    typedef short v4i16 __attribute__((ext_vector_type(4)));
+    const v4i16 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4i16*)(const_cast<char*>(p)));
+    return __builtin_bit_cast(u32x2, v);
+}
+
 // Up to four neighbouring elements of a row: whole at an aligned address, one
 // by one at others and at the row's end.
 template <class T>

@@ -194,6 +194,12 @@ __global__ __launch_bounds__(64 * TWaves) void ffn_thin(FfnArgs a, int tiles_m) 
 // frees its region for the pair NREG later, whose loads go out between the matrix
 // instructions of the next two half steps. Gated, a wave's rows of W are half gate,
 // half up projection, so an output's two sums end in one lane.
+//
+// XK, WK = false (16-bit gradients' products): the operand is stored with the
+// contraction along its rows, element (i, p) at p * ld + i. Its region holds the
+// pair's 64 k-rows of BM (BN) elements (chunk c of k-row r at slot c ^ k_swizzle(r)),
+// fragments take two transposing reads, and the resource moves on with the pair, so
+// that no offset grows with the contraction; k-rows past the end lie outside it.
 // ---------------------------------------------------------------------------
 template <int WM_, int WN_, int FM_, int FN_, int NREG_>
 struct PipeShape {
@@ -210,7 +216,17 @@ struct PipeShape {
 
 constexpr int PipeGroup = 4;  // tile-rows of a group: neighbours in time share W through L2
 
-template <class Out, class Z>
+__device__ __forceinline__ int k_swizzle(int r) { return 2 * ((r & 3) + 4 * ((r >> 3) & 1)); }
+
+// Region R of operand OP where one is strided: arrays of their own, so that the
+// compiler sees that transposing reads of one do not meet loads into the others.
+template <int BYTES, int R, int OP>
+__device__ __forceinline__ char* pipe_region() {
+    __shared__ __attribute__((aligned(1024))) char st[BYTES];
+    return st;
+}
+
+template <class Out, class Z, bool XK = true, bool WK = true>
 __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe(FfnArgs a) {
     using E = typename Out::E;
     using Acc = typename AccOf<E>::type;
@@ -219,7 +235,7 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
     constexpr int TM = 16 * FM, TN = 16 * FN;        // wave tile
     constexpr int WO = G ? BN / 2 : BN;              // outputs of a tile
     constexpr int LPP = Z::LOADS, LA = Z::HALF, LB = LPP - LA;
-    extern __shared__ __attribute__((aligned(1024))) char pipe_lds[];
+    extern __shared__ __attribute__((aligned(1024))) char pipe_lds[];  // (where both are contiguous)
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / Z::WN, wn = w % Z::WN, lr = lane & 15, lq = lane >> 4;
@@ -234,32 +250,77 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
     const int64_t m0 = (first + t % (PipeGroup * tiles_n) % size) * BM;
     const int64_t n0 = t % (PipeGroup * tiles_n) / size * WO;
 
+    constexpr bool SPLIT = !XK || !WK;  // regions as arrays of their own
+    static_assert(!SPLIT || (!G && sizeof(typename E::store_t) == 2 && BM >= 128 && BN >= 128), "strided operands");
     const int64_t bytes = a.k * (int64_t)sizeof(typename E::store_t);
-    const int chunks = (int)(bytes / 16);
+    const int chunks = (int)((bytes + 15) / 16);  // (whole ones where an operand is contiguous)
     const int pairs = ((chunks + 7) / 8 + NREG - 1) / NREG * NREG;
     const int ldx = (int)a.ldx, ldw = (int)a.ldw;
     const int64_t xrows = a.m - m0 < BM ? a.m - m0 : BM, wrows = a.n - n0 < WO ? a.n - n0 : WO;
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, m0, a.ldx, xrows, bytes);
-    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w, n0, a.ldw, wrows, bytes);
-    const __amdgpu_buffer_rsrc_t ru = rows_rsrc(a.w, n0 + (G ? a.n : 0), a.ldw, wrows, bytes);
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, XK ? m0 : 0, a.ldx, XK ? xrows : 0, bytes);
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w, WK ? n0 : 0, a.ldw, WK ? wrows : 0, bytes);
+    const __amdgpu_buffer_rsrc_t ru = rows_rsrc(a.w, WK ? n0 + (G ? a.n : 0) : 0, a.ldw, WK ? wrows : 0, bytes);
+    // Strided: the k-rows of pair p, `rows` elements of each from `first` on. (A dword
+    // of the last one that reaches past them holds one of them: it is inside.)
+    auto pair_rsrc = [&](const void* base, int64_t first, int64_t ld, int64_t rows, int p) {
+        const int64_t left = a.k - (int64_t)p * 64, k_rows = left < 64 ? left : 64;
+        return __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(static_cast<const char*>(base) + (left > 0 ? (int64_t)p * 64 * ld : 0) + first * 2), (short)0,
+            left > 0 ? (int)((k_rows - 1) * ld + (rows * 2 + 3) / 4 * 4) : 0, 0x00020000);
+    };
+    // Contiguous: a load covers 8 rows, the lane the chunk that belongs at slot lane % 8.
     const int dch = (lane & 7) ^ (lane >> 3);
     const int vox = (lane >> 3) * ldx + dch * 16, vow = (lane >> 3) * ldw + dch * 16;
+    // Strided: a load covers 512 / B k-rows of B elements.
+    constexpr int XC = BM / 8, WC = BN / 8;  // chunks of a k-row
+    int vkx[XK ? 1 : Z::XI], vkw[WK ? 1 : Z::WI];
+    if constexpr (!XK) {
+#pragma unroll
+        for (int q = 0; q < Z::XI; ++q)
+            vkx[q] = lane / XC * ldx + (lane % XC ^ k_swizzle((w * Z::XI + q) * (64 / XC) + lane / XC)) * 16;
+    }
+    if constexpr (!WK) {
+#pragma unroll
+        for (int q = 0; q < Z::WI; ++q)
+            vkw[q] = lane / WC * ldw + (lane % WC ^ k_swizzle((w * Z::WI + q) * (64 / WC) + lane / WC)) * 16;
+    }
+    auto region_x = [&](auto R_) -> char* {
+        if constexpr (SPLIT) return pipe_region<BM * 128, decltype(R_)::value, 0>();
+        else return pipe_lds + decltype(R_)::value * Z::REGION;
+    };
+    auto region_w = [&](auto R_) -> char* {
+        if constexpr (SPLIT) return pipe_region<BN * 128, decltype(R_)::value, 1>();
+        else return pipe_lds + decltype(R_)::value * Z::REGION + BM * 128;
+    };
 
-    // Load q of pair p into region R: rows of x first, then of W.
+    // Load q of pair p into region R: x first, then W.
     auto dma = [&](auto R_, int p, auto Q_) {
-        constexpr int R = decltype(R_)::value, q = decltype(Q_)::value;
+        constexpr int q = decltype(Q_)::value;
         const bool live = p * 8 + dch < chunks;
-        char* region = pipe_lds + R * Z::REGION;
         if constexpr (q < Z::XI) {
-            const int row = (w * Z::XI + q) * 8;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MM_LDS(region + row * 128), 16, live ? (uint32_t)vox : kPastEnd,
-                                                     row * ldx + p * 128, 0, 0);
+            const int i = w * Z::XI + q;
+            if constexpr (XK) {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MM_LDS(region_x(R_) + i * 1024), 16,
+                                                         live ? (uint32_t)vox : kPastEnd, i * 8 * ldx + p * 128, 0, 0);
+            } else {
+                const __amdgpu_buffer_rsrc_t rp = pair_rsrc(a.x, m0, a.ldx, xrows, p);
+                const int at = vkx[q];
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, MM_LDS(region_x(R_) + i * 1024), 16, at,
+                                                         i * (64 / XC) * ldx, 0, 0);
+            }
         } else {
-            const int row = (w * Z::WI + q - Z::XI) * 8;
+            const int i = w * Z::WI + q - Z::XI, row = i * 8;
             const bool up = G && row % TN >= TN / 2;
             const int col = G ? row / TN * (TN / 2) + row % (TN / 2) : row;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : rw, MM_LDS(region + (BM + row) * 128), 16,
-                                                     live ? (uint32_t)vow : kPastEnd, col * ldw + p * 128, 0, 0);
+            if constexpr (WK) {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : rw, MM_LDS(region_w(R_) + i * 1024), 16,
+                                                         live ? (uint32_t)vow : kPastEnd, col * ldw + p * 128, 0, 0);
+            } else {
+                const __amdgpu_buffer_rsrc_t rp = pair_rsrc(a.w, n0, a.ldw, wrows, p);
+                const int at = vkw[q - Z::XI];
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, MM_LDS(region_w(R_) + i * 1024), 16, at,
+                                                         i * (64 / WC) * ldw, 0, 0);
+            }
         }
     };
     Acc acc[FM][FN];
@@ -268,19 +329,35 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
     const int f0 = lr * 128 + ((lq ^ (lr & 7)) << 4), f1 = lr * 128 + (((4 + lq) ^ (lr & 7)) << 4);
+    // Strided: lane s of group g addresses k-rows 8 g + s / 4 and + 4 of the step, columns
+    // 4 (s % 4) on; a fragment's columns are an exclusive or away.
+    const int kr = 8 * lq + (lr >> 2), kc = ((((lr & 3) >> 1) ^ k_swizzle(kr)) << 4) + 8 * (lr & 1);
+    auto strided = [&](const char* region, int h, int row0, int b) {
+        const char* at = region + (h * 32 + kr) * 2 * b + (kc ^ (row0 * 2));
+        const u32x2 lo = read_transposed(at), hi = read_transposed(at + 8 * b);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
     // Step S (region S / 2, half S % 2): x fragments of half hh of the wave's rows, all of W's.
     auto rdx = [&](auto S_, int hh, u32x4 (&f)[HF]) {
         constexpr int s = decltype(S_)::value;
-        const char* p = pipe_lds + (s / 2) * Z::REGION + (wm * TM + hh * (TM / 2)) * 128 + (s % 2 ? f1 : f0);
+        const char* p = region_x(std::integral_constant<int, s / 2>{});
+        const int row0 = wm * TM + hh * (TM / 2);
 #pragma unroll
-        for (int i = 0; i < HF; ++i) f[i] = *reinterpret_cast<const u32x4*>(p + i * 16 * 128);
+        for (int i = 0; i < HF; ++i) {
+            if constexpr (XK) f[i] = *reinterpret_cast<const u32x4*>(p + (row0 + i * 16) * 128 + (s % 2 ? f1 : f0));
+            else f[i] = strided(p, s % 2, row0 + i * 16, BM);
+        }
     };
     auto rdw = [&](auto S_, u32x4 (&f)[FN]) {
         constexpr int s = decltype(S_)::value;
-        const char* p = pipe_lds + (s / 2) * Z::REGION + (BM + wn * TN) * 128 + (s % 2 ? f1 : f0);
+        const char* p = region_w(std::integral_constant<int, s / 2>{});
 #pragma unroll
-        for (int j = 0; j < FN; ++j) f[j] = *reinterpret_cast<const u32x4*>(p + j * 16 * 128);
+        for (int j = 0; j < FN; ++j) {
+            if constexpr (WK) f[j] = *reinterpret_cast<const u32x4*>(p + (wn * TN + j * 16) * 128 + (s % 2 ? f1 : f0));
+            else f[j] = strided(p, s % 2, wn * TN + j * 16, BN);
+        }
     };
+    constexpr int RX = XK ? HF : 2 * HF, RW = WK ? FN : 2 * FN;  // LDS reads of each
     auto mma = [&](int hh, const u32x4 (&fx)[HF], const u32x4 (&fw)[FN]) {
 #pragma unroll
         for (int i = 0; i < HF; ++i)
@@ -312,21 +389,21 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
             dma(std::integral_constant<int, RP>{}, p + NREG - 1, std::integral_constant<int, LA + decltype(Q_)::value>{});
         });
         mma(0, x0, w0);
-        weave(std::integral_constant<int, HF>{}, std::integral_constant<int, LB>{});
+        weave(std::integral_constant<int, RX>{}, std::integral_constant<int, LB>{});
         rdx(S1{}, 0, x0);
         rdw(S1{}, w1);
         mma(1, x1, w0);
-        weave(std::integral_constant<int, HF + FN>{}, std::integral_constant<int, 0>{});
+        weave(std::integral_constant<int, RX + RW>{}, std::integral_constant<int, 0>{});
         rdx(S1{}, 1, x1);
         mma(0, x0, w1);
-        weave(std::integral_constant<int, HF>{}, std::integral_constant<int, 0>{});
+        weave(std::integral_constant<int, RX>{}, std::integral_constant<int, 0>{});
         __builtin_amdgcn_s_waitcnt(ffn_wait((NREG - 2) * LPP));  // pair p + 1 has landed
         __builtin_amdgcn_s_barrier();                            // region R has been read
         rdx(SN{}, 0, x0);
         rdw(SN{}, w0);
         ffn_for<LA>([&](auto Q_) { dma(R_, p + NREG, Q_); });
         mma(1, x1, w1);
-        weave(std::integral_constant<int, HF + FN>{}, std::integral_constant<int, LA>{});
+        weave(std::integral_constant<int, RX + RW>{}, std::integral_constant<int, LA>{});
     };
     // Pairs 0 .. NREG - 2 whole, and the first loads of the next.
     ffn_for<NREG - 1>([&](auto R_) { ffn_for<LPP>([&](auto Q_) { dma(R_, decltype(R_)::value, Q_); }); });
@@ -375,13 +452,13 @@ hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
                            dim3(64 * TWaves), args, 0, s);
 }
 
-template <class Out, class Z>
+template <class Out, class Z, bool XK = true, bool WK = true>
 hipError_t run_ffn_pipe(const FfnArgs& a, hipStream_t s) {
     constexpr int WO = Out::kGated ? Z::BN / 2 : Z::BN;
     const int64_t tiles = (a.m + Z::BM - 1) / Z::BM * ((a.n + WO - 1) / WO);
     void* args[] = {const_cast<FfnArgs*>(&a)};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe<Out, Z>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                           dim3(Z::THREADS), args, Z::LDS, s);
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe<Out, Z, XK, WK>),
+                           dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(Z::THREADS), args, XK && WK ? Z::LDS : 0, s);
 }
 
 // The pipelined forms: tokens and rows of W of a tile, tiles at a time on the 256

@@ -61,16 +61,6 @@ __device__ __forceinline__ void parts_of(const typename T::store_t (&e)[N], uint
     }
 }
 
-// Transposing LDS read (ds_read_b64_tr_b16): in each group of 16 lanes, lane j gets
-// element j % 4 of the four 16-bit elements at the addresses of lanes j / 4, j / 4 + 4,
-// j / 4 + 8 and j / 4 + 12.
-__device__ __forceinline__ u32x2 read_transposed(const char* p) {
-    typedef short v4i16 __attribute__((ext_vector_type(4)));
-    const v4i16 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) v4i16*)(const_cast<char*>(p)));
-    return __builtin_bit_cast(u32x2, v);
-}
-
 // One operand's share of a thread: R rows by KT elements of k, spread over NT threads.
 template <class T, int R, int KT, int NT, bool KC>
 struct TileOperand {
@@ -328,20 +318,28 @@ hipError_t run_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
                            Z::BUF * Z::BYTES, s);
 }
 
-// 128 x 128 tiles when they give every CU two blocks, 64 x 64 below; four groups
-// over k when even those leave CUs without a tile, 32 tokens where there are no more.
+// 128 x 128 tiles (f32 with a strided operand, whose registers would spill: 128 x 64)
+// from one for each CU on, 16-bit ones with a strided operand from three on (3719 x 1178
+// over 3998 bf16, 300 tiles, 174, 64 x 64 171; its transpose's 217 and 167; 4096 x 4096
+// over 4096 175 and 259); below, tiles as narrow as still leaves CUs without one, and
+// four groups over k (two where the tiles are enough). us, gated and others, f32 unless
+// stated: 4172 x 1792 over 576 (462 tiles of 128) 63 and 78 in 64 x 64; 71 x 1664 over
+// 640, 32 x 64 9.3, 64 x 64 13.6; 951 x 640 over 1518, 36.4 and 29.4, and 41.0 with one
+// group; 509 x 2816 over 2048 bf16, two groups 25.8, four 35.8, one 26.8.
 template <class Out, bool AK, bool BK>
 hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     using T = typename Out::E;
+    constexpr bool F32 = kParts<T> == 3;
     const int64_t outs = Out::kGated ? 2 * t.n : t.n;
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn); };
-    if (tiles(128, 128) >= 512) return run_tile<Out, TileShape<T, 4, 4, kParts<T> == 3 ? 1 : 2, 1>, AK, BK>(t, o, s);
+    if (tiles(128, 128) >= (F32 || (AK && BK) ? 256 : 768))
+        return run_tile<Out, TileShape<T, 4, F32 && !(AK && BK) ? 2 : 4, F32 ? 1 : 2, 1>, AK, BK>(t, o, s);
     if constexpr (!Out::kGated) {
-        if (tiles(64, 64) <= 64) return run_tile<Out, TileShape<T, 1, 1, 1, 4>, AK, BK>(t, o, s);
+        if (tiles(32, 32) <= 128) return run_tile<Out, TileShape<T, 1, 1, 1, 4>, AK, BK>(t, o, s);
     }
-    if (t.m <= 32) return run_tile<Out, TileShape<T, 1, 2, 1, 4>, AK, BK>(t, o, s);
-    if (tiles(64, 64) <= 256) return run_tile<Out, TileShape<T, 2, 2, 1, 4>, AK, BK>(t, o, s);
-    return run_tile<Out, TileShape<T, 2, 2, kParts<T> == 3 ? 1 : 2, 1>, AK, BK>(t, o, s);
+    if (t.m <= 32 || tiles(32, 64) <= 256) return run_tile<Out, TileShape<T, 1, 2, 1, 4>, AK, BK>(t, o, s);
+    if (tiles(64, 64) <= 320) return run_tile<Out, TileShape<T, 2, 2, 1, 4>, AK, BK>(t, o, s);
+    return run_tile<Out, TileShape<T, 2, 2, 1, 2>, AK, BK>(t, o, s);
 }
 
 // The products with the rows of W, from a product's own arguments.
