@@ -226,8 +226,11 @@ __device__ __forceinline__ char* pipe_region() {
     return st;
 }
 
-template <class Out, class Z, bool XK = true, bool WK = true>
-__global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe(FfnArgs a) {
+extern __shared__ __attribute__((aligned(1024))) char pipe_lds[];  // (where both operands are contiguous)
+
+// One tile: tokens from m0 on, outputs from n0 on.
+template <class Out, class Z, bool XK, bool WK>
+__device__ __forceinline__ void pipe_tile(const FfnArgs& a, int64_t m0, int64_t n0) {
     using E = typename Out::E;
     using Acc = typename AccOf<E>::type;
     constexpr bool G = Out::kGated;
@@ -235,20 +238,9 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
     constexpr int TM = 16 * FM, TN = 16 * FN;        // wave tile
     constexpr int WO = G ? BN / 2 : BN;              // outputs of a tile
     constexpr int LPP = Z::LOADS, LA = Z::HALF, LB = LPP - LA;
-    extern __shared__ __attribute__((aligned(1024))) char pipe_lds[];  // (where both are contiguous)
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / Z::WN, wn = w % Z::WN, lr = lane & 15, lq = lane >> 4;
-
-    // Groups of tile-rows, column by column inside a group, a contiguous run on each XCD.
-    const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + WO - 1) / WO, tiles = tiles_m * tiles_n;
-    const int64_t per_xcd = (tiles + 7) / 8;
-    const int64_t t = (int64_t)(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
-    if (t >= tiles) return;
-    const int64_t first = t / (PipeGroup * tiles_n) * PipeGroup;
-    const int64_t size = tiles_m - first < PipeGroup ? tiles_m - first : PipeGroup;
-    const int64_t m0 = (first + t % (PipeGroup * tiles_n) % size) * BM;
-    const int64_t n0 = t % (PipeGroup * tiles_n) / size * WO;
 
     constexpr bool SPLIT = !XK || !WK;  // regions as arrays of their own
     static_assert(!SPLIT || (!G && sizeof(typename E::store_t) == 2 && BM >= 128 && BN >= 128), "strided operands");
@@ -430,6 +422,48 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
         }
     }
 }
+
+// Place of tile t: groups of tile-rows, column by column inside a group.
+template <int BM, int WO>
+__device__ __forceinline__ void pipe_place(const FfnArgs& a, int64_t t, int64_t* m0, int64_t* n0) {
+    const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + WO - 1) / WO;
+    const int64_t first = t / (PipeGroup * tiles_n) * PipeGroup;
+    const int64_t size = tiles_m - first < PipeGroup ? tiles_m - first : PipeGroup;
+    *m0 = (first + t % (PipeGroup * tiles_n) % size) * BM;
+    *n0 = t % (PipeGroup * tiles_n) / size * WO;
+}
+// Tile of block `b` of `n`, a contiguous run on each XCD.
+__device__ __forceinline__ int64_t xcd_run(int64_t b, int64_t n) { return b % 8 * ((n + 7) / 8) + b / 8; }
+
+template <class Out, class Z, bool XK = true, bool WK = true>
+__global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe(FfnArgs a, int64_t tiles) {
+    const int64_t t = xcd_run(blockIdx.x, tiles);
+    if (t >= tiles) return;
+    int64_t m0, n0;
+    pipe_place<Z::BM, (Out::kGated ? Z::BN / 2 : Z::BN)>(a, t, &m0, &n0);
+    pipe_tile<Out, Z, XK, WK>(a, m0, n0);
+}
+
+// `whole` tiles (a multiple of the CUs) in shape Z, the tiles after them as two of H
+// each: a last round that would leave more than half of the CUs idle takes 0.6 of its
+// time (4096 x 22016 over 4096 bf16, 1376 tiles: 661 -> 615 us).
+template <class Out, class Z, class H>
+__global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe_halves(FfnArgs a, int64_t whole,
+                                                                                     int64_t halves) {
+    static_assert(Z::THREADS == H::THREADS && Z::BM == H::BM && Z::BN == 2 * H::BN && Z::BLOCKS == H::BLOCKS, "halves");
+    constexpr int WO = Out::kGated ? Z::BN / 2 : Z::BN;
+    int64_t m0, n0;
+    if ((int64_t)blockIdx.x < whole) {
+        pipe_place<Z::BM, WO>(a, xcd_run(blockIdx.x, whole), &m0, &n0);
+        pipe_tile<Out, Z, true, true>(a, m0, n0);
+    } else {
+        const int64_t t = xcd_run(blockIdx.x - whole, halves);
+        if (t >= halves) return;
+        pipe_place<Z::BM, WO>(a, whole + t / 2, &m0, &n0);
+        n0 += t % 2 * (WO / 2);
+        if (n0 < a.n) pipe_tile<Out, H, true, true>(a, m0, n0);
+    }
+}
 #undef MM_LDS
 
 // ---------------------------------------------------------------------------
@@ -452,13 +486,29 @@ hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
                            dim3(64 * TWaves), args, 0, s);
 }
 
+template <class Out, class Z>
+int64_t pipe_tiles(const FfnArgs& a) {
+    constexpr int WO = Out::kGated ? Z::BN / 2 : Z::BN;
+    return (a.m + Z::BM - 1) / Z::BM * ((a.n + WO - 1) / WO);
+}
 template <class Out, class Z, bool XK = true, bool WK = true>
 hipError_t run_ffn_pipe(const FfnArgs& a, hipStream_t s) {
-    constexpr int WO = Out::kGated ? Z::BN / 2 : Z::BN;
-    const int64_t tiles = (a.m + Z::BM - 1) / Z::BM * ((a.n + WO - 1) / WO);
-    void* args[] = {const_cast<FfnArgs*>(&a)};
+    int64_t tiles = pipe_tiles<Out, Z>(a);
+    void* args[] = {const_cast<FfnArgs*>(&a), &tiles};
     return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe<Out, Z, XK, WK>),
                            dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(Z::THREADS), args, XK && WK ? Z::LDS : 0, s);
+}
+// Shape Z, with the tiles of a last round that fills no more than half of the CUs as
+// halves H.
+template <class Out, class Z, class H>
+hipError_t run_ffn_pipe_halves(const FfnArgs& a, hipStream_t s) {
+    const int64_t tiles = pipe_tiles<Out, Z>(a);
+    int64_t whole = tiles / 256 * 256, halves = 2 * (tiles - whole);
+    if (halves == 0 || halves > 256) return run_ffn_pipe<Out, Z>(a, s);
+    void* args[] = {const_cast<FfnArgs*>(&a), &whole, &halves};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe_halves<Out, Z, H>),
+                           dim3((unsigned)(whole + (halves + 7) / 8 * 8)), dim3(Z::THREADS), args,
+                           Z::LDS > H::LDS ? Z::LDS : H::LDS, s);
 }
 
 // The pipelined forms: tokens and rows of W of a tile, tiles at a time on the 256
@@ -478,20 +528,24 @@ constexpr FfnForm kFfnForms[] = {
     {64, 128, 256, 0.320f, 2.26f}, {128, 128, 256, 0.607f, 2.15f}, {256, 128, 256, 0.956f, 3.35f},
     {256, 256, 256, 1.593f, 7.15f},
 };
+constexpr int kForms = sizeof kFfnForms / sizeof *kFfnForms;
 inline int ffn_form(int64_t m, int64_t rows, int64_t bytes) {
     const float pairs = (float)((bytes + 127) / 128);
     int best = -1;
     float least = 0.f;
-    for (int i = m > 16 ? 1 : 0; i < (int)(sizeof kFfnForms / sizeof *kFfnForms); ++i) {
+    for (int i = m > 16 ? 1 : 0; i < kForms; ++i) {
         const FfnForm& f = kFfnForms[i];
         const int64_t tiles = ((m + f.tokens - 1) / f.tokens) * ((rows + f.rows - 1) / f.rows);
-        const float us = (float)((tiles + f.at_a_time - 1) / f.at_a_time) * (pairs * f.pair_us + f.round_us);
+        const int64_t last = tiles % f.at_a_time;
+        float us = (float)((tiles + f.at_a_time - 1) / f.at_a_time) * (pairs * f.pair_us + f.round_us);
+        if (i == kForms - 1 && last > 0 && last <= f.at_a_time / 2)  // halves
+            us -= pairs * (f.pair_us - kFfnForms[i - 1].pair_us) + f.round_us - kFfnForms[i - 1].round_us;
         if ((best < 0 || us < least) && tiles < (1 << 22)) {  // (a grid holds fewer than 2^32 threads)
             best = i;
             least = us;
         }
     }
-    return best < 0 ? (int)(sizeof kFfnForms / sizeof *kFfnForms) - 1 : best;
+    return best < 0 ? kForms - 1 : best;
 }
 
 // A product in the form that suits its size; the receipt's variant names it.
@@ -514,7 +568,7 @@ hipError_t run_ffn(const FfnArgs& a, hipStream_t s, Launched* L) {
             case 3: return run_ffn_pipe<Out, PipeShape<2, 4, 2, 2, 4>>(a, s);
             case 4: return run_ffn_pipe<Out, PipeShape<2, 4, 4, 2, 4>>(a, s);
             case 5: return run_ffn_pipe<Out, PipeShape<4, 2, 4, 4, 3>>(a, s);
-            default: return run_ffn_pipe<Out, PipeShape<2, 4, 8, 4, 2>>(a, s);
+            default: return run_ffn_pipe_halves<Out, PipeShape<2, 4, 8, 4, 2>, PipeShape<4, 2, 4, 4, 3>>(a, s);
         }
     }
     return hipErrorInvalidValue;

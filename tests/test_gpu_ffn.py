@@ -331,7 +331,14 @@ TILES = [(16, 16, 768, 0.183, 2.02), (32, 16, 512, 0.257, 0.60), (64, 64, 256, 0
 def form(m, rows, row_bytes):
     """The form that the measured costs choose, as a receipt's variant."""
     up = lambda a, b: -(-a // b)  # noqa: E731
-    cost = lambda f: up(up(m, f[0]) * up(rows, f[1]), f[2]) * (up(row_bytes, 128) * f[3] + f[4])  # noqa: E731
+
+    def cost(f):
+        tiles, one = up(m, f[0]) * up(rows, f[1]), up(row_bytes, 128) * f[3] + f[4]
+        us = up(tiles, f[2]) * one
+        if f is TILES[-1] and 0 < tiles % f[2] <= f[2] // 2:  # a last round of halves
+            us -= one - (up(row_bytes, 128) * TILES[-2][3] + TILES[-2][4])
+        return us
+
     f = min(TILES[1:] if m > 16 else TILES, key=cost)
     return f[0] + 4096 * f[1]
 
@@ -339,7 +346,7 @@ def form(m, rows, row_bytes):
 # m, n, k of a gated product in 16 bits (k twice as long in codes); every form is among them
 SHAPES = [(1, 8209, 520), (16, 8209, 1032), (1, 70, 4104), (9, 33, 8), (17, 145, 1048), (30, 257, 2048), (40, 33, 1032),
           (33, 4105, 264), (48, 8209, 520), (64, 1100, 8), (65, 1100, 1032), (200, 257, 72), (300, 1411, 520), (500, 1411, 2056),
-          (129, 8209, 264), (1100, 1985, 200), (700, 2049, 1032), (1200, 4097, 520), (3500, 1795, 200), (3329, 1985, 1096)]
+          (129, 8209, 264), (1100, 1985, 200), (700, 2049, 1032), (1200, 4097, 520), (3500, 1795, 200), (3329, 1985, 1096), (4200, 2400, 136), (4100, 2700, 264)]
 
 
 def test_every_form_is_reached():
