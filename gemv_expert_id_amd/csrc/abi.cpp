@@ -755,17 +755,10 @@ mm_status gated_plan(const mm_gated_params* p, mmk::FfnArgs* a, GatedSizes* z, i
     return MM_OK;
 }
 
-// One product C = op(A) . op(B) of rows.
-GemmPlan rows_product(int dt, int64_t m, int64_t n, int64_t k, bool ta, const void* a, int64_t lda,
-                      const void* b, int64_t ldb, void* c, int64_t ldc) {
-    return GemmPlan{dt, 1, m, n, k, lda, ldb, ldc, 0, 0, 0, ta, false,
-                    static_cast<const char*>(a), static_cast<const char*>(b), static_cast<char*>(c)};
-}
-hipError_t launch_product(const GemmPlan& p, hipStream_t s, mmk::Launched* L) {
-    if (p.m == 1 || p.n == 1) return mmk::launch_gemv(gemv_args(p), s, L);
-    mmk::GemmArgs g{p.a, p.b, p.c, p.m, p.n, p.k, p.lda, p.ldb, p.ldc, p.sa, p.sb, p.sc,
-                    p.batch, p.dt, p.ta, p.tb, p.alpha, p.beta};
-    return mmk::launch_gated_product(g, s, L);
+// C [m, n] = A [m, k] . B [k, n], or with ta A [k, m]^T . B.
+mmk::GemmArgs rows_product(int dt, int64_t m, int64_t n, int64_t k, bool ta, const void* a, int64_t lda,
+                           const void* b, int64_t ldb, void* c, int64_t ldc) {
+    return mmk::GemmArgs{a, b, c, m, n, k, lda, ldb, ldc, 0, 0, 0, 1, dt, ta, 0, 1.f, 0.f};
 }
 
 }  // namespace
@@ -1177,13 +1170,13 @@ mm_status mm_gated_grad(const mm_gated_params* params, mm_buf x, mm_buf w, mm_bu
     const int64_t n2 = 2 * a.n;
     if (dx.ptr) {  // dx [m, k] = dpre [m, 2n] . w [2n, k]
         ++g_launches;
-        const GemmPlan p = rows_product(a.dtype, a.m, a.k, n2, false, dpre.ptr, a.ldpre, w.ptr, ldw, dx.ptr, ldx);
-        if ((st = enqueue(launch_product(p, s, &L))) != MM_OK) return st;
+        const mmk::GemmArgs p = rows_product(a.dtype, a.m, a.k, n2, false, dpre.ptr, a.ldpre, w.ptr, ldw, dx.ptr, ldx);
+        if ((st = enqueue(mmk::launch_gated_product(p, s, &L))) != MM_OK) return st;
     }
     if (dw.ptr) {  // dw [2n, k] = dpre [m, 2n]^T . x [m, k]
         ++g_launches;
-        const GemmPlan p = rows_product(a.dtype, n2, a.k, a.m, true, dpre.ptr, a.ldpre, x.ptr, ldx, dw.ptr, ldw);
-        if ((st = enqueue(launch_product(p, s, &L))) != MM_OK) return st;
+        const mmk::GemmArgs p = rows_product(a.dtype, n2, a.k, a.m, true, dpre.ptr, a.ldpre, x.ptr, ldx, dw.ptr, ldw);
+        if ((st = enqueue(mmk::launch_gated_product(p, s, &L))) != MM_OK) return st;
     }
     set_receipt(receipt, MM_ROUTE_GATED, (uint32_t)a.dtype, launches, L);
     return ok();

@@ -16,8 +16,10 @@
 // one is multiplied, in 16-byte pieces at any address, along k or along the rows. LDS
 // keeps a contiguous operand by rows, padded by 16 bytes so that the 16 rows of a
 // fragment read start in distinct banks, and a strided one by k, as it comes; its
-// fragments take two transposing reads each. Rows past the end repeat the last one
-// (their sums are not stored); elements of k past the end are zeros in both operands.
+// fragments take two transposing reads each. Rows past the end repeat others (their
+// sums are not stored); elements of k past the end are zeros in both operands. A piece
+// that passes an end is fetched from where it still lies inside and moved up in
+// registers, so that edges cost no loads of single elements.
 #pragma once
 
 #include "ffn.hpp"
@@ -73,12 +75,16 @@ struct TileOperand {
     static constexpr int ALL = R * KT / V;                   // pieces
     static constexpr int N = ALL > NT ? ALL / NT : 1;        // of a thread (of the first ALL, if fewer)
     static_assert(N * NT == ALL || N == 1, "whole pieces");
+    static_assert(NT % C == 0, "a thread's pieces lie at one place of their rows");
     Pack<S, V> v[N];
-    const S* p[KC ? N : V];  // row starts; or the columns (p[0] alone while they are neighbours)
+    const S* p[KC ? N : 1];  // row starts; or the columns
     int64_t ld;
-    bool split;  // strided: the columns are fetched one by one
+    int shift;               // a piece that passes the end is fetched this many elements earlier
+    int some;                // an operand shorter than a piece: elements to fetch one by one (else 0)
 
     static __device__ __forceinline__ int piece(int i) { return (int)threadIdx.x + i * NT; }
+    // Place of this thread's pieces in their rows.
+    static __device__ __forceinline__ int place() { return (int)threadIdx.x % C * V; }
     // Strided: 16-byte chunk swizzle of k-row r, by which the 16 k-rows of a
     // transposing read cover all banks twice.
     static __device__ __forceinline__ int swizzle(int r) {
@@ -86,23 +92,25 @@ struct TileOperand {
         else if constexpr (R == 64) return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1));
         else return 2 * ((r >> 3) & 1);
     }
-    // `row(r)`: the operand's row that tile row r stands for, already inside it.
+    // Contiguous: `row(r)` is the operand's row that tile row r stands for, already
+    // inside it. Strided: the tile's columns are first .. first + R - 1 of `cols`.
     template <class Row>
-    __device__ __forceinline__ void init(const void* base, int64_t pitch, Row row) {
+    __device__ __forceinline__ void init(const void* base, int64_t pitch, int64_t first, int64_t cols, Row row) {
         const S* s = static_cast<const S*>(base);
         ld = pitch;
+        shift = some = 0;
         if constexpr (KC) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) p[i] = s + row(piece(i) / C) * ld + (piece(i) % C) * V;
+            for (int i = 0; i < N; ++i) p[i] = s + row(piece(i) / C) * ld;
         } else {
-            static_assert(NT % C == 0, "a thread's pieces share their columns");
-            const int64_t first = row(piece(0) % C * V);
-            split = false;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int64_t r = row(piece(0) % C * V + e);
-                split |= r != first + e;
-                p[e] = s + r;
+            const int64_t c = first + place();
+            const int64_t over = c + V - cols;  // elements past the end
+            if (cols < V) {
+                some = (int)cols;
+                p[0] = s;  // (first is 0)
+            } else {
+                p[0] = s + (over > 0 ? cols - V : c);
+                if (over > 0 && over < V) shift = (int)over;
             }
         }
     }
@@ -110,37 +118,48 @@ struct TileOperand {
     template <bool TAIL>
     __device__ __forceinline__ void fetch(int64_t k0, int64_t K) {
         if (ALL < NT && (int)threadIdx.x >= ALL) return;
+        const int64_t at = k0 + place();
+        if constexpr (KC && TAIL) {
+            const int64_t over = at + V - K;
+            shift = over > 0 ? (int)(over < V ? over : V) : 0;
+            some = K < V ? (int)K : 0;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if constexpr (KC) {
-                const int64_t left = K - k0 - piece(i) % C * V;
-                if (!TAIL || left >= V) {
-                    v[i] = *reinterpret_cast<const Pack<S, V>*>(p[i] + k0);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[i].v[e] = e < left ? p[i][k0 + e] : S(0);
-                }
+                if (!TAIL || (shift == 0 && !some)) v[i] = *reinterpret_cast<const Pack<S, V>*>(p[i] + at);
+                else if (!some) v[i] = *reinterpret_cast<const Pack<S, V>*>(p[i] + K - V);
+                else few(v[i], p[i], place() ? 0 : some);
             } else {
-                const int64_t at = k0 + piece(i) / C;
-                if (TAIL && at >= K) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[i].v[e] = S(0);
-                } else if (!split) {
-                    v[i] = *reinterpret_cast<const Pack<S, V>*>(p[0] + at * ld);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[i].v[e] = p[e][at * ld];
-                }
+                const int64_t k = k0 + piece(i) / C;
+                if (TAIL && k >= K) few(v[i], p[0], 0);
+                else if (!some) v[i] = *reinterpret_cast<const Pack<S, V>*>(p[0] + k * ld);
+                else few(v[i], p[0] + k * ld, place() ? 0 : some);
             }
         }
+        if (KC && TAIL && some) shift = 0;
     }
-    __device__ __forceinline__ void store(char* lds) const {
+    static __device__ __forceinline__ void few(Pack<S, V>& to, const S* from, int n) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) to.v[e] = e < n ? from[e] : S(0);
+    }
+    __device__ __forceinline__ void store(char* lds) {
         if (ALL < NT && (int)threadIdx.x >= ALL) return;
+        if (shift) {  // the elements wanted to the front, zeros behind
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int b = 1; b <= V; b *= 2)
+                    if (shift & b) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) v[i].v[e] = e + b < V ? v[i].v[e + b < V ? e + b : 0] : S(0);
+                    }
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             uint32_t w[P][V / 2];
             parts_of<T, V>(v[i].v, w);
-            const int r = piece(i) / C, at = piece(i) % C * V * 2;
+            const int r = piece(i) / C, at = place() * 2;
             char* to = lds + r * PITCH + (KC ? at : (((at >> 4) ^ swizzle(r)) << 4) + (at & 15));
 #pragma unroll
             for (int q = 0; q < P; ++q) {
@@ -206,8 +225,8 @@ __global__ __launch_bounds__(Z::THREADS, Z::KS > 1 ? Z::KS : 2) void ffn_tile(Ti
     const int64_t m0 = (int64_t)(blockIdx.x / t.tiles_n) * Z::BM, n0 = (int64_t)(blockIdx.x % t.tiles_n) * RO;
     OA a;
     OB b;
-    a.init(t.a, t.lda, [&](int r) { return m0 + r < t.m ? m0 + r : t.m - 1; });
-    b.init(t.b, t.ldb, [&](int r) {
+    a.init(t.a, t.lda, m0, t.m, [&](int r) { return m0 + r < t.m ? m0 + r : t.m - 1; });
+    b.init(t.b, t.ldb, n0, t.n, [&](int r) {
         // Gated: each wave column's rows are half gate, half up projection.
         const int64_t col = n0 + (G ? (r / TN) * (TN / 2) + r % (TN / 2) : r);
         return (col < t.n ? col : t.n - 1) + (G && r % TN >= TN / 2 ? t.n : 0);
@@ -318,28 +337,39 @@ hipError_t run_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
                            Z::BUF * Z::BYTES, s);
 }
 
-// 128 x 128 tiles (f32 with a strided operand, whose registers would spill: 128 x 64)
-// from one for each CU on, 16-bit ones with a strided operand from three on (3719 x 1178
-// over 3998 bf16, 300 tiles, 174, 64 x 64 171; its transpose's 217 and 167; 4096 x 4096
-// over 4096 175 and 259); below, tiles as narrow as still leaves CUs without one, and
-// four groups over k (two where the tiles are enough). us, gated and others, f32 unless
-// stated: 4172 x 1792 over 576 (462 tiles of 128) 63 and 78 in 64 x 64; 71 x 1664 over
-// 640, 32 x 64 9.3, 64 x 64 13.6; 951 x 640 over 1518, 36.4 and 29.4, and 41.0 with one
-// group; 509 x 2816 over 2048 bf16, two groups 25.8, four 35.8, one 26.8.
+// The forms: 32 FM x 32 FN tiles, SUB steps, KS groups; and what a round of 512 (of
+// 256 with four groups) costs in us, for each iteration over k and at its start.
+// From 130 products of each type and layout, in every form; the form with the lowest
+// sum of rounds is within 2% (16-bit rows any way stored: 5%) of the fastest in the
+// mean. Both sides of some borders, us: gated f32, 4172 x 1792 over 576, 128 x 128
+// 63, 64 x 64 81; 71 x 1664 over 640, 32 x 64 9.3, 64 x 64 13.6; 951 x 640 over 1518,
+// 64 x 64 with four groups 29.4, 32 x 64 36.4, 64 x 64 with one 43.6.
 template <class Out, bool AK, bool BK>
 hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     using T = typename Out::E;
-    constexpr bool F32 = kParts<T> == 3;
+    constexpr bool F32 = kParts<T> == 3, ROWS = AK && BK;
+    using Big = TileShape<T, 4, F32 && !ROWS ? 2 : 4, F32 ? 1 : 2, 1>;
+    using Mid = TileShape<T, 2, 2, 1, 1>;
+    using Deep = TileShape<T, 2, 2, 1, 4>;
+    using Low = TileShape<T, 1, 2, 1, 4>;
+    constexpr float big = F32 ? (ROWS ? 3.0f : 1.7f) : (ROWS ? 1.6f : 1.4f);
+    constexpr float mid = F32 ? (ROWS ? 1.17f : 1.3f) : (ROWS ? 0.42f : 0.36f);
+    constexpr float deep = F32 ? (ROWS ? 2.5f : 3.5f) : (ROWS ? 1.5f : 1.36f);
+    constexpr float low = F32 ? (ROWS ? 1.55f : 2.4f) : (ROWS ? 0.91f : 0.96f);
     const int64_t outs = Out::kGated ? 2 * t.n : t.n;
-    const auto tiles = [&](int64_t bm, int64_t bn) { return ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn); };
-    if (tiles(128, 128) >= (F32 || (AK && BK) ? 256 : 768))
-        return run_tile<Out, TileShape<T, 4, F32 && !(AK && BK) ? 2 : 4, F32 ? 1 : 2, 1>, AK, BK>(t, o, s);
-    if constexpr (!Out::kGated) {
-        if (tiles(32, 32) <= 128) return run_tile<Out, TileShape<T, 1, 1, 1, 4>, AK, BK>(t, o, s);
+    const auto us = [&](int bm, int bn, int kt, int at_a_time, float step, float start) {
+        const int64_t tiles = ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn);
+        return (float)((tiles + at_a_time - 1) / at_a_time) * ((float)((t.k + kt - 1) / kt) * step + start);
+    };
+    if constexpr (!Out::kGated) {  // the narrowest while half of the CUs have none
+        if (((t.m + 31) / 32) * ((t.n + 31) / 32) <= 128) return run_tile<Out, TileShape<T, 1, 1, 1, 4>, AK, BK>(t, o, s);
     }
-    if (t.m <= 32 || tiles(32, 64) <= 256) return run_tile<Out, TileShape<T, 1, 2, 1, 4>, AK, BK>(t, o, s);
-    if (tiles(64, 64) <= 320) return run_tile<Out, TileShape<T, 2, 2, 1, 4>, AK, BK>(t, o, s);
-    return run_tile<Out, TileShape<T, 2, 2, 1, 2>, AK, BK>(t, o, s);
+    const float b = us(Big::BM, Big::BN, Big::KT, 512, big, 5.f), m = us(64, 64, 32, 512, mid, 1.5f);
+    const float d = us(64, 64, 128, 256, deep, 1.4f), l = us(32, 64, 128, 256, low, 1.4f);
+    if (b <= m && b <= d && b <= l) return run_tile<Out, Big, AK, BK>(t, o, s);
+    if (m <= d && m <= l) return run_tile<Out, Mid, AK, BK>(t, o, s);
+    if (d <= l) return run_tile<Out, Deep, AK, BK>(t, o, s);
+    return run_tile<Out, Low, AK, BK>(t, o, s);
 }
 
 // The products with the rows of W, from a product's own arguments.
