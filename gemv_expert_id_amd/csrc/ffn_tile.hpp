@@ -343,7 +343,9 @@ hipError_t run_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
 // sum of rounds is within 2% (16-bit rows any way stored: 5%) of the fastest in the
 // mean. Both sides of some borders, us: gated f32, 4172 x 1792 over 576, 128 x 128
 // 63, 64 x 64 81; 71 x 1664 over 640, 32 x 64 9.3, 64 x 64 13.6; 951 x 640 over 1518,
-// 64 x 64 with four groups 29.4, 32 x 64 36.4, 64 x 64 with one 43.6.
+// 64 x 64 with four groups 29.4, 32 x 64 36.4, 64 x 64 with one 43.6. Others: 25 x 377
+// over 20864 f32, 32 x 32 156, 32 x 64 248; 3 x 3456 over 3200 bf16, two steps an
+// iteration 14.3, one 20.5; gated 2 x 24192 over 2503 bf16, 48.8 and 37.1.
 template <class Out, bool AK, bool BK>
 hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     using T = typename Out::E;
@@ -352,6 +354,7 @@ hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     using Mid = TileShape<T, 2, 2, 1, 1>;
     using Deep = TileShape<T, 2, 2, 1, 4>;
     using Low = TileShape<T, 1, 2, 1, 4>;
+    using Long = TileShape<T, 1, 2, F32 ? 1 : 2, 4>;
     constexpr float big = F32 ? (ROWS ? 3.0f : 1.7f) : (ROWS ? 1.6f : 1.4f);
     constexpr float mid = F32 ? (ROWS ? 1.17f : 1.3f) : (ROWS ? 0.42f : 0.36f);
     constexpr float deep = F32 ? (ROWS ? 2.5f : 3.5f) : (ROWS ? 1.5f : 1.36f);
@@ -361,14 +364,17 @@ hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
         const int64_t tiles = ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn);
         return (float)((tiles + at_a_time - 1) / at_a_time) * ((float)((t.k + kt - 1) / kt) * step + start);
     };
-    if constexpr (!Out::kGated) {  // the narrowest while half of the CUs have none
-        if (((t.m + 31) / 32) * ((t.n + 31) / 32) <= 128) return run_tile<Out, TileShape<T, 1, 1, 1, 4>, AK, BK>(t, o, s);
+    if constexpr (!Out::kGated) {  // the narrowest while CUs are left
+        if (((t.m + 31) / 32) * ((t.n + 31) / 32) <= 256)
+            return run_tile<Out, TileShape<T, 1, 1, F32 ? 1 : 2, 4>, AK, BK>(t, o, s);
     }
+    const bool few = ((t.m + 31) / 32) * ((outs + 63) / 64) <= 256;
     const float b = us(Big::BM, Big::BN, Big::KT, 512, big, 5.f), m = us(64, 64, 32, 512, mid, 1.5f);
-    const float d = us(64, 64, 128, 256, deep, 1.4f), l = us(32, 64, 128, 256, low, 1.4f);
+    const float d = us(64, 64, 128, 256, deep, 1.4f), l = few && !F32 ? us(32, 64, 256, 256, 1.3f, 1.4f) : us(32, 64, 128, 256, low, 1.4f);
     if (b <= m && b <= d && b <= l) return run_tile<Out, Big, AK, BK>(t, o, s);
     if (m <= d && m <= l) return run_tile<Out, Mid, AK, BK>(t, o, s);
     if (d <= l) return run_tile<Out, Deep, AK, BK>(t, o, s);
+    if (few) return run_tile<Out, Long, AK, BK>(t, o, s);
     return run_tile<Out, Low, AK, BK>(t, o, s);
 }
 
