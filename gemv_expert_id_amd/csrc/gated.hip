@@ -60,6 +60,101 @@ __global__ __launch_bounds__(256) void gated_grad(FfnArgs a, int sh) {
     }
 }
 
+// Few rows by few columns over a long contraction (dpre . w of a small batch): 16 FM
+// rows x 16 columns a block, whose 16 waves take every 16th step of 32 of the
+// contraction, read both operands straight into fragments, DEP steps in flight, and are
+// summed in order through LDS. A wave's lanes hold 8 rows of w at a column each, so w's
+// loads are single elements: 16 neighbours a row. Bound by the CU's own load path, for
+// few blocks share one contraction. us, here and in the narrowest tiles: f32 8 x 49 over
+// 21376 55.0 and 154.4, 16 x 1024 over 8198 32.1 and 60.9, 32 x 64 over 2000 11.1 and
+// 16.9, 32 x 130 over 600 9.8 and 7.4; bf16 8 x 49 over 21376 35.1 and 90.0, 16 x 4096
+// over 22016 120.7 and 124.8, 32 x 1024 over 8198 30.3 and 35.6, 32 x 256 over 4096 15.0
+// and 15.2, 16 x 1601 over 700 6.8 and 5.8.
+template <class T, int FM>
+__global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
+    using S = typename T::store_t;
+    using M = MmaOf<T>;
+    constexpr int P = kParts<T>, DEP = T::code == 0 && FM > 1 ? 2 : 4;
+    __shared__ f32x4 part[16][FM][64];
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * 16, ldw = a.ldw / (int64_t)sizeof(S);
+    const S* w = static_cast<const S*>(a.w) + (n0 + lr < a.n ? n0 + lr : a.n - 1);  // columns past the end repeat the last
+    const S* x[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        x[i] = static_cast<const S*>(a.x) + (i * 16 + lr < a.m ? i * 16 + lr : a.m - 1) * (a.ldx / (int64_t)sizeof(S));
+    f32x4 acc[FM], low[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) acc[i] = low[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const auto multiply = [&](const S (&ew)[8], const Pack<S, 8> (&ex)[FM]) {
+        uint32_t pw[P][4], px[P][4];
+        parts_of<T, 8>(ew, pw);
+        u32x4 fw[P], fx[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q) fw[q] = u32x4{pw[q][0], pw[q][1], pw[q][2], pw[q][3]};
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            parts_of<T, 8>(ex[i].v, px);
+#pragma unroll
+            for (int q = 0; q < P; ++q) fx[q] = u32x4{px[q][0], px[q][1], px[q][2], px[q][3]};
+            if constexpr (P == 3) {
+                low[i] = step_mma<M>(fw[2], fx[0], low[i]);
+                low[i] = step_mma<M>(fw[0], fx[2], low[i]);
+                low[i] = step_mma<M>(fw[1], fx[1], low[i]);
+                low[i] = step_mma<M>(fw[1], fx[0], low[i]);
+                low[i] = step_mma<M>(fw[0], fx[1], low[i]);
+            }
+            acc[i] = step_mma<M>(fw[0], fx[0], acc[i]);
+        }
+    };
+    const int64_t whole = a.k / 32;  // steps
+    int64_t s = wave;
+    for (; s + 16 * (DEP - 1) < whole; s += 16 * DEP) {
+        S ew[DEP][8];
+        Pack<S, 8> ex[DEP][FM];
+#pragma unroll
+        for (int d = 0; d < DEP; ++d) {
+            const int64_t r = (s + 16 * d) * 32 + 8 * lq;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) ex[d][i] = *reinterpret_cast<const Pack<S, 8>*>(x[i] + r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ew[d][e] = w[(r + e) * ldw];
+        }
+#pragma unroll
+        for (int d = 0; d < DEP; ++d) multiply(ew[d], ex[d]);
+    }
+    for (; s * 32 < a.k; s += 16) {  // the rest; rows past the end are zeros in both
+        const int64_t r = s * 32 + 8 * lq;
+        S ew[8];
+        Pack<S, 8> ex[FM];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool in = r + e < a.k;
+            ew[e] = in ? w[(r + e) * ldw] : S(0);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) ex[i].v[e] = in ? x[i][r + e] : S(0);
+        }
+        multiply(ew, ex);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) part[wave][i][lane] = acc[i] + low[i];
+    __syncthreads();
+    if (wave >= FM) return;
+    f32x4 sum = part[0][wave][lane];
+#pragma unroll
+    for (int g = 1; g < 16; ++g) sum += part[g][wave][lane];
+    const PlainOut<T> out{a};
+    if (wave * 16 + lr < a.m) out.one(wave * 16 + lr, n0 + 4 * lq, sum);
+}
+template <class T>
+hipError_t long_product(const FfnArgs& o, hipStream_t s) {
+    const dim3 grid((unsigned)((o.n + 15) / 16));
+    void* args[] = {const_cast<FfnArgs*>(&o)};
+    const void* fn = o.m <= 16 ? (const void*)&long_product<T, 1> : (const void*)&long_product<T, 2>;
+    return hipLaunchKernel(fn, grid, dim3(1024), args, 0, s);
+}
+
 template <class T>
 hipError_t tile_product(const GemmArgs& g, const FfnArgs& o, hipStream_t s) {
     const TileArgs t{g.A, g.B, g.m, g.n, g.k, g.lda, g.ldb, 0};
@@ -115,6 +210,10 @@ hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
     o.ldx = g.lda * es;
     o.ldw = g.ldb * es;
     o.ldy = g.ldc;
+    if (!g.ta && g.m <= 32 && g.n <= 4096 && g.k >= (g.dtype == 0 || g.m <= 16 ? 1024 : 8192))
+        return g.dtype == 0   ? long_product<TF32>(o, s)
+               : g.dtype == 1 ? long_product<TF16>(o, s)
+                              : long_product<TBF16>(o, s);
     if (chunked && tiles > 64)
         return g.dtype == 1 ? chunked_product<TF16>(g, o, tiles, s) : chunked_product<TBF16>(g, o, tiles, s);
     return g.dtype == 0   ? tile_product<TF32>(g, o, s)

@@ -366,6 +366,14 @@ def test_i8_forms(m, n, k):
     assert check_i8(m % 3, m, 2 * n - 1, k, pad=16).variant == form(m, 2 * n - 1, k)
 
 
+# Contractions (2n) long enough for few rows to be split over a block's waves, and the borders of that.
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 511, 33), (1, 512, 1), (2, 513, 17), (16, 515, 49), (17, 2047, 16), (16, 1040, 4096),
+                                   (13, 529, 4097), (17, 4096, 31), (32, 4111, 64), (33, 4111, 20)])
+def test_long_contractions(dt, m, n, k):
+    check_grad(dt, m, n, k, gate=GATES[m % 2], pad=n % 2, shift=k % 3, want=("dx",))
+
+
 @pytest.mark.parametrize("m,n,k", SHAPES)
 def test_gradient_forms(m, n, k):
     assert check_grad(1, m, n, k, gate=GATES[m % 2], saved=False, want=()).variant == form(m, 2 * n, 2 * k)
