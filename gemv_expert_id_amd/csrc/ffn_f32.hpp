@@ -1,0 +1,263 @@
+// Gated products of f32 rows in three bf16 parts (ffn_tile.hpp): forms whose waves part
+// the fragments themselves, and the choice among all of f32's forms.
+#pragma once
+
+#include "ffn_pipe.hpp"
+
+namespace mmk {
+
+__device__ __forceinline__ void part8(const u32x4 (&r)[2], u32x4 (&out)[3]) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(r[i / 4][i % 4]);
+    uint32_t w[3][4];
+    parts_of<TF32, 8>(e, w);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) out[q] = u32x4{w[q][0], w[q][1], w[q][2], w[q][3]};
+}
+
+// One step of 32 of k: the six products of FM x FN fragments. `x(i, f)` and `w(j, f)`
+// give a fragment's parts.
+template <int FM, int FN>
+struct PartsAcc {
+    f32x4 acc[FM][FN], low[FM][FN];  // upper parts; the small products
+    __device__ __forceinline__ PartsAcc() {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = low[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    template <class X, class W>
+    __device__ __forceinline__ void step(X x, W w) {
+        u32x4 fx[FM][3], fw[3];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) x(i, fx[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            w(j, fw);
+            constexpr int PW[5] = {2, 0, 1, 1, 0}, PX[5] = {0, 2, 1, 0, 1};  // smallest first
+#pragma unroll
+            for (int q = 0; q < 5; ++q)
+#pragma unroll
+                for (int i = 0; i < FM; ++i) low[i][j] = step_mma<TBF16>(fw[PW[q]], fx[i][PX[q]], low[i][j]);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) acc[i][j] = step_mma<TBF16>(fw[0], fx[i][0], acc[i][j]);
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Rows of whole 16-byte chunks through the regions of ffn_pipe, two of them (a pair's
+// 128 bytes are one step): LDS holds the raw 4 bytes an element, loads go there without
+// a register, and each wave parts the fragments that it reads. Three blocks of 64 x 64
+// share a CU: one's loads and barriers fall into the others' arithmetic.
+// ---------------------------------------------------------------------------
+#define MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
+template <class Out, class Z>
+__global__ __launch_bounds__(Z::THREADS, 3) void ffn_pipe_f32(FfnArgs a, int64_t tiles) {
+    static_assert(Out::kGated && Z::WAVES == 4 && 3 * Z::LDS <= 160 * 1024, "three blocks of a CU");
+    constexpr int BM = Z::BM, FM = Z::FM, FN = Z::FN, NREG = Z::NREG, TM = 16 * FM, TN = 16 * FN, WO = Z::BN / 2;
+    const int64_t t = xcd_run(blockIdx.x, tiles);
+    if (t >= tiles) return;
+    int64_t m0, n0;
+    pipe_place<BM, WO>(a, t, &m0, &n0);
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / Z::WN, wn = w % Z::WN, lr = lane & 15, lq = lane >> 4;
+    const int64_t bytes = a.k * 4;
+    const int chunks = (int)(bytes / 16), pairs = (chunks + 7) / 8;
+    const int ldx = (int)a.ldx, ldw = (int)a.ldw;
+    const int64_t xrows = a.m - m0 < BM ? a.m - m0 : BM, wrows = a.n - n0 < WO ? a.n - n0 : WO;
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, m0, a.ldx, xrows, bytes);
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w, n0, a.ldw, wrows, bytes);
+    const __amdgpu_buffer_rsrc_t ru = rows_rsrc(a.w, n0 + a.n, a.ldw, wrows, bytes);
+    // A load covers 8 rows, the lane the chunk that belongs at slot lane % 8.
+    const int dch = (lane & 7) ^ (lane >> 3);
+    const int vox = (lane >> 3) * ldx + dch * 16, vow = (lane >> 3) * ldw + dch * 16;
+    auto issue = [&](auto R_, int p) {
+        char* region = pipe_lds + decltype(R_)::value * Z::REGION;
+        const bool live = p * 8 + dch < chunks;  // (chunks past k are zeros)
+#pragma unroll
+        for (int q = 0; q < Z::XI; ++q) {
+            const int row = (w * Z::XI + q) * 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MM_LDS(region + row * 128), 16, live ? (uint32_t)vox : kPastEnd,
+                                                     row * ldx + p * 128, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < Z::WI; ++q) {
+            const int row = (w * Z::WI + q) * 8;  // each wave column's rows are half gate, half up projection
+            const int col = row / TN * (TN / 2) + row % (TN / 2);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row % TN >= TN / 2 ? ru : rw, MM_LDS(region + (BM + row) * 128), 16,
+                                                     live ? (uint32_t)vow : kPastEnd, col * ldw + p * 128, 0, 0);
+        }
+    };
+    PartsAcc<FM, FN> s;
+    const int f0 = lr * 128 + ((lq ^ (lr & 7)) << 4), f1 = lr * 128 + (((4 + lq) ^ (lr & 7)) << 4);  // (k in one order for both)
+    ffn_for<NREG - 1>([&](auto R_) { issue(R_, decltype(R_)::value); });
+    for (int p = 0; p < pairs; p += NREG) {  // (pairs past the last one are zeros)
+        ffn_for<NREG>([&](auto R_) {
+            constexpr int R = decltype(R_)::value;
+            // Pair p + R has landed; the pair before it has been read by every wave.
+            __builtin_amdgcn_s_waitcnt(ffn_wait((NREG - 2) * Z::LOADS));
+            __builtin_amdgcn_s_barrier();
+            issue(std::integral_constant<int, (R + NREG - 1) % NREG>{}, p + R + NREG - 1);
+            const char* xs = pipe_lds + R * Z::REGION + wm * TM * 128;
+            const char* ws = pipe_lds + R * Z::REGION + (BM + wn * TN) * 128;
+            const auto read = [&](const char* rows, u32x4(&f)[3]) {
+                const u32x4 r[2] = {*reinterpret_cast<const u32x4*>(rows + f0), *reinterpret_cast<const u32x4*>(rows + f1)};
+                part8(r, f);
+            };
+            s.step([&](int i, u32x4(&f)[3]) { read(xs + i * 2048, f); },
+                   [&](int j, u32x4(&f)[3]) { read(ws + j * 2048, f); });
+        });
+    }
+    __builtin_amdgcn_s_waitcnt(ffn_wait(0));  // no load into LDS outlives its wave
+    const Out out{a};
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t row = m0 + wm * TM + i * 16 + lr;
+        if (row >= a.m) continue;
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j)
+            out.pair(row, n0 + wn * (TN / 2) + j * 16 + 4 * lq, s.acc[i][j] + s.low[i][j],
+                     s.acc[i][j + FN / 2] + s.low[i][j + FN / 2]);
+    }
+}
+#undef MM_LDS
+
+// ---------------------------------------------------------------------------
+// Rows of any alignment, few tiles: each of a block's KS waves computes the whole tile
+// of 16 FM x 16 FN over every KS-th step. Waves share nothing, so there is no LDS and no
+// barrier on the way: fragments come straight into registers (8 elements of a row a
+// lane, a row's 128 bytes by four lanes), the next step's as soon as a fragment has been
+// parted. At the end the partial tiles meet in LDS, summed in the order of the waves.
+// ---------------------------------------------------------------------------
+template <class Out, int FM, int FN, int KS>
+__global__ __launch_bounds__(64 * KS, 2) void ffn_waves_f32(FfnArgs a, int64_t tiles) {
+    constexpr int BM = 16 * FM, WO = 8 * FN;
+    static_assert(Out::kGated, "gated");
+    const int64_t t = xcd_run(blockIdx.x, tiles);
+    if (t >= tiles) return;
+    int64_t m0, n0;
+    pipe_place<BM, WO>(a, t, &m0, &n0);
+    const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+    const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const float* x[FM];  // (rows past the end repeat the last; their sums are not stored)
+    const float* w[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t r = m0 + i * 16 + lr;
+        x[i] = static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4) + kg * 32 + 8 * lq;
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int64_t r = n0 + j % (FN / 2) * 16 + lr;
+        w[j] = static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4) +
+               kg * 32 + 8 * lq;
+    }
+    u32x4 rx[FM][2], rw[FN][2];
+    const auto load = [](const float*& p, u32x4(&r)[2]) {  // and on to the next step
+        r[0] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<float, 4>*>(p));
+        r[1] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<float, 4>*>(p + 4));
+        p += 32 * KS;
+    };
+    PartsAcc<FM, FN> s;
+    const auto step = [&](auto more_) {
+        const auto take = [&](const float*& p, u32x4(&r)[2], u32x4(&f)[3]) {
+            part8(r, f);
+            if constexpr (decltype(more_)::value) load(p, r);
+        };
+        s.step([&](int i, u32x4(&f)[3]) { take(x[i], rx[i], f); }, [&](int j, u32x4(&f)[3]) { take(w[j], rw[j], f); });
+    };
+    const int whole = (int)(a.k / 32);
+    int left = whole > kg ? (whole - kg + KS - 1) / KS : 0;
+    if (left > 0) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) load(x[i], rx[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) load(w[j], rw[j]);
+        for (; left > 1; --left) step(std::true_type{});
+        step(std::false_type{});
+    }
+    if (a.k % 32 && whole % KS == kg) {  // the step that k ends in: zeros behind it, in both operands
+        const int valid = (int)(a.k - (int64_t)whole * 32) - 8 * lq;
+        const auto part = [&](const float* p, u32x4(&r)[2]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e / 4][e % 4] = e < valid ? __float_as_uint(p[e]) : 0u;
+        };
+#pragma unroll
+        for (int i = 0; i < FM; ++i) part(x[i], rx[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) part(w[j], rw[j]);
+        step(std::false_type{});
+    }
+    __shared__ f32x4 sums[KS][FM * FN][64];
+#pragma unroll
+    for (int f = 0; f < FM * FN; ++f) sums[kg][f][lane] = s.acc[f / FN][f % FN] + s.low[f / FN][f % FN];
+    __syncthreads();
+    const Out out{a};
+    for (int u = kg; u < FM * FN / 2; u += KS) {
+        const int i = u / (FN / 2), j = u % (FN / 2), f = i * FN + j;
+        f32x4 g = sums[0][f][lane], v = sums[0][f + FN / 2][lane];
+#pragma unroll
+        for (int q = 1; q < KS; ++q) {
+            g += sums[q][f][lane];
+            v += sums[q][f + FN / 2][lane];
+        }
+        if (m0 + i * 16 + lr < a.m) out.pair(m0 + i * 16 + lr, n0 + j * 16 + 4 * lq, g, v);
+    }
+}
+
+template <class Out, int FM, int FN, int KS>
+hipError_t run_ffn_waves(const FfnArgs& a, hipStream_t s) {
+    int64_t tiles = (a.m + 16 * FM - 1) / (16 * FM) * ((a.n + 8 * FN - 1) / (8 * FN));
+    void* args[] = {const_cast<FfnArgs*>(&a), &tiles};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_waves_f32<Out, FM, FN, KS>),
+                           dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * KS), args, 0, s);
+}
+
+// The forms of f32 rows: tokens and rows of w of a tile, elements of k an iteration,
+// tiles at a time on the 256 CUs; and what a round of them costs in us, for each
+// iteration and at its start. From 150 products of 65 to 4096 tokens in every form; the
+// one with the lowest sum of rounds is within 4% of the fastest in the mean (9% where
+// rows are not whole 16-byte chunks). Few tokens take f32 instructions, at 2/5 of the
+// rate of the six products but with nothing to part. Both sides of some borders, us:
+// 70 tokens by 1200 over 8000, thin 33.8, 32 x 32 57.3; 256 by the same, 32 x 64 86, thin
+// 98, 32 x 32 112; 70 by 2816 over 2048, thin 19.8, 32 x 64 25.3; 160 by 22016 over 4096,
+// 64 x 64 by four waves 259, through LDS 272, 128 x 128 311; 509 by 2816 over 2048, 64 x 64
+// through LDS 53.6, by four waves 61.8, 128 x 128 124; 4096 by 8192 over 4096, 128 x 128
+// 1392, 64 x 64 through LDS 1756.
+// Bound by arithmetic from 512 tokens on: 4096 x 8192 over 4096 runs at 197 TFLOP/s, six
+// times that in the matrix units; 509 by 2816 over 2048 at 106, for 352 tiles of 512.
+template <class Out>
+hipError_t run_ffn_f32(const FfnArgs& a, hipStream_t s, Launched* L) {
+    const bool chunked = ffn_chunked(a, 4);
+    const auto us = [&](int tokens, int rows, int kt, int at_a_time, float step, float start) {
+        const int64_t tiles = (a.m + tokens - 1) / tokens * ((2 * a.n + rows - 1) / rows);
+        if (tokens < 128 && tiles >= (1 << 22)) return 3e38f;  // (a grid holds fewer than 2^32 threads)
+        return (float)((tiles + at_a_time - 1) / at_a_time) * ((float)((a.k + kt - 1) / kt) * step + start);
+    };
+    const float big = us(128, 128, 32, 512, 2.6f, 14.f);
+    const float mid = chunked ? us(64, 64, 32, 512, 0.9f, 1.f) : us(64, 64, 32, 512, 1.2f, 3.f);
+    const float four = us(64, 64, 128, 256, 1.6f, 4.f);
+    const float eight = us(32, 32, 256, 256, 1.78f, 0.8f), wide = us(32, 64, 256, 256, 2.55f, 2.f);
+    const float thin = chunked ? a.m <= 16 ? 0.f : us(32, TRows, 64, 256, 0.2f, 0.5f) : big;
+    if (chunked && thin <= big && thin <= mid && thin <= four && thin <= eight && thin <= wide) {
+        L->variant = (a.m <= 16 ? 16 : 32) + 4096 * TRows;
+        return a.m <= 16 ? run_ffn_thin<Out, 1>(a, s) : run_ffn_thin<Out, 2>(a, s);
+    }
+    if (eight <= big && eight <= mid && eight <= four && eight <= wide) return run_ffn_waves<Out, 2, 2, 8>(a, s);
+    if (wide <= big && wide <= mid && wide <= four) return run_ffn_waves<Out, 2, 4, 8>(a, s);
+    if (four <= big && four <= mid) return run_ffn_waves<Out, 4, 4, 4>(a, s);
+    const TileArgs t{a.x, a.w, a.m, a.n, a.k, a.ldx / 4, a.ldw / 4, 0};
+    if (big <= mid) return run_tile<Out, TileShape<TF32, 4, 4, 1, 1>, true, true>(t, a, s);
+    if (!chunked) return run_tile<Out, TileShape<TF32, 2, 2, 1, 1>, true, true>(t, a, s);
+    using Z = PipeShape<2, 2, 2, 2, 2>;
+    L->variant = Z::BM + 4096 * Z::BN;
+    int64_t tiles = pipe_tiles<Out, Z>(a);
+    void* args[] = {const_cast<FfnArgs*>(&a), &tiles};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe_f32<Out, Z>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                           dim3(Z::THREADS), args, Z::LDS, s);
+}
+
+}  // namespace mmk

@@ -553,25 +553,22 @@ template <class Out>
 hipError_t run_ffn(const FfnArgs& a, hipStream_t s, Launched* L) {
     using E = typename Out::E;
     constexpr int es = sizeof(typename E::store_t);
-    const bool thin_f32 = a.m <= 64;  // f32 beyond: six bf16 products instead of f32 instructions
-    if constexpr (E::code != 3) {     // codes always are
-        if (!ffn_chunked(a, es) || (E::code == 0 && !thin_f32)) return run_ffn_tile<Out>(a, s);
+    static_assert(E::code != 0, "f32 has a choice of its own");
+    if constexpr (E::code != 3) {  // codes always are
+        if (!ffn_chunked(a, es)) return run_ffn_tile<Out>(a, s);
     }
     const int64_t rows = Out::kGated ? 2 * a.n : a.n;
-    const int form = E::code == 0 ? (a.m > 16) : ffn_form(a.m, rows, a.k * es);
+    const int form = ffn_form(a.m, rows, a.k * es);
     L->variant = kFfnForms[form].tokens + 4096 * kFfnForms[form].rows;
-    if (form == 0) return run_ffn_thin<Out, 1>(a, s);
-    if (form == 1) return run_ffn_thin<Out, 2>(a, s);
-    if constexpr (E::code != 0) {
-        switch (form) {
-            case 2: return run_ffn_pipe<Out, PipeShape<2, 2, 2, 2, 4>>(a, s);
-            case 3: return run_ffn_pipe<Out, PipeShape<2, 4, 2, 2, 4>>(a, s);
-            case 4: return run_ffn_pipe<Out, PipeShape<2, 4, 4, 2, 4>>(a, s);
-            case 5: return run_ffn_pipe<Out, PipeShape<4, 2, 4, 4, 3>>(a, s);
-            default: return run_ffn_pipe_halves<Out, PipeShape<2, 4, 8, 4, 2>, PipeShape<4, 2, 4, 4, 3>>(a, s);
-        }
+    switch (form) {
+        case 0: return run_ffn_thin<Out, 1>(a, s);
+        case 1: return run_ffn_thin<Out, 2>(a, s);
+        case 2: return run_ffn_pipe<Out, PipeShape<2, 2, 2, 2, 4>>(a, s);
+        case 3: return run_ffn_pipe<Out, PipeShape<2, 4, 2, 2, 4>>(a, s);
+        case 4: return run_ffn_pipe<Out, PipeShape<2, 4, 4, 2, 4>>(a, s);
+        case 5: return run_ffn_pipe<Out, PipeShape<4, 2, 4, 4, 3>>(a, s);
+        default: return run_ffn_pipe_halves<Out, PipeShape<2, 4, 8, 4, 2>, PipeShape<4, 2, 4, 4, 3>>(a, s);
     }
-    return hipErrorInvalidValue;
 }
 
 }  // namespace mmk

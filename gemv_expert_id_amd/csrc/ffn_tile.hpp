@@ -341,27 +341,27 @@ hipError_t run_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
 // 256 with four groups) costs in us, for each iteration over k and at its start.
 // From 130 products of each type and layout, in every form; the form with the lowest
 // sum of rounds is within 2% (16-bit rows any way stored: 5%) of the fastest in the
-// mean. Both sides of some borders, us: gated f32, 4172 x 1792 over 576, 128 x 128
-// 63, 64 x 64 81; 71 x 1664 over 640, 32 x 64 9.3, 64 x 64 13.6; 951 x 640 over 1518,
-// 64 x 64 with four groups 29.4, 32 x 64 36.4, 64 x 64 with one 43.6. Others: 25 x 377
-// over 20864 f32, 32 x 32 156, 32 x 64 248; 3 x 3456 over 3200 bf16, two steps an
-// iteration 14.3, one 20.5; gated 2 x 24192 over 2503 bf16, 48.8 and 37.1.
+// mean. Both sides of some borders, us: 25 x 377 over 20864 f32, 32 x 32 156, 32 x 64
+// 248; 3 x 3456 over 3200 bf16, two steps an iteration 14.3, one 20.5; gated 2 x 24192
+// over 2503 bf16, 48.8 and 37.1. (Gated f32 has its own choice in ffn_f32.hpp.)
 template <class Out, bool AK, bool BK>
 hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     using T = typename Out::E;
     constexpr bool F32 = kParts<T> == 3, ROWS = AK && BK;
-    using Big = TileShape<T, 4, F32 && !ROWS ? 2 : 4, F32 ? 1 : 2, 1>;
+    static_assert(!(F32 && ROWS), "f32 rows have a choice of their own");
+    using Big = TileShape<T, 4, F32 ? 2 : 4, F32 ? 1 : 2, 1>;
     using Mid = TileShape<T, 2, 2, 1, 1>;
     using Deep = TileShape<T, 2, 2, 1, 4>;
     using Low = TileShape<T, 1, 2, 1, 4>;
     using Long = TileShape<T, 1, 2, F32 ? 1 : 2, 4>;
-    constexpr float big = F32 ? (ROWS ? 3.0f : 1.7f) : (ROWS ? 1.6f : 1.4f);
-    constexpr float mid = F32 ? (ROWS ? 1.17f : 1.3f) : (ROWS ? 0.42f : 0.36f);
-    constexpr float deep = F32 ? (ROWS ? 2.5f : 3.5f) : (ROWS ? 1.5f : 1.36f);
-    constexpr float low = F32 ? (ROWS ? 1.55f : 2.4f) : (ROWS ? 0.91f : 0.96f);
+    constexpr float big = F32 ? 1.7f : (ROWS ? 1.6f : 1.4f);
+    constexpr float mid = F32 ? 1.3f : (ROWS ? 0.42f : 0.36f);
+    constexpr float deep = F32 ? 3.5f : (ROWS ? 1.5f : 1.36f);
+    constexpr float low = F32 ? 2.4f : (ROWS ? 0.91f : 0.96f);
     const int64_t outs = Out::kGated ? 2 * t.n : t.n;
     const auto us = [&](int bm, int bn, int kt, int at_a_time, float step, float start) {
         const int64_t tiles = ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn);
+        if (bm < 128 && tiles >= (1 << 22)) return 3e38f;  // (a grid holds fewer than 2^32 threads)
         return (float)((tiles + at_a_time - 1) / at_a_time) * ((float)((t.k + kt - 1) / kt) * step + start);
     };
     if constexpr (!Out::kGated) {  // the narrowest while CUs are left

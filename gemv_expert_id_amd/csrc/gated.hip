@@ -1,6 +1,6 @@
 // Gated feed-forward block: h = act(x G^T) * (x U^T), and the gradients of its
 // pre-activations (mm.h, "Feed-forward block").
-#include "ffn_pipe.hpp"
+#include "ffn_f32.hpp"
 
 namespace mmk {
 
@@ -223,14 +223,14 @@ hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
 
 hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_GATED;
-    return a.dtype == 0   ? run_ffn<GatedOut<TF32>>(a, s, L)
+    return a.dtype == 0   ? run_ffn_f32<GatedOut<TF32>>(a, s, L)
            : a.dtype == 1 ? run_ffn<GatedOut<TF16>>(a, s, L)
                           : run_ffn<GatedOut<TBF16>>(a, s, L);
 }
 
 hipError_t launch_gated_again(const FfnArgs& a, hipStream_t s, Launched* L) {
     L->kernel = MM_KERNEL_GATED_GRAD;
-    return a.dtype == 0   ? run_ffn<GradOut<TF32>>(a, s, L)
+    return a.dtype == 0   ? run_ffn_f32<GradOut<TF32>>(a, s, L)
            : a.dtype == 1 ? run_ffn<GradOut<TF16>>(a, s, L)
                           : run_ffn<GradOut<TBF16>>(a, s, L);
 }
