@@ -6,14 +6,21 @@
 
 namespace mmk {
 
-__device__ __forceinline__ void part8(const u32x4 (&r)[2], u32x4 (&out)[3]) {
-    float e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(r[i / 4][i % 4]);
+// The five small products, smallest first: parts of w and of x.
+constexpr int kPartW[5] = {2, 0, 1, 1, 0}, kPartX[5] = {0, 2, 1, 0, 1};
+
+__device__ __forceinline__ void part8(const float (&e)[8], u32x4 (&out)[3]) {
     uint32_t w[3][4];
     parts_of<TF32, 8>(e, w);
 #pragma unroll
     for (int q = 0; q < 3; ++q) out[q] = u32x4{w[q][0], w[q][1], w[q][2], w[q][3]};
+}
+
+__device__ __forceinline__ void part8(const u32x4 (&r)[2], u32x4 (&out)[3]) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(r[i / 4][i % 4]);
+    part8(e, out);
 }
 
 // One step of 32 of k: the six products of FM x FN fragments. `x(i, f)` and `w(j, f)`
@@ -35,11 +42,10 @@ struct PartsAcc {
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             w(j, fw);
-            constexpr int PW[5] = {2, 0, 1, 1, 0}, PX[5] = {0, 2, 1, 0, 1};  // smallest first
 #pragma unroll
             for (int q = 0; q < 5; ++q)
 #pragma unroll
-                for (int i = 0; i < FM; ++i) low[i][j] = step_mma<TBF16>(fw[PW[q]], fx[i][PX[q]], low[i][j]);
+                for (int i = 0; i < FM; ++i) low[i][j] = step_mma<TBF16>(fw[kPartW[q]], fx[i][kPartX[q]], low[i][j]);
 #pragma unroll
             for (int i = 0; i < FM; ++i) acc[i][j] = step_mma<TBF16>(fw[0], fx[i][0], acc[i][j]);
         }

@@ -337,27 +337,24 @@ hipError_t run_tile(TileArgs t, const FfnArgs& o, hipStream_t s) {
                            Z::BUF * Z::BYTES, s);
 }
 
-// The forms: 32 FM x 32 FN tiles, SUB steps, KS groups; and what a round of 512 (of
-// 256 with four groups) costs in us, for each iteration over k and at its start.
-// From 130 products of each type and layout, in every form; the form with the lowest
-// sum of rounds is within 2% (16-bit rows any way stored: 5%) of the fastest in the
-// mean. Both sides of some borders, us: 25 x 377 over 20864 f32, 32 x 32 156, 32 x 64
-// 248; 3 x 3456 over 3200 bf16, two steps an iteration 14.3, one 20.5; gated 2 x 24192
-// over 2503 bf16, 48.8 and 37.1. (Gated f32 has its own choice in ffn_f32.hpp.)
+// The forms of 16-bit elements: 32 FM x 32 FN tiles, SUB steps, KS groups; and what a
+// round of 512 (of 256 with four groups) costs in us, for each iteration over k and at
+// its start. From 130 products of each layout in every form; the form with the lowest
+// sum of rounds is within 5% of the fastest in the mean. Both sides of some borders, us:
+// 3 x 3456 over 3200 bf16, two steps an iteration 14.3, one 20.5; gated 2 x 24192 over
+// 2503 bf16, 48.8 and 37.1. (f32 has choices of its own: ffn_f32.hpp, ffn_strided.hpp.)
 template <class Out, bool AK, bool BK>
 hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     using T = typename Out::E;
-    constexpr bool F32 = kParts<T> == 3, ROWS = AK && BK;
-    static_assert(!(F32 && ROWS), "f32 rows have a choice of their own");
-    using Big = TileShape<T, 4, F32 ? 2 : 4, F32 ? 1 : 2, 1>;
+    static_assert(T::code != 0, "16 bits");
+    constexpr bool ROWS = AK && BK;
+    using Big = TileShape<T, 4, 4, 2, 1>;
     using Mid = TileShape<T, 2, 2, 1, 1>;
     using Deep = TileShape<T, 2, 2, 1, 4>;
     using Low = TileShape<T, 1, 2, 1, 4>;
-    using Long = TileShape<T, 1, 2, F32 ? 1 : 2, 4>;
-    constexpr float big = F32 ? 1.7f : (ROWS ? 1.6f : 1.4f);
-    constexpr float mid = F32 ? 1.3f : (ROWS ? 0.42f : 0.36f);
-    constexpr float deep = F32 ? 3.5f : (ROWS ? 1.5f : 1.36f);
-    constexpr float low = F32 ? 2.4f : (ROWS ? 0.91f : 0.96f);
+    using Long = TileShape<T, 1, 2, 2, 4>;
+    constexpr float big = ROWS ? 1.6f : 1.4f, mid = ROWS ? 0.42f : 0.36f;
+    constexpr float deep = ROWS ? 1.5f : 1.36f, low = ROWS ? 0.91f : 0.96f;
     const int64_t outs = Out::kGated ? 2 * t.n : t.n;
     const auto us = [&](int bm, int bn, int kt, int at_a_time, float step, float start) {
         const int64_t tiles = ((t.m + bm - 1) / bm) * ((outs + bn - 1) / bn);
@@ -366,11 +363,11 @@ hipError_t run_ffn_tile(const TileArgs& t, const FfnArgs& o, hipStream_t s) {
     };
     if constexpr (!Out::kGated) {  // the narrowest while CUs are left
         if (((t.m + 31) / 32) * ((t.n + 31) / 32) <= 256)
-            return run_tile<Out, TileShape<T, 1, 1, F32 ? 1 : 2, 4>, AK, BK>(t, o, s);
+            return run_tile<Out, TileShape<T, 1, 1, 2, 4>, AK, BK>(t, o, s);
     }
     const bool few = ((t.m + 31) / 32) * ((outs + 63) / 64) <= 256;
-    const float b = us(Big::BM, Big::BN, Big::KT, 512, big, 5.f), m = us(64, 64, 32, 512, mid, 1.5f);
-    const float d = us(64, 64, 128, 256, deep, 1.4f), l = few && !F32 ? us(32, 64, 256, 256, 1.3f, 1.4f) : us(32, 64, 128, 256, low, 1.4f);
+    const float b = us(128, 128, 64, 512, big, 5.f), m = us(64, 64, 32, 512, mid, 1.5f), d = us(64, 64, 128, 256, deep, 1.4f);
+    const float l = few ? us(32, 64, 256, 256, 1.3f, 1.4f) : us(32, 64, 128, 256, low, 1.4f);
     if (b <= m && b <= d && b <= l) return run_tile<Out, Big, AK, BK>(t, o, s);
     if (m <= d && m <= l) return run_tile<Out, Mid, AK, BK>(t, o, s);
     if (d <= l) return run_tile<Out, Deep, AK, BK>(t, o, s);

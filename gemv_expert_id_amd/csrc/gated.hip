@@ -1,6 +1,6 @@
 // Gated feed-forward block: h = act(x G^T) * (x U^T), and the gradients of its
 // pre-activations (mm.h, "Feed-forward block").
-#include "ffn_f32.hpp"
+#include "ffn_strided.hpp"
 
 namespace mmk {
 
@@ -216,9 +216,8 @@ hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
                               : long_product<TBF16>(o, s);
     if (chunked && tiles > 64)
         return g.dtype == 1 ? chunked_product<TF16>(g, o, tiles, s) : chunked_product<TBF16>(g, o, tiles, s);
-    return g.dtype == 0   ? tile_product<TF32>(g, o, s)
-           : g.dtype == 1 ? tile_product<TF16>(g, o, s)
-                          : tile_product<TBF16>(g, o, s);
+    if (g.dtype == 0) return g.ta ? run_f32_product<true>(o, s) : run_f32_product<false>(o, s);
+    return g.dtype == 1 ? tile_product<TF16>(g, o, s) : tile_product<TBF16>(g, o, s);
 }
 
 hipError_t launch_gated(const FfnArgs& a, hipStream_t s, Launched* L) {

@@ -384,6 +384,14 @@ def test_gated_forms_f32(m, n, k):
     check_gated(0, m, n, k, gate=GATES[m % 2], pad=4)
     check_grad(0, m, n, k, gate=GATES[m % 2], saved=False, want=())
 
+# Products of f32 gradients: 16, 32 and 64 rows at a time, columns that no four fill, fewer than four of them, contractions
+# that end inside a step.
+@pytest.mark.parametrize("m,n,k", [(1, 33, 3), (3, 520, 5), (40, 600, 6), (40, 600, 65), (70, 700, 700), (33, 300, 4099), (130, 1001, 500), (200, 1500, 130),
+                                   (300, 130, 1030), (1024, 70, 67), (1029, 250, 301), (2001, 300, 500), (2100, 2, 3), (2100, 1, 70), (600, 9, 40), (1500, 700, 97)])
+def test_f32_gradients(m, n, k):
+    check_grad(0, m, n, k, gate=GATES[m % 2], pad=m % 3, shift=n % 2)
+
+
 def f32_form(m, n, k, chunked):
     """The choice among f32's forms, from their measured costs."""
     up = lambda a, b: -(-a // b)  # noqa: E731
