@@ -165,24 +165,29 @@ hipError_t pipe_product(const GemmArgs& g, const FfnArgs& o, hipStream_t s) {
     return g.ta ? run_ffn_pipe<PlainOut<T>, Z, false, false>(o, s) : run_ffn_pipe<PlainOut<T>, Z, true, false>(o, s);
 }
 // 16-byte pieces in both operands: 128 x 128 tiles by one block a CU while there are no
-// more of them than CUs, by two up to 1024, 256 x 128 tiles beyond (us, bf16: 1024 x
-// 4096 over 8192, 256 tiles, 73.7 and 111; 3001 x 2048 over 2816, 46.3, 42.0 and 42.1;
-// 8192 x 8192 over 8192, 1101, 1031 and 910).
+// more of them than CUs, by two beyond; 256 x 128 tiles where they make one round that
+// fills more than half of the CUs (`one_round`) or many, over a long contraction (us,
+// f16: 1024 x 4096 over 4096, 256 tiles of 128 x 128, 35.8, 45.5 and 51.0; 2816 x 2048 over 3001
+// transposed, 352, 56.8, 50.1 and 45.4; 11008 x 2048 over 512, 1376, 52.3, 40.7 and 45.2;
+// over 4096, 225, 201 and 188).
 template <class T>
-hipError_t chunked_product(const GemmArgs& g, const FfnArgs& o, int64_t tiles, hipStream_t s) {
+hipError_t chunked_product(const GemmArgs& g, const FfnArgs& o, int64_t tiles, bool one_round, hipStream_t s) {
     if (tiles <= 256) return pipe_product<T, PipeShape<2, 4, 4, 2, 4>>(g, o, s);
-    if (tiles <= 1024) return pipe_product<T, PipeShape<2, 4, 4, 2, 2>>(g, o, s);
-    return pipe_product<T, PipeShape<4, 2, 4, 4, 3>>(g, o, s);
+    if (one_round || (tiles > 1024 && g.k >= 2048)) return pipe_product<T, PipeShape<4, 2, 4, 4, 3>>(g, o, s);
+    return pipe_product<T, PipeShape<2, 4, 4, 2, 2>>(g, o, s);
 }
 
 }  // namespace
 
 // dpre . w (both as stored: NN) or dpre^T . x (TN). Products whose contraction the
 // pipelined GEMM takes whole go to it, and large TN ones of any contraction (it reads
-// zeros past the end); others take the forms here: pipelined ones where rows hold
-// whole 16-byte pieces and 128 x 128 tiles are more than 64, tiles of any alignment
-// else (us, bf16: 512 x 2048 over 2816, 64 tiles, 20.1 in those against 22.4 pipelined
-// and 20.5 by the GEMM; 2816 x 2048 over 3001, 352 tiles, 89 against 46).
+// zeros past the end), unless the tiles here leave fewer CUs idle in their last round;
+// others take the forms here: pipelined ones where rows hold whole 16-byte pieces and
+// 128 x 128 tiles are more than 64, tiles of any alignment else. us, f16, GEMM and here:
+// 4096 x 4096 over 4096, 111 and 129; 3001 x 2048 over 2816, 48.6 and 42.2, over 11008,
+// 177 and 136; 11008 x 2048 over 1024 transposed, 344 tiles of 256 x 256, 75.5 and 66.5,
+// 22016 x 4096 over 4096, 1376 tiles, 710 and 810;
+// 512 x 2048 over 2816, 64 tiles, any alignment 20.1, pipelined 22.4, GEMM 20.5.
 hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
     const auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const int64_t es = g.dtype == 0 ? 4 : 2;
@@ -194,7 +199,12 @@ hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
     const bool gemm = chunked && (reinterpret_cast<uintptr_t>(g.C) & 7) == 0 && g.ldc % 4 == 0 &&
                       span_a < (1ll << 30) && span_b < (1ll << 30);
     const bool whole = g.k % 128 == 0 && g.k >= 256;
-    if (gemm && tiles > 64 && (whole || (g.ta && ((g.m + 255) / 256) * ((g.n + 255) / 256) >= 192))) {
+    // Rounds of 256 x 256 tiles (one costs 1.7 to 1.9 of the other) and of 256 x 128 tiles.
+    const int64_t tall = (g.m + 255) / 256, squares = tall * ((g.n + 255) / 256), halves = tall * ((g.n + 127) / 128);
+    const bool one_round = halves > 128 && halves <= 256 && g.k >= 1024;
+    const bool fuller = (squares > 128 && 10 * ((halves + 255) / 256) < 17 * ((squares + 255) / 256)) ||
+                        (one_round && !g.ta && g.k >= 2048);
+    if (gemm && tiles > 64 && !fuller && (whole || (g.ta && squares >= 192))) {
         GemmArgs q = g;
         q.ragged_k = 1;
         return launch_gemm(q, s, L);
@@ -215,7 +225,8 @@ hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
                : g.dtype == 1 ? long_product<TF16>(o, s)
                               : long_product<TBF16>(o, s);
     if (chunked && tiles > 64)
-        return g.dtype == 1 ? chunked_product<TF16>(g, o, tiles, s) : chunked_product<TBF16>(g, o, tiles, s);
+        return g.dtype == 1 ? chunked_product<TF16>(g, o, tiles, one_round, s)
+                            : chunked_product<TBF16>(g, o, tiles, one_round, s);
     if (g.dtype == 0) return g.ta ? run_f32_product<true>(o, s) : run_f32_product<false>(o, s);
     return g.dtype == 1 ? tile_product<TF16>(g, o, s) : tile_product<TBF16>(g, o, s);
 }
