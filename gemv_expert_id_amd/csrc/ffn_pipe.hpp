@@ -42,7 +42,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 // ---------------------------------------------------------------------------
 // Few tokens: 16 FM tokens by 16 rows of W, the contraction in stages of 256 bytes.
 //
-// W is read once, 256 contiguous bytes of a row at a time, and the tokens' pieces
+// Bound by memory. W is read once, 256 contiguous bytes of a row at a time, and the tokens' pieces
 // with it (from L2). A stage is four steps of matrix instructions, one for each
 // wave; the waves' sums are joined through LDS at the end. So narrow a tile keeps
 // many blocks in flight: one token through 22016 x 4096 takes 36.1 us in bf16 (5.0
@@ -194,6 +194,12 @@ __global__ __launch_bounds__(64 * TWaves) void ffn_thin(FfnArgs a, int tiles_m) 
 // frees its region for the pair NREG later, whose loads go out between the matrix
 // instructions of the next two half steps. Gated, a wave's rows of W are half gate,
 // half up projection, so an output's two sums end in one lane.
+//
+// The largest tile, 8 waves of 128 x 64, is bound by LDS and power together: a pair is
+// 2048 cycles of matrix instructions and, at 128 bytes a cycle, 1536 of fragment reads
+// and 512 of loads, at 1750 to 2050 MHz under this load. 8192 x 8192 over 8192: 808 us in
+// bf16 (1360 TFLOP/s), 461 in codes (2390 TOP/s). Few tiles are bound by memory: 48 tokens
+// by 22016 x 4096 bf16 take 43.5 us, 4.2 TB/s.
 //
 // XK, WK = false (16-bit gradients' products): the operand is stored with the
 // contraction along its rows, element (i, p) at p * ld + i. Its region holds the
@@ -446,7 +452,7 @@ __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe
 
 // `whole` tiles (a multiple of the CUs) in shape Z, the tiles after them as two of H
 // each: a last round that would leave more than half of the CUs idle takes 0.6 of its
-// time (4096 x 22016 over 4096 bf16, 1376 tiles: 661 -> 615 us).
+// time (4096 x 22016 over 4096 bf16, 1376 tiles: 661 -> 637 us).
 template <class Out, class Z, class H>
 __global__ __launch_bounds__(Z::THREADS, Z::BLOCKS * Z::WAVES / 4) void ffn_pipe_halves(FfnArgs a, int64_t whole,
                                                                                      int64_t halves) {

@@ -20,6 +20,10 @@
 // sums are not stored); elements of k past the end are zeros in both operands. A piece
 // that passes an end is fetched from where it still lies inside and moved up in
 // registers, so that edges cost no loads of single elements.
+//
+// Large f32 products are bound by the matrix units: 4096 x 8192 over 4096 takes 1392 us,
+// 197 TFLOP/s, 1180 of bf16 products; rows of 16 bits that no pipelined form takes by
+// the staging through registers (2000 x 4100 over 10000 bf16 470 us, 348 TFLOP/s).
 #pragma once
 
 #include "ffn.hpp"
