@@ -425,7 +425,6 @@ def test_f32_forms(m, n, k):
     assert check_grad(0, m, n, k, gate=GATES[m % 2], saved=False, pad=3, shift=1, want=()).variant == 0
 
 
-
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("m,n,k", [(1, 64, 96), (2, 128, 256), (37, 64, 96), (129, 128, 512), (300, 260, 264), (511, 192, 2040),
                                    (1025, 516, 72), (2, 4096, 2048), (700, 1024, 1032)])
@@ -441,3 +440,74 @@ def test_any_alignment_large_tiles(dt, m, n, k):
     check_gated(dt, m, n, k, pad=1)
     check_grad(dt, m, n, k, pad=1, saved=False)
     check_grad(dt, m, n, k, gate=ref.GELU)
+
+
+# ---- far offsets ------------------------------------------------------------------
+# Rows so far apart that the last ones lie past 2^32 bytes: just inside the pitches of the pipelined forms (below 4 MiB), and
+# beyond them.
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("pitch,m,n,k", [((1 << 22) - 16, 1050, 530, 72), (1 << 24, 270, 140, 40), ((1 << 24) + 12, 265, 135, 33)])
+def test_far_rows(dt, pitch, m, n, k):
+    z = torch.finfo(TORCH[dt]).bits // 8
+    check_gated(dt, m, n, k, pad=pitch // z - k)
+    torch.cuda.empty_cache()
+    check_grad(dt, m, n, k, pad=pitch // z - 2 * n, want=("dx",))
+    torch.cuda.empty_cache()
+    check_grad(dt, m, n, k, pad=pitch // z - 2 * n, saved=False, want=("dw",))
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_far_rows_few(dt):
+    z = torch.finfo(TORCH[dt]).bits // 8
+    check_gated(dt, 9, 530, 72, pad=((1 << 22) - 16) // z - 72)  # few tokens
+    check_grad(dt, 9, 530, 33, pad=(1 << 22) // z, want=("dx",))  # a contraction split over waves
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+def test_far_codes(dt):
+    z = torch.finfo(TORCH[dt]).bits // 8
+    check_quant(dt, 270, 1000, ldx=(1 << 24) // z, ldq=(1 << 24) + 5)
+    check_i8(dt, 1050, 1060, 80, pad=(1 << 22) - 96, ypad=(1 << 22) // z)
+    torch.cuda.empty_cache()
+
+
+# ---- values that are not finite ------------------------------------------------------
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k,pad", [(9, 40, 72, 8), (70, 70, 264, 8), (70, 70, 264, 1), (200, 600, 700, 4), (67, 3656, 196, 4), (300, 1409, 72, 8),
+                                       (513, 1411, 40, 1), (1037, 2900, 300, 4)])
+def test_rows_that_are_not_finite(dt, m, n, k, pad):
+    """A NaN or an infinity stays in its token's row and in its weight's column."""
+    t = TORCH[dt]
+    x, w = gated_operands(dt, m, n, k, pad, 0)
+    x.t[3, k // 2] = float("nan")
+    x.t[m - 1, 0] = float("inf")
+    w.t[5, k - 1] = float("nan")
+    h, pre = Rows(m, n, t, n), Rows(m, 2 * n, t, 2 * n)
+    mm.mm_gated(mm.gated_params(dt, m, n, k, ldx=x.ld, ldw=w.ld), x.buf, w.buf, h.buf, pre.buf, stream=stream())
+    token = torch.zeros(m, 1, dtype=torch.bool, device=DEV)
+    token[3] = token[m - 1] = True
+    column = torch.zeros(1, 2 * n, dtype=torch.bool, device=DEV)
+    column[0, 5] = True
+    assert torch.equal(~pre.t.isfinite(), token | column)
+    assert torch.equal(~h.t.isfinite(), token | column[:, :n])
+
+
+def test_gradient_rows_that_are_not_finite():
+    """dx: a token's row alone; dw: a pre-activation's row alone."""
+    for dt, m, n, k in ((0, 70, 40, 60), (0, 20, 700, 40), (0, 300, 130, 257), (0, 1030, 70, 130), (1, 70, 40, 60), (2, 300, 192, 264), (2, 20, 700, 40)):
+        t = TORCH[dt]
+        x, w = gated_operands(dt, m, n, k, 0, 0)
+        pre, dh = Rows(m, 2 * n, t, 2 * n, value=randn(1, m, 2 * n)), Rows(m, n, t, n, value=randn(2, m, n))
+        dh.t[7, 2] = float("nan")
+        dpre, dx, dw = Rows(m, 2 * n, t, 2 * n), Rows(m, k, t, k), Rows(2 * n, k, t, k)
+        mm.mm_gated_grad(mm.gated_params(dt, m, n, k), x.buf, w.buf, pre.buf, dh.buf, dpre.buf, dx.buf, dw.buf, stream=stream())
+        for got, rows in ((dx.t, [7]), (dw.t, [2, n + 2])):
+            want = torch.zeros(got.shape[0], 1, dtype=torch.bool, device=DEV)
+            want[rows] = True
+            assert torch.equal(got.isnan(), want.expand_as(got))
