@@ -55,8 +55,9 @@ struct PartsAcc {
 // ---------------------------------------------------------------------------
 // Rows of whole 16-byte chunks through the regions of ffn_pipe, two of them (a pair's
 // 128 bytes are one step): LDS holds the raw 4 bytes an element, loads go there without
-// a register, and each wave parts the fragments that it reads. Three blocks of 64 x 64
-// share a CU: one's loads and barriers fall into the others' arithmetic.
+// a register, and each wave parts the fragments that it reads. Blocks share a CU: one's
+// loads and barriers fall into the others' arithmetic. Bound by vector issue: parting is
+// 176 of the 211 vector instructions a wave issues for 24 matrix instructions.
 // ---------------------------------------------------------------------------
 #define MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 template <class Out, class Z>
@@ -215,6 +216,14 @@ __global__ __launch_bounds__(64 * KS, 2) void ffn_waves_f32(FfnArgs a, int64_t t
     }
 }
 
+template <class Out, class Z>
+hipError_t run_pipe_f32(const FfnArgs& a, hipStream_t s, Launched* L) {
+    L->variant = Z::BM + 4096 * Z::BN;
+    int64_t tiles = pipe_tiles<Out, Z>(a);
+    void* args[] = {const_cast<FfnArgs*>(&a), &tiles};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe_f32<Out, Z>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                           dim3(Z::THREADS), args, Z::LDS, s);
+}
 template <class Out, int FM, int FN, int KS>
 hipError_t run_ffn_waves(const FfnArgs& a, hipStream_t s) {
     int64_t tiles = (a.m + 16 * FM - 1) / (16 * FM) * ((a.n + 8 * FN - 1) / (8 * FN));
@@ -226,12 +235,13 @@ hipError_t run_ffn_waves(const FfnArgs& a, hipStream_t s) {
 // The forms of f32 rows: tokens and rows of w of a tile, elements of k an iteration,
 // tiles at a time on the 256 CUs; and what a round of them costs in us, for each
 // iteration and at its start. From 150 products of 65 to 4096 tokens in every form; the
-// one with the lowest sum of rounds is within 4% of the fastest in the mean (9% where
+// one with the lowest sum of rounds is within 3% of the fastest in the mean (9% where
 // rows are not whole 16-byte chunks). Few tokens take f32 instructions, at 2/5 of the
 // rate of the six products but with nothing to part. Both sides of some borders, us:
 // 70 tokens by 1200 over 8000, thin 33.8, 32 x 32 57.3; 256 by the same, 32 x 64 86, thin
-// 98, 32 x 32 112; 70 by 2816 over 2048, thin 19.8, 32 x 64 25.3; 160 by 22016 over 4096,
-// 64 x 64 by four waves 259, through LDS 272, 128 x 128 311; 509 by 2816 over 2048, 64 x 64
+// 98, 32 x 32 112; 70 by 2816 over 2048, thin 19.8, 32 x 64 25.3; 70 by 24000 over
+// 1000, 64 x 64 by four waves 47.8, 64 x 128 49.7; 400 by 22016 over 4096, 64 x 128 455, 64 x 64
+// through LDS 537, by four waves 575, 128 x 128 548; 509 by 2816 over 2048, 64 x 64
 // through LDS 53.6, by four waves 61.8, 128 x 128 124; 4096 by 8192 over 4096, 128 x 128
 // 1392, 64 x 64 through LDS 1756.
 // Bound by arithmetic from 512 tokens on: 4096 x 8192 over 4096 runs at 197 TFLOP/s, six
@@ -247,8 +257,13 @@ hipError_t run_ffn_f32(const FfnArgs& a, hipStream_t s, Launched* L) {
     const float big = us(128, 128, 32, 512, 2.6f, 14.f);
     const float mid = chunked ? us(64, 64, 32, 512, 0.9f, 1.f) : us(64, 64, 32, 512, 1.2f, 3.f);
     const float four = us(64, 64, 128, 256, 1.6f, 4.f);
+    // A tile alone on its CU runs at 5/8 of the speed of two.
+    const bool pairs = (a.m + 63) / 64 * ((2 * a.n + 127) / 128) > 256;
+    const float broad = chunked && pairs ? us(64, 128, 32, 256, 0.74f, 2.f) : 3e38f;
     const float eight = us(32, 32, 256, 256, 1.78f, 0.8f), wide = us(32, 64, 256, 256, 2.55f, 2.f);
     const float thin = chunked ? a.m <= 16 ? 0.f : us(32, TRows, 64, 256, 0.2f, 0.5f) : big;
+    if (broad <= thin && broad <= big && broad <= mid && broad <= four && broad <= eight && broad <= wide)
+        return run_pipe_f32<Out, PipeShape<2, 2, 2, 4, 2>>(a, s, L);
     if (chunked && thin <= big && thin <= mid && thin <= four && thin <= eight && thin <= wide) {
         L->variant = (a.m <= 16 ? 16 : 32) + 4096 * TRows;
         return a.m <= 16 ? run_ffn_thin<Out, 1>(a, s) : run_ffn_thin<Out, 2>(a, s);
@@ -259,12 +274,7 @@ hipError_t run_ffn_f32(const FfnArgs& a, hipStream_t s, Launched* L) {
     const TileArgs t{a.x, a.w, a.m, a.n, a.k, a.ldx / 4, a.ldw / 4, 0};
     if (big <= mid) return run_tile<Out, TileShape<TF32, 4, 4, 1, 1>, true, true>(t, a, s);
     if (!chunked) return run_tile<Out, TileShape<TF32, 2, 2, 1, 1>, true, true>(t, a, s);
-    using Z = PipeShape<2, 2, 2, 2, 2>;
-    L->variant = Z::BM + 4096 * Z::BN;
-    int64_t tiles = pipe_tiles<Out, Z>(a);
-    void* args[] = {const_cast<FfnArgs*>(&a), &tiles};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_pipe_f32<Out, Z>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                           dim3(Z::THREADS), args, Z::LDS, s);
+    return run_pipe_f32<Out, PipeShape<2, 2, 2, 2, 2>>(a, s, L);
 }
 
 }  // namespace mmk

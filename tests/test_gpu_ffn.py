@@ -400,23 +400,25 @@ def f32_form(m, n, k, chunked):
              "waves 64 x 64": cost(64, 64, 128, 256, 1.6, 4.0), "128 x 128": cost(128, 128, 32, 512, 2.6, 14.0),
              "pipe" if chunked else "64 x 64": cost(64, 64, 32, 512, *((0.9, 1.0) if chunked else (1.2, 3.0)))}
     if chunked:
+        if up(m, 64) * up(2 * n, 128) > 256:
+            costs["broad"] = cost(64, 128, 32, 256, 0.74, 2.0)
         costs["thin"] = 0 if m <= 16 else cost(32, 16, 64, 256, 0.2, 0.5)
     return min(costs, key=costs.get)
 
 
 F32_SHAPES = [(16, 300, 200), (17, 130, 64), (141, 149, 952), (70, 40, 8), (99, 902, 224), (69, 2185, 196), (67, 3656, 196),
-              (70, 4105, 260), (300, 1409, 72), (513, 1411, 40), (1037, 2900, 300), (129, 4100, 130), (257, 2050, 131), (700, 4100, 33),
+              (70, 4105, 260), (300, 1409, 72), (513, 1411, 40), (1037, 2900, 300), (904, 3401, 520), (280, 3271, 204), (129, 4100, 130), (257, 2050, 131), (700, 4100, 33),
               (129, 90, 31), (65, 33, 1), (1100, 1985, 203)]
 
 
 def test_every_f32_form_is_reached():
-    assert {f32_form(*s, True) for s in F32_SHAPES if s[2] % 4 == 0} == {"thin", "waves 32 x 32", "waves 32 x 64", "waves 64 x 64", "128 x 128", "pipe"}
+    assert {f32_form(*s, True) for s in F32_SHAPES if s[2] % 4 == 0} == {"thin", "waves 32 x 32", "waves 32 x 64", "waves 64 x 64", "128 x 128", "pipe", "broad"}
     assert {f32_form(*s, False) for s in F32_SHAPES} == {"waves 32 x 32", "waves 32 x 64", "waves 64 x 64", "128 x 128", "64 x 64"}
 
 
 @pytest.mark.parametrize("m,n,k", F32_SHAPES)
 def test_f32_forms(m, n, k):
-    variant = {"thin": (16 if m <= 16 else 32) + 4096 * 16, "pipe": 64 + 4096 * 64}
+    variant = {"thin": (16 if m <= 16 else 32) + 4096 * 16, "pipe": 64 + 4096 * 64, "broad": 64 + 4096 * 128}
     if k % 4 == 0:
         want = variant.get(f32_form(m, n, k, True), 0)
         assert check_gated(0, m, n, k, gate=GATES[m % 2], pad=4).variant == want
