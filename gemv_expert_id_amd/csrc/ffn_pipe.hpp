@@ -45,7 +45,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 // Bound by memory. W is read once, 256 contiguous bytes of a row at a time, and the tokens' pieces
 // with it (from L2). A stage is four steps of matrix instructions, one for each
 // wave; the waves' sums are joined through LDS at the end. So narrow a tile keeps
-// many blocks in flight: one token through 22016 x 4096 takes 36.1 us in bf16 (5.0
+// many blocks in flight: one token through 22016 x 4096 takes 35.1 us in f16 (5.1
 // TB/s), 41.6 with 64 rows a block and unsplit steps; through 1024 x 8192, 10.3 and
 // 16.9. Chunk c of LDS row r lies at slot c ^ (r & 15), so the 16 rows of a fragment
 // read cover all banks.
@@ -525,21 +525,25 @@ hipError_t run_ffn_pipe_halves(const FfnArgs& a, hipStream_t s) {
 // tiles 44.2, 64 x 64 49.7, 128 x 128 45.5; 512 by 2816 x 2048 codes, 64 x 128 9.3,
 // 64 x 64 10.2, 128 x 128 13.2; 1024 by 22016 x 4096 bf16, 256 x 128 179, 256 x 256
 // 214; 2048 by the same, 349 and 323; 32 by 1152 x 1792 bf16, 32 x 16 6.1, 64 x 64 7.8.
+// Up to 16 tokens take the thinnest: 1 by 22016 x 4096 f16 35.1, 64 x 128 38.3; 1 by
+// 8192 x 11008, 38.5, 64 x 64 51; the one loss found is 16 by 28672 x 4096 codes, 25.7
+// and 24.7.
 struct FfnForm {
     int tokens, rows, at_a_time;
     float pair_us, round_us;
 };
 constexpr FfnForm kFfnForms[] = {
-    {16, 16, 768, 0.183f, 2.02f},  {32, 16, 512, 0.257f, 0.60f},   {64, 64, 256, 0.300f, 1.93f},
+    {16, 16, 0, 0.f, 0.f},         {32, 16, 512, 0.257f, 0.60f},   {64, 64, 256, 0.300f, 1.93f},
     {64, 128, 256, 0.320f, 2.26f}, {128, 128, 256, 0.607f, 2.15f}, {256, 128, 256, 0.956f, 3.35f},
     {256, 256, 256, 1.593f, 7.15f},
 };
 constexpr int kForms = sizeof kFfnForms / sizeof *kFfnForms;
 inline int ffn_form(int64_t m, int64_t rows, int64_t bytes) {
+    if (m <= 16) return 0;
     const float pairs = (float)((bytes + 127) / 128);
     int best = -1;
     float least = 0.f;
-    for (int i = m > 16 ? 1 : 0; i < kForms; ++i) {
+    for (int i = 1; i < kForms; ++i) {
         const FfnForm& f = kFfnForms[i];
         const int64_t tiles = ((m + f.tokens - 1) / f.tokens) * ((rows + f.rows - 1) / f.rows);
         const int64_t last = tiles % f.at_a_time;

@@ -324,7 +324,7 @@ def test_i8_largest_sums(m, n):
 # ---- the forms a product takes, by its size ------------------------------------------
 
 
-TILES = [(16, 16, 768, 0.183, 2.02), (32, 16, 512, 0.257, 0.60), (64, 64, 256, 0.300, 1.93), (64, 128, 256, 0.320, 2.26),
+TILES = [(16, 16, 0, 0, 0), (32, 16, 512, 0.257, 0.60), (64, 64, 256, 0.300, 1.93), (64, 128, 256, 0.320, 2.26),
          (128, 128, 256, 0.607, 2.15), (256, 128, 256, 0.956, 3.35), (256, 256, 256, 1.593, 7.15)]
 
 
@@ -339,7 +339,7 @@ def form(m, rows, row_bytes):
             us -= one - (up(row_bytes, 128) * TILES[-2][3] + TILES[-2][4])
         return us
 
-    f = min(TILES[1:] if m > 16 else TILES, key=cost)
+    f = min(TILES[1:], key=cost) if m > 16 else TILES[0]
     return f[0] + 4096 * f[1]
 
 
