@@ -54,7 +54,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 // projection: the two sums of an output end 32 lanes apart.
 // ---------------------------------------------------------------------------
 constexpr int TStage = 256;  // bytes of k a stage
-constexpr int TRing = 4;     // stages in LDS
 constexpr int TRows = 16;    // rows of W
 constexpr int TWaves = 4;    // one for each 64-byte step of a stage
 
@@ -73,7 +72,8 @@ __device__ __forceinline__ char* thin_stage() {
     return st;
 }
 
-template <class Out, int FM>
+// RING stages in LDS.
+template <class Out, int FM, int RING>
 __global__ __launch_bounds__(64 * TWaves) void ffn_thin(FfnArgs a, int tiles_m) {
     using E = typename Out::E;
     using Acc = typename AccOf<E>::type;
@@ -139,14 +139,14 @@ __global__ __launch_bounds__(64 * TWaves) void ffn_thin(FfnArgs a, int tiles_m) 
             }
         }
     };
-    ffn_for<TRing - 1>([&](auto S_) { issue(S_, decltype(S_)::value); });
-    for (int st = 0; st < stages; st += TRing) {
-        ffn_for<TRing>([&](auto S_) {
+    ffn_for<RING - 1>([&](auto S_) { issue(S_, decltype(S_)::value); });
+    for (int st = 0; st < stages; st += RING) {
+        ffn_for<RING>([&](auto S_) {
             constexpr int s = decltype(S_)::value;
             // Stage st + s has landed; the stage before it has been read by every wave.
-            __builtin_amdgcn_s_waitcnt(ffn_wait((TRing - 2) * Z::LOADS));
+            __builtin_amdgcn_s_waitcnt(ffn_wait((RING - 2) * Z::LOADS));
             __builtin_amdgcn_s_barrier();
-            issue(std::integral_constant<int, (s + TRing - 1) % TRing>{}, st + s + TRing - 1);
+            issue(std::integral_constant<int, (s + RING - 1) % RING>{}, st + s + RING - 1);
             compute(S_);
         });
     }
@@ -482,14 +482,24 @@ inline bool ffn_chunked(const FfnArgs& a, int es) {
            a.ldx < (1 << 22) && a.ldw < (1 << 22);
 }
 
+// 16 tokens: 8 stages in LDS from 32 on, unless the last turn of the ring would be more
+// than a twelfth in vain; 4 otherwise. us, 4 and 8: f16 1 by 8192 x 11008, 86 stages, 39.1
+// and 35.8; 1 by 1200 x 8000, 63, 10.7 and 7.8; f32 1 by 4096 x 8192, 128, 37.4 and 31.9;
+// codes 13 by 4099 x 11008, 43 in turns of 48, 11.3 and 13.2; 1 by 22016 x 4096, 16, 17.5 and
+// 20.2. 32 tokens, 8 stages of 12 KB: 32 by 22016 x 4096 f32 91.5 and 104.9.
 template <class Out, int FM>
 hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
-    constexpr int XR = ThinShape<FM>::XR, WO = Out::kGated ? TRows / 2 : TRows;
+    constexpr int XR = ThinShape<FM>::XR, WO = Out::kGated ? TRows / 2 : TRows, es = sizeof(typename Out::E::store_t);
     int tiles_m = (int)((a.m + XR - 1) / XR);
     const int64_t tiles = (int64_t)tiles_m * ((a.n + WO - 1) / WO);
     void* args[] = {const_cast<FfnArgs*>(&a), &tiles_m};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&ffn_thin<Out, FM>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                           dim3(64 * TWaves), args, 0, s);
+    const int64_t stages = (a.k * es + TStage - 1) / TStage;
+    const void* fn = reinterpret_cast<const void*>(&ffn_thin<Out, FM, 4>);
+    if constexpr (FM == 1) {
+        if (stages >= 32 && ((stages + 7) / 8 * 8 - stages) * 12 <= stages)
+            fn = reinterpret_cast<const void*>(&ffn_thin<Out, FM, 8>);
+    }
+    return hipLaunchKernel(fn, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * TWaves), args, 0, s);
 }
 
 template <class Out, class Z>

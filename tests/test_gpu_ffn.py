@@ -374,6 +374,16 @@ def test_long_contractions(dt, m, n, k):
     check_grad(dt, m, n, k, gate=GATES[m % 2], pad=n % 2, shift=k % 3, want=("dx",))
 
 
+# Up to 16 tokens: 4 or 8 stages of 256 bytes ahead, by their number (here in bytes of k).
+@pytest.mark.parametrize("row_bytes", [31 * 256, 32 * 256, 32 * 256 + 16, 33 * 256, 38 * 256 - 16, 40 * 256, 85 * 256 + 240, 96 * 256])
+@pytest.mark.parametrize("m,n", [(1, 33), (16, 8)])
+def test_stages(m, n, row_bytes):
+    for dt in DTYPES:
+        check_gated(dt, m, n, row_bytes // (2 if dt else 4), pad=8)
+    check_i8(m % 3, m, n, row_bytes, gate=ref.SILU)
+    check_i8(m % 3, m, 2 * n - 1, row_bytes, pad=16)
+
+
 @pytest.mark.parametrize("m,n,k", SHAPES)
 def test_gradient_forms(m, n, k):
     assert check_grad(1, m, n, k, gate=GATES[m % 2], saved=False, want=()).variant == form(m, 2 * n, 2 * k)
