@@ -482,11 +482,11 @@ inline bool ffn_chunked(const FfnArgs& a, int es) {
            a.ldx < (1 << 22) && a.ldw < (1 << 22);
 }
 
-// 16 tokens: 8 stages in LDS from 32 on, unless the last turn of the ring would be more
-// than a twelfth in vain; 4 otherwise. us, 4 and 8: f16 1 by 8192 x 11008, 86 stages, 39.1
+// 8 stages in LDS from 32 on, unless the last turn of the ring would be more than a
+// twelfth in vain or, of 32 tokens (12 KB a stage), CUs have more than a tile; 4 otherwise. us, 4 and 8: f16 1 by 8192 x 11008, 86 stages, 39.1
 // and 35.8; 1 by 1200 x 8000, 63, 10.7 and 7.8; f32 1 by 4096 x 8192, 128, 37.4 and 31.9;
 // codes 13 by 4099 x 11008, 43 in turns of 48, 11.3 and 13.2; 1 by 22016 x 4096, 16, 17.5 and
-// 20.2. 32 tokens, 8 stages of 12 KB: 32 by 22016 x 4096 f32 91.5 and 104.9.
+// 20.2; f32 32 by 4096 x 8192, 45.8 and 36.7, by 22016 x 4096 91.5 and 104.9.
 template <class Out, int FM>
 hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
     constexpr int XR = ThinShape<FM>::XR, WO = Out::kGated ? TRows / 2 : TRows, es = sizeof(typename Out::E::store_t);
@@ -495,10 +495,8 @@ hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
     void* args[] = {const_cast<FfnArgs*>(&a), &tiles_m};
     const int64_t stages = (a.k * es + TStage - 1) / TStage;
     const void* fn = reinterpret_cast<const void*>(&ffn_thin<Out, FM, 4>);
-    if constexpr (FM == 1) {
-        if (stages >= 32 && ((stages + 7) / 8 * 8 - stages) * 12 <= stages)
-            fn = reinterpret_cast<const void*>(&ffn_thin<Out, FM, 8>);
-    }
+    if (stages >= 32 && ((stages + 7) / 8 * 8 - stages) * 12 <= stages && (FM == 1 || tiles <= 256))
+        fn = reinterpret_cast<const void*>(&ffn_thin<Out, FM, 8>);
     return hipLaunchKernel(fn, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * TWaves), args, 0, s);
 }
 

@@ -374,9 +374,9 @@ def test_long_contractions(dt, m, n, k):
     check_grad(dt, m, n, k, gate=GATES[m % 2], pad=n % 2, shift=k % 3, want=("dx",))
 
 
-# Up to 16 tokens: 4 or 8 stages of 256 bytes ahead, by their number (here in bytes of k).
+# Few tokens: 4 or 8 stages of 256 bytes ahead, by their number (here in bytes of k).
 @pytest.mark.parametrize("row_bytes", [31 * 256, 32 * 256, 32 * 256 + 16, 33 * 256, 38 * 256 - 16, 40 * 256, 85 * 256 + 240, 96 * 256])
-@pytest.mark.parametrize("m,n", [(1, 33), (16, 8)])
+@pytest.mark.parametrize("m,n", [(1, 33), (16, 8), (30, 70)])
 def test_stages(m, n, row_bytes):
     for dt in DTYPES:
         check_gated(dt, m, n, row_bytes // (2 if dt else 4), pad=8)
