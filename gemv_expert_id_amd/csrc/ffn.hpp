@@ -144,8 +144,8 @@ struct GradOut {
     }
 };
 
-// Whole sums of codes, times the channel's scale, then the token's: the f32
-// product of a sum and a channel scale overflows only where the result does.
+// Whole sums of codes, rounded to f32, times the channel's scale, then the token's:
+// three roundings of 2^-24 before the gate or the output's own.
 template <class T, bool GATED>
 struct CodesOut {
     using E = TI8;

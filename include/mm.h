@@ -152,7 +152,7 @@ typedef struct {
                                  outputs of a block; for MM_KERNEL_GATED,
                                  MM_KERNEL_I8 and a recomputing MM_KERNEL_GATED_GRAD
                                  tokens of a tile plus 4096 times its rows of w, 0 for
-                                 the form that takes any alignment; 0 for every other family */
+                                 a form that takes any alignment; 0 for every other family */
 } mm_receipt;
 
 /* ------------------------------------------------------------------------ */
