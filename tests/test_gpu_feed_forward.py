@@ -100,7 +100,7 @@ def calls(dt, m, n, k, seed):
 
 
 @pytest.mark.parametrize("dt", [0, 1, 2])
-@pytest.mark.parametrize("m,n,k", [(1, 48, 64), (33, 200, 144), (200, 264, 400)])
+@pytest.mark.parametrize("m,n,k", [(1, 48, 64), (33, 200, 144), (200, 264, 400), (20, 700, 144), (280, 3272, 208), (1500, 1100, 1024)])
 def test_graph_replays_and_streams(dt, m, n, k):
     """Replays, with eager work between them, and runs on two other streams at once give the eager bits."""
     run, outs = calls(dt, m, n, k, 1)
