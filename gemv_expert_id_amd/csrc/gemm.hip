@@ -41,10 +41,11 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 // row]); out-of-range elements are zero.
 //
 // VEC (16-byte aligned chunks): one buffer load per chunk, unconditional, over
-// a resource that spans exactly the operand's valid elements, so chunks past
-// the last row (or k) read zero from the range check; the k (or row) tail of a
-// chunk that straddles the edge is masked when the chunk is stored (`nv` keeps
-// the valid count). Nothing touches a loaded value before the store, so the
+// a resource that spans the operand's valid elements, so chunks past the last
+// row (or k) read zero from the range check, and to the end of the four bytes
+// that hold the last one: the check drops four bytes that lie inside only in
+// part. The k (or row) tail of a chunk that straddles the edge is masked when
+// the chunk is stored (`nv` keeps the valid count). Nothing touches a loaded value before the store, so the
 // loads of several k-tiles stay in flight together.
 constexpr int GCH = (GBM * GBK / 8) / GThreads;  // chunks per thread per operand
 
@@ -64,8 +65,8 @@ __device__ __forceinline__ void fetch_tile(const uint16_t* __restrict__ base, in
                                            u32x4 (&v)[GCH], int (&nv)[GCH]) {
     const int tid = threadIdx.x;
     if constexpr (VEC) {
-        // Valid span: (nrows-1)*ld + K elements (KCONTIG) or (K-1)*ld + nrows.
-        const int64_t span = KCONTIG ? (nrows - 1) * ld + K : (K - 1) * ld + nrows;
+        // Valid span: (nrows-1)*ld + K elements (KCONTIG) or (K-1)*ld + nrows, to the next whole dword.
+        const int64_t span = ((KCONTIG ? (nrows - 1) * ld + K : (K - 1) * ld + nrows) + 1) / 2 * 2;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint16_t*>(base), (short)0, (int)(span * 2), 0x00020000);
 #pragma unroll
@@ -716,13 +717,15 @@ __device__ __forceinline__ bool pipelined_tile(const GemmArgs& a, int64_t& m0, i
 // Buffer resource over one operand's tile of batch item b: BM rows from row0
 // (K-contiguous: rows of k elements ld apart) or BM columns from column col0
 // of k rows ld apart (K-strided). With RAG the range stops at the operand's
-// true extent (`rows` of the BM inside it), so reads past it return zeros.
+// true extent (`rows` of the BM inside it), so reads past it return zeros; an
+// odd one at the end of its last dword, which the range check drops otherwise
+// (k is even where K-contiguous).
 template <int BM, bool KC, bool RAG>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t pipelined_rsrc(const void* base, int64_t batch_off,
                                                                  int64_t first, int64_t ld, int64_t k,
                                                                  int64_t rows) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + batch_off + (KC ? first * ld : first);
-    const int bytes = RAG ? (int)((KC ? (rows - 1) * ld + k : (k - 1) * ld + rows) * 2)
+    const int bytes = RAG ? (int)((KC ? (rows - 1) * ld + k : (k - 1) * ld + (rows + 1) / 2 * 2) * 2)
                           : (KC ? BM * (int)ld * 2 : (int)(((k - 1) * ld + BM) * 2));
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), (short)0, bytes, 0x00020000);
 }
