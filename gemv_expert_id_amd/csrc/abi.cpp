@@ -1168,16 +1168,17 @@ mm_status mm_gated_grad(const mm_gated_params* params, mm_buf x, mm_buf w, mm_bu
     if ((st = enqueue(pre.ptr ? mmk::launch_gated_grad(a, s, &L) : mmk::launch_gated_again(a, s, &L))) != MM_OK)
         return st;
     const int64_t n2 = 2 * a.n;
-    if (dx.ptr) {  // dx [m, k] = dpre [m, 2n] . w [2n, k]
+    const auto product = [&](const mmk::GemmArgs& p) {
         ++g_launches;
-        const mmk::GemmArgs p = rows_product(a.dtype, a.m, a.k, n2, false, dpre.ptr, a.ldpre, w.ptr, ldw, dx.ptr, ldx);
-        if ((st = enqueue(mmk::launch_gated_product(p, s, &L))) != MM_OK) return st;
-    }
-    if (dw.ptr) {  // dw [2n, k] = dpre [m, 2n]^T . x [m, k]
-        ++g_launches;
-        const mmk::GemmArgs p = rows_product(a.dtype, n2, a.k, a.m, true, dpre.ptr, a.ldpre, x.ptr, ldx, dw.ptr, ldw);
-        if ((st = enqueue(mmk::launch_gated_product(p, s, &L))) != MM_OK) return st;
-    }
+        L = mmk::Launched{};  // (the receipt names the last launch)
+        return enqueue(mmk::launch_gated_product(p, s, &L));
+    };
+    if (dx.ptr &&  // dx [m, k] = dpre [m, 2n] . w [2n, k]
+        (st = product(rows_product(a.dtype, a.m, a.k, n2, false, dpre.ptr, a.ldpre, w.ptr, ldw, dx.ptr, ldx))) != MM_OK)
+        return st;
+    if (dw.ptr &&  // dw [2n, k] = dpre [m, 2n]^T . x [m, k]
+        (st = product(rows_product(a.dtype, n2, a.k, a.m, true, dpre.ptr, a.ldpre, x.ptr, ldx, dw.ptr, ldw))) != MM_OK)
+        return st;
     set_receipt(receipt, MM_ROUTE_GATED, (uint32_t)a.dtype, launches, L);
     return ok();
 }

@@ -114,8 +114,9 @@ typedef enum {
     MM_KERNEL_COMBINE_GRAD = 19,     /* its gradients */
     MM_KERNEL_Q4 = 20,               /* 4-bit weights on MFMA */
     MM_KERNEL_GATED = 21,            /* both projections and the gate */
-    MM_KERNEL_GATED_GRAD = 22,       /* gradients of the pre-activations; a call that also makes
-                                        products reports the kernel of the last one */
+    MM_KERNEL_GATED_GRAD = 22,       /* gradients of the pre-activations, and those of x and w; a
+                                        call that makes these products reports the kernel of the
+                                        last one: this, or MM_KERNEL_GEMM_LARGE */
     MM_KERNEL_I8_QUANT = 23,         /* rows to 8-bit codes */
     MM_KERNEL_I8 = 24                /* products of 8-bit codes */
 } mm_kernel;
@@ -150,9 +151,10 @@ typedef struct {
                                  in the same launch; for MM_KERNEL_Q4 the
                                  tokens of a tile (4 or 16) plus 256 times the
                                  outputs of a block; for MM_KERNEL_GATED,
-                                 MM_KERNEL_I8 and a recomputing MM_KERNEL_GATED_GRAD
-                                 tokens of a tile plus 4096 times its rows of w, 0 for
-                                 a form that takes any alignment; 0 for every other family */
+                                 MM_KERNEL_I8 and an MM_KERNEL_GATED_GRAD whose call
+                                 recomputes and makes no products, tokens of a tile
+                                 plus 4096 times its rows of w, 0 for a form that
+                                 takes any alignment; 0 for every other family */
 } mm_receipt;
 
 /* ------------------------------------------------------------------------ */
