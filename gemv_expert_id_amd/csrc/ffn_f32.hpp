@@ -9,18 +9,18 @@ namespace mmk {
 // The five small products, smallest first: parts of w and of x.
 constexpr int kPartW[5] = {2, 0, 1, 1, 0}, kPartX[5] = {0, 2, 1, 0, 1};
 
-__device__ __forceinline__ void part8(const float (&e)[8], u32x4 (&out)[3]) {
+__device__ __forceinline__ void part8(const float (&e)[8], u32x4 (&out)[3], uint32_t& lost) {
     uint32_t w[3][4];
-    parts_of<TF32, 8>(e, w);
+    parts_of<TF32, 8>(e, w, lost);
 #pragma unroll
     for (int q = 0; q < 3; ++q) out[q] = u32x4{w[q][0], w[q][1], w[q][2], w[q][3]};
 }
 
-__device__ __forceinline__ void part8(const u32x4 (&r)[2], u32x4 (&out)[3]) {
+__device__ __forceinline__ void part8(const u32x4 (&r)[2], u32x4 (&out)[3], uint32_t& lost) {
     float e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(r[i / 4][i % 4]);
-    part8(e, out);
+    part8(e, out, lost);
 }
 
 // One step of 32 of k: the six products of FM x FN fragments. `x(i, f)` and `w(j, f)`
@@ -28,6 +28,7 @@ __device__ __forceinline__ void part8(const u32x4 (&r)[2], u32x4 (&out)[3]) {
 template <int FM, int FN>
 struct PartsAcc {
     f32x4 acc[FM][FN], low[FM][FN];  // upper parts; the small products
+    uint32_t lost = 0;               // (parts_of)
     __device__ __forceinline__ PartsAcc() {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -49,6 +50,15 @@ struct PartsAcc {
 #pragma unroll
             for (int i = 0; i < FM; ++i) acc[i][j] = step_mma<TBF16>(fw[0], fx[i][0], acc[i][j]);
         }
+    }
+    // The sums, in acc: of the parts, and what `again` makes of them where bits were lost.
+    template <class A>
+    __device__ __forceinline__ void join(A again) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] += low[i][j];
+        if (__any(parts_lost(lost))) again(acc);
     }
 };
 
@@ -112,13 +122,24 @@ __global__ __launch_bounds__(Z::THREADS, 3) void ffn_pipe_f32(FfnArgs a, int64_t
             const char* ws = pipe_lds + R * Z::REGION + (BM + wn * TN) * 128;
             const auto read = [&](const char* rows, u32x4(&f)[3]) {
                 const u32x4 r[2] = {*reinterpret_cast<const u32x4*>(rows + f0), *reinterpret_cast<const u32x4*>(rows + f1)};
-                part8(r, f);
+                part8(r, f, s.lost);
             };
             s.step([&](int i, u32x4(&f)[3]) { read(xs + i * 2048, f); },
                    [&](int j, u32x4(&f)[3]) { read(ws + j * 2048, f); });
         });
     }
     __builtin_amdgcn_s_waitcnt(ffn_wait(0));  // no load into LDS outlives its wave
+    s.join([&](f32x4(&acc)[FM][FN]) {
+        const auto x = [&](int row, int i) {
+            const int64_t r = m0 + wm * TM + i * 16 + row;
+            return static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4);
+        };
+        const auto wr = [&](int row, int j) {
+            const int64_t r = n0 + wn * (TN / 2) + j % (FN / 2) * 16 + row;
+            return static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4);
+        };
+        f32_again<1, true, true>(a.k, 0, x, 1, wr, 1, acc);
+    });
     const Out out{a};
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -126,8 +147,7 @@ __global__ __launch_bounds__(Z::THREADS, 3) void ffn_pipe_f32(FfnArgs a, int64_t
         if (row >= a.m) continue;
 #pragma unroll
         for (int j = 0; j < FN / 2; ++j)
-            out.pair(row, n0 + wn * (TN / 2) + j * 16 + 4 * lq, s.acc[i][j] + s.low[i][j],
-                     s.acc[i][j + FN / 2] + s.low[i][j + FN / 2]);
+            out.pair(row, n0 + wn * (TN / 2) + j * 16 + 4 * lq, s.acc[i][j], s.acc[i][j + FN / 2]);
     }
 }
 #undef MM_LDS
@@ -139,6 +159,7 @@ __global__ __launch_bounds__(Z::THREADS, 3) void ffn_pipe_f32(FfnArgs a, int64_t
 // with all CUs at work): fragments come straight into registers (8 elements of a row a
 // lane, a row's 128 bytes by four lanes), the next step's as soon as a fragment has been
 // parted. At the end the partial tiles meet in LDS, summed in the order of the waves.
+// Loads go through buffer resources: pitches up to 2^24 bytes, of 64 rows.
 // ---------------------------------------------------------------------------
 template <class Out, int FM, int FN, int KS>
 __global__ __launch_bounds__(64 * KS, 2) void ffn_waves_f32(FfnArgs a, int64_t tiles) {
@@ -150,58 +171,75 @@ __global__ __launch_bounds__(64 * KS, 2) void ffn_waves_f32(FfnArgs a, int64_t t
     pipe_place<BM, WO>(a, t, &m0, &n0);
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const float* x[FM];  // (rows past the end repeat the last; their sums are not stored)
-    const float* w[FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int64_t r = m0 + i * 16 + lr;
-        x[i] = static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4) + kg * 32 + 8 * lq;
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int64_t r = n0 + j % (FN / 2) * 16 + lr;
-        w[j] = static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4) +
-               kg * 32 + 8 * lq;
-    }
+    // Loads take a lane's row and chunk as an offset, a fragment and a step as a scalar one. Rows
+    // past the end are zeros; a fragment that has none but those reads the first one's.
+    const int ldx = (int)a.ldx, ldw = (int)a.ldw;
+    const int64_t xrows = a.m - m0 < BM ? a.m - m0 : BM, wrows = a.n - n0 < WO ? a.n - n0 : WO;
+    const __amdgpu_buffer_rsrc_t bx = rows_rsrc(a.x, m0, a.ldx, xrows, a.k * 4);
+    const __amdgpu_buffer_rsrc_t bw = rows_rsrc(a.w, n0, a.ldw, wrows, a.k * 4);
+    const __amdgpu_buffer_rsrc_t bu = rows_rsrc(a.w, n0 + a.n, a.ldw, wrows, a.k * 4);
+    const int vox = lr * ldx + 32 * lq, vow = lr * ldw + 32 * lq;
+    const auto at_x = [&](int i) { return i * 16 < xrows ? i * 16 * ldx : 0; };
+    const auto at_w = [&](int j) { return j % (FN / 2) * 16 < wrows ? j % (FN / 2) * 16 * ldw : 0; };
+    int at = kg * 128;  // bytes
     u32x4 rx[FM][2], rw[FN][2];
-    const auto load = [](const float*& p, u32x4(&r)[2]) {  // and on to the next step
-        r[0] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<float, 4>*>(p));
-        r[1] = __builtin_bit_cast(u32x4, *reinterpret_cast<const Pack<float, 4>*>(p + 4));
-        p += 32 * KS;
+    const auto load = [](__amdgpu_buffer_rsrc_t rs, int vo, int so, u32x4(&r)[2]) {
+        r[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, vo, so, 0));
+        r[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, vo + 16, so, 0));
     };
+    const auto load_x = [&](int i) { load(bx, vox, at_x(i) + at, rx[i]); };
+    const auto load_w = [&](int j) { load(j < FN / 2 ? bw : bu, vow, at_w(j) + at, rw[j]); };
     PartsAcc<FM, FN> s;
-    const auto step = [&](auto more_) {
-        const auto take = [&](const float*& p, u32x4(&r)[2], u32x4(&f)[3]) {
-            part8(r, f);
-            if constexpr (decltype(more_)::value) load(p, r);
-        };
-        s.step([&](int i, u32x4(&f)[3]) { take(x[i], rx[i], f); }, [&](int j, u32x4(&f)[3]) { take(w[j], rw[j], f); });
+    const auto step = [&](auto more_) {  // and the next one's loads, each as soon as its registers are free
+        constexpr bool more = decltype(more_)::value;
+        if constexpr (more) at += 128 * KS;
+        s.step(
+            [&](int i, u32x4(&f)[3]) {
+                part8(rx[i], f, s.lost);
+                if constexpr (more) load_x(i);
+            },
+            [&](int j, u32x4(&f)[3]) {
+                part8(rw[j], f, s.lost);
+                if constexpr (more) load_w(j);
+            });
     };
     const int whole = (int)(a.k / 32);
     int left = whole > kg ? (whole - kg + KS - 1) / KS : 0;
     if (left > 0) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) load(x[i], rx[i]);
+        for (int i = 0; i < FM; ++i) load_x(i);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) load(w[j], rw[j]);
+        for (int j = 0; j < FN; ++j) load_w(j);
         for (; left > 1; --left) step(std::true_type{});
         step(std::false_type{});
     }
     if (a.k % 32 && whole % KS == kg) {  // the step that k ends in: zeros behind it, in both operands
         const int valid = (int)(a.k - (int64_t)whole * 32) - 8 * lq;
-        const auto part = [&](const float* p, u32x4(&r)[2]) {
+        const auto part = [&](__amdgpu_buffer_rsrc_t rs, int vo, int so, u32x4(&r)[2]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e / 4][e % 4] = e < valid ? __float_as_uint(p[e]) : 0u;
+            for (int e = 0; e < 8; ++e)
+                r[e / 4][e % 4] = __builtin_amdgcn_raw_buffer_load_b32(rs, e < valid ? vo + 4 * e : (int)kPastEnd, so, 0);
         };
 #pragma unroll
-        for (int i = 0; i < FM; ++i) part(x[i], rx[i]);
+        for (int i = 0; i < FM; ++i) part(bx, vox, at_x(i) + whole * 128, rx[i]);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) part(w[j], rw[j]);
+        for (int j = 0; j < FN; ++j) part(j < FN / 2 ? bw : bu, vow, at_w(j) + whole * 128, rw[j]);
         step(std::false_type{});
     }
+    s.join([&](f32x4(&acc)[FM][FN]) {
+        const auto x = [&](int row, int i) {
+            const int64_t r = m0 + i * 16 + row;
+            return static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4);
+        };
+        const auto w = [&](int row, int j) {
+            const int64_t r = n0 + j % (FN / 2) * 16 + row;
+            return static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4);
+        };
+        f32_again<KS, true, true>(a.k, kg, x, 1, w, 1, acc);
+    });
     __shared__ f32x4 sums[KS][FM * FN][64];
 #pragma unroll
-    for (int f = 0; f < FM * FN; ++f) sums[kg][f][lane] = s.acc[f / FN][f % FN] + s.low[f / FN][f % FN];
+    for (int f = 0; f < FM * FN; ++f) sums[kg][f][lane] = s.acc[f / FN][f % FN];
     __syncthreads();
     const Out out{a};
     for (int u = kg; u < FM * FN / 2; u += KS) {
@@ -256,11 +294,13 @@ hipError_t run_ffn_f32(const FfnArgs& a, hipStream_t s, Launched* L) {
     };
     const float big = us(128, 128, 32, 512, 2.6f, 14.f);
     const float mid = chunked ? us(64, 64, 32, 512, 0.9f, 1.f) : us(64, 64, 32, 512, 1.2f, 3.f);
-    const float four = us(64, 64, 128, 256, 1.6f, 4.f);
+    const bool near = a.ldx <= (1 << 24) && a.ldw <= (1 << 24);  // (a tile within a resource's 31 bits)
+    const float four = near ? us(64, 64, 128, 256, 1.6f, 4.f) : 3e38f;
     // A tile alone on its CU runs at 5/8 of the speed of two.
     const bool pairs = (a.m + 63) / 64 * ((2 * a.n + 127) / 128) > 256;
     const float broad = chunked && pairs ? us(64, 128, 32, 256, 0.74f, 2.f) : 3e38f;
-    const float eight = us(32, 32, 256, 256, 1.78f, 0.8f), wide = us(32, 64, 256, 256, 2.55f, 2.f);
+    const float eight = near ? us(32, 32, 256, 256, 1.78f, 0.8f) : 3e38f;
+    const float wide = near ? us(32, 64, 256, 256, 2.55f, 2.f) : 3e38f;
     const float thin = chunked ? a.m <= 16 ? 0.f : us(32, TRows, 64, 256, 0.2f, 0.5f) : big;
     if (broad <= thin && broad <= big && broad <= mid && broad <= four && broad <= eight && broad <= wide)
         return run_pipe_f32<Out, PipeShape<2, 2, 2, 4, 2>>(a, s, L);

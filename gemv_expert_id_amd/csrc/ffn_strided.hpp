@@ -24,7 +24,7 @@ struct RowFrag {  // 8 neighbouring elements of p of one row
 #pragma unroll
         for (int e = 0; e < 8; ++e) v.v[e] = e < valid ? p[e] : 0.f;
     }
-    __device__ __forceinline__ void parts(u32x4 (&f)[3]) const { part8(v.v, f); }
+    __device__ __forceinline__ void parts(u32x4 (&f)[3], uint32_t& lost) const { part8(v.v, f, lost); }
 };
 struct ColumnFrags {  // 4 neighbouring columns of 8 rows of p
     Pack<float, 4> v[8];
@@ -39,9 +39,9 @@ struct ColumnFrags {  // 4 neighbouring columns of 8 rows of p
             else v[e] = Pack<float, 4>{};
         }
     }
-    __device__ __forceinline__ void parts(int j, u32x4 (&f)[3]) const {
+    __device__ __forceinline__ void parts(int j, u32x4 (&f)[3], uint32_t& lost) const {
         const float e[8] = {v[0].v[j], v[1].v[j], v[2].v[j], v[3].v[j], v[4].v[j], v[5].v[j], v[6].v[j], v[7].v[j]};
-        part8(e, f);
+        part8(e, f, lost);
     }
 };
 
@@ -58,18 +58,17 @@ __global__ __launch_bounds__(64 * KS, FM == 4 ? 1 : 2) void strided_f32(FfnArgs 
     const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ldx = a.ldx / 4, ldw = a.ldw / 4, p0 = kg * 32 + 8 * lq;
     const auto first = [](int64_t at, int64_t end) { return at + 4 <= end ? at : end - 4; };
-    const float* w = static_cast<const float*>(a.w) + p0 * ldw + first(n0 + 4 * lr, a.n);
+    const auto w_col = [&](int c, int j) { return static_cast<const float*>(a.w) + first(n0 + 4 * c, a.n) + j; };
+    const auto x_row = [&](int row, int i) {
+        const int64_t r = m0 + i * 16 + row;
+        return static_cast<const float*>(a.x) + (AT ? first(m0 + 4 * row, a.m) + i : (r < a.m ? r : a.m - 1) * ldx);
+    };
+    const float* w = w_col(lr, 0) + p0 * ldw;
     const float* x[AT ? 1 : FM];
-    if constexpr (AT) {
-        x[0] = static_cast<const float*>(a.x) + p0 * ldx + first(m0 + 4 * lr, a.m);
-    } else {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int64_t r = m0 + i * 16 + lr;
-            x[i] = static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * ldx + p0;
-        }
-    }
+    for (int i = 0; i < (AT ? 1 : FM); ++i) x[i] = x_row(lr, i) + p0 * (AT ? ldx : 1);
     f32x4 acc[FM][4], low[FM][4];  // upper parts; the small products
+    uint32_t lost = 0;             // (parts_of)
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -93,12 +92,12 @@ __global__ __launch_bounds__(64 * KS, FM == 4 ? 1 : 2) void strided_f32(FfnArgs 
         constexpr bool more = decltype(more_)::value;
         u32x4 fw[4][3], fx[3];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) rw.parts(j, fw[j]);
+        for (int j = 0; j < 4; ++j) rw.parts(j, fw[j], lost);
         if constexpr (more) load_w();
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            if constexpr (AT) rx[0].parts(i, fx);
-            else rx[i].parts(fx);
+            if constexpr (AT) rx[0].parts(i, fx, lost);
+            else rx[i].parts(fx, lost);
             if constexpr (more) {
                 if (!AT || i == FM - 1) load_x(i);
             }
@@ -132,8 +131,10 @@ __global__ __launch_bounds__(64 * KS, FM == 4 ? 1 : 2) void strided_f32(FfnArgs 
     }
     __shared__ f32x4 sums[KS][FM * 4][64];
 #pragma unroll
-    for (int f = 0; f < FM * 4; ++f)
-        sums[kg][f][lane] = acc[f / 4][f % 4] + low[f / 4][f % 4];
+    for (int f = 0; f < FM * 4; ++f) acc[f / 4][f % 4] += low[f / 4][f % 4];
+    if (__any(parts_lost(lost))) f32_again<KS, !AT, false>(a.k, kg, x_row, ldx, w_col, ldw, acc);
+#pragma unroll
+    for (int f = 0; f < FM * 4; ++f) sums[kg][f][lane] = acc[f / 4][f % 4];
     __syncthreads();
     // Unit (i, e): row i of a lane's, element e of its four fragments.
     const PlainOut<TF32> out{a};

@@ -6,8 +6,9 @@
 // exact down to 2^-133) and six products of parts, 00 01 10 11 02 20; what is left
 // out is below 2^-24 of a product. 16x16x32 bf16 takes 16 cycles, f32 instructions
 // 256 for the same tile: 96 for the six. The products of upper parts have an
-// accumulator of their own, so the small ones are not rounded away. 16-bit operands
-// are one part.
+// accumulator of their own, so the small ones are not rounded away. Operands with bits
+// below 2^-133 (any below 2^-110) are noticed while they are parted, and the tile's sums
+// are then computed again by f32 instructions (f32_again). 16-bit operands are one part.
 //
 // A group of 4 waves (2 x 2) computes a tile of 32 FM x 32 FN, each wave SUB steps of
 // 32 elements of k an iteration; a block has KS groups, which take different steps
@@ -47,23 +48,152 @@ struct TileArgs {
 template <class T> constexpr int kParts = T::code == 0 ? 3 : 1;
 template <class T> using MmaOf = std::conditional_t<T::code == 1, TF16, TBF16>;
 
-// N elements as their parts, two to a register.
+constexpr uint32_t kUpperHalves = 0x07060302u;  // (v_perm_b32) of two registers
+
+// N elements as their parts, two to a register. `lost` collects what the first two
+// parts leave: the third one holds it unless some of its lower 16 bits are set
+// (parts_lost), as only bits of f32 below 2^-133 are. (One instruction in 12. In
+// assembly that the third part passes through, or the compiler would gather the
+// remainders until later and spill: 160 x 11008 x 4096 in 650 us instead of 287.)
 template <class T, int N>
-__device__ __forceinline__ void parts_of(const typename T::store_t (&e)[N], uint32_t (&out)[kParts<T>][N / 2]) {
+__device__ __forceinline__ void parts_of(const typename T::store_t (&e)[N], uint32_t (&out)[kParts<T>][N / 2],
+                                         uint32_t& lost) {
     if constexpr (T::code == 0) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             float lo = e[2 * i], hi = e[2 * i + 1];
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                out[q][i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+            for (int q = 0; q < 2; ++q) {
+                out[q][i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), kUpperHalves);
                 lo -= __uint_as_float(__float_as_uint(lo) & 0xFFFF0000u);
                 hi -= __uint_as_float(__float_as_uint(hi) & 0xFFFF0000u);
             }
+            out[2][i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), kUpperHalves);
+            asm("v_or3_b32 %0, %2, %3, %0" : "+&v"(lost), "+v"(out[2][i]) : "v"(lo), "v"(hi));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) out[0][i] = (uint32_t)e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
+    }
+}
+
+__device__ __forceinline__ bool parts_lost(uint32_t lost) { return (lost & 0xFFFFu) != 0; }
+
+// Elements 4 g .. 4 g + 3 and 16 + 4 g .. of a step of 32 of a row (`row` at its element
+// 4 g, g = lane / 16 % 4), C contiguous or `stride` apart; with TAIL, zeros from `valid` on.
+template <bool C, bool TAIL>
+__device__ __forceinline__ void row_eight(const float* row, int64_t stride, int valid, float (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (C && !TAIL) {
+            const Pack<float, 4> four = *reinterpret_cast<const Pack<float, 4>*>(row + 16 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * h + e] = four.v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * h + e] = !TAIL || 16 * h + e < valid ? row[(16 * h + e) * (C ? 1 : stride)] : 0.f;
+        }
+    }
+}
+
+// A wave's sums of FM x FN fragments again, by f32 instructions straight from memory, for
+// operands that parts do not hold, where that shows: what is lost of k products is less
+// than k 2^-133 (|x| + |w|), with the largest magnitudes of the two rows, and changes
+// nothing in a sum 2^24 times as large. (The few tiny values among ordinary ones, as
+// gradients behind a gate that is almost shut, cost a look at the rows, 1.5 to 5 times the
+// product; rows of tiny values take 2.5 to 8 times as long.)
+//
+// `x(lr, i)` and `w(lr, j)` point to element 0 of row lr of a fragment, whose elements lie
+// together (XC, WC) or xs (ws) apart; the wave takes every KS-th step of 32 elements from
+// step kg on. Instruction q of 16 elements takes element 4 g + q of lanes 16 g on, in both
+// operands. (The lane is hidden from the compiler, which would otherwise hold the addresses
+// in registers all through the loop before.)
+template <int KS, bool XC, bool WC, int FM, int FN, class X, class W>
+__device__ __forceinline__ void f32_again(int64_t k, int kg, X x, int64_t xs, W w, int64_t ws, f32x4 (&acc)[FM][FN]) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int lr = lane & 15, lq = lane >> 4;
+    const int64_t first = kg * 32 + 4 * lq, whole = k / 32, end = whole * 32;
+    const bool tail = k % 32 && whole % KS == kg;
+    const int valid = (int)(k - end) - 4 * lq;
+    // Largest magnitude of a row.
+    const auto row_top = [&](const float* row, int64_t stride, auto C_) {
+        constexpr bool C = decltype(C_)::value;
+        float top = 0.f, v[8];
+        const float* p = row + first * (C ? 1 : stride);
+#pragma unroll 4
+        for (int64_t s = kg * 32; s < end; s += 32 * KS, p += 32 * KS * (C ? 1 : stride)) {
+            row_eight<C, false>(p, stride, 0, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(v[e]));
+        }
+        if (tail) {
+            row_eight<C, true>(row + (end + 4 * lq) * (C ? 1 : stride), stride, valid, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(v[e]));
+        }
+        top = __builtin_fmaxf(top, __shfl_xor(top, 16, kWave));
+        return __builtin_fmaxf(top, __shfl_xor(top, 32, kWave));
+    };
+    const float least = (float)k * 0x1p-109f;
+    float tops[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) tops[i] = row_top(x(lr, i), xs, std::bool_constant<XC>{});
+    bool shows = false;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const float top = row_top(w(lr, j), ws, std::bool_constant<WC>{});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float up = __shfl(top, 4 * lq + e, kWave);  // of the row of sum e
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                shows |= __builtin_fabsf(acc[i][j][e]) < least * (tops[i] + up) && tops[i] > 0.f && up > 0.f;
+        }
+    }
+    if (!__any(shows)) return;
+    constexpr int JN = FN % 2 ? 1 : 2;  // fragments of w at a time
+#pragma unroll
+    for (int j = 0; j < FN; j += JN) {
+        const float* px[FM];
+        const float* pw[JN];
+        f32x4 sum[FM][JN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            px[i] = x(lr, i) + first * (XC ? 1 : xs);
+#pragma unroll
+            for (int u = 0; u < JN; ++u) sum[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int u = 0; u < JN; ++u) pw[u] = w(lr, j + u) + first * (WC ? 1 : ws);
+        const auto step = [&](auto tail_) {
+            constexpr bool TAIL = decltype(tail_)::value;
+            float fx[FM][8], fw[JN][8];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                row_eight<XC, TAIL>(px[i], xs, valid, fx[i]);
+                px[i] += 32 * KS * (XC ? 1 : xs);
+            }
+#pragma unroll
+            for (int u = 0; u < JN; ++u) {
+                row_eight<WC, TAIL>(pw[u], ws, valid, fw[u]);
+                pw[u] += 32 * KS * (WC ? 1 : ws);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int u = 0; u < JN; ++u)
+                        sum[i][u] = __builtin_amdgcn_mfma_f32_16x16x4f32(fw[u][q], fx[i][q], sum[i][u], 0, 0, 0);
+        };
+#pragma unroll 1
+        for (int64_t s = kg * 32; s < end; s += 32 * KS) step(std::false_type{});
+        if (tail) step(std::true_type{});
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int u = 0; u < JN; ++u) acc[i][j + u] = sum[i][u];
     }
 }
 
@@ -85,6 +215,7 @@ struct TileOperand {
     int64_t ld;
     int shift;               // a piece that passes the end is fetched this many elements earlier
     int some;                // an operand shorter than a piece: elements to fetch one by one (else 0)
+    uint32_t lost = 0;       // (parts_of)
 
     static __device__ __forceinline__ int piece(int i) { return (int)threadIdx.x + i * NT; }
     // Place of this thread's pieces in their rows.
@@ -162,7 +293,7 @@ struct TileOperand {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             uint32_t w[P][V / 2];
-            parts_of<T, V>(v[i].v, w);
+            parts_of<T, V>(v[i].v, w, lost);
             const int r = piece(i) / C, at = place() * 2;
             char* to = lds + r * PITCH + (KC ? at : (((at >> 4) ^ swizzle(r)) << 4) + (at & 15));
 #pragma unroll
@@ -229,12 +360,14 @@ __global__ __launch_bounds__(Z::THREADS, Z::KS > 1 ? Z::KS : 2) void ffn_tile(Ti
     const int64_t m0 = (int64_t)(blockIdx.x / t.tiles_n) * Z::BM, n0 = (int64_t)(blockIdx.x % t.tiles_n) * RO;
     OA a;
     OB b;
-    a.init(t.a, t.lda, m0, t.m, [&](int r) { return m0 + r < t.m ? m0 + r : t.m - 1; });
-    b.init(t.b, t.ldb, n0, t.n, [&](int r) {
+    const auto row_a = [&](int r) { return m0 + r < t.m ? m0 + r : t.m - 1; };
+    a.init(t.a, t.lda, m0, t.m, row_a);
+    const auto row_b = [&](int r) {
         // Gated: each wave column's rows are half gate, half up projection.
         const int64_t col = n0 + (G ? (r / TN) * (TN / 2) + r % (TN / 2) : r);
         return (col < t.n ? col : t.n - 1) + (G && r % TN >= TN / 2 ? t.n : 0);
-    });
+    };
+    b.init(t.b, t.ldb, n0, t.n, row_b);
     f32x4 acc[FM][FN], low[P == 3 ? FM : 1][P == 3 ? FN : 1];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -300,6 +433,15 @@ __global__ __launch_bounds__(Z::THREADS, Z::KS > 1 ? Z::KS : 2) void ffn_tile(Ti
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] += low[i][j];
+        if (__syncthreads_or(parts_lost(a.lost | b.lost))) {
+            const auto x = [&](int r, int i) {
+                return static_cast<const float*>(t.a) + row_a(wm * TM + i * 16 + r) * (AK ? t.lda : 1);
+            };
+            const auto w = [&](int r, int j) {
+                return static_cast<const float*>(t.b) + row_b(wn * TN + j * 16 + r) * (BK ? t.ldb : 1);
+            };
+            f32_again<Z::KS, AK, BK>(t.k, kg, x, t.lda, w, t.ldb, acc);
+        }
     }
     if constexpr (Z::KS > 1) {
         f32x4* part = reinterpret_cast<f32x4*>(tile_lds);

@@ -79,23 +79,29 @@ __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
     const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * 16, ldw = a.ldw / (int64_t)sizeof(S);
-    const S* w = static_cast<const S*>(a.w) + (n0 + lr < a.n ? n0 + lr : a.n - 1);  // columns past the end repeat the last
+    const auto w_col = [&](int c, int) {  // columns past the end repeat the last
+        return static_cast<const S*>(a.w) + (n0 + c < a.n ? n0 + c : a.n - 1);
+    };
+    const S* w = w_col(lr, 0);
+    const auto x_row = [&](int row, int i) {
+        return static_cast<const S*>(a.x) + (i * 16 + row < a.m ? i * 16 + row : a.m - 1) * (a.ldx / (int64_t)sizeof(S));
+    };
     const S* x[FM];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-        x[i] = static_cast<const S*>(a.x) + (i * 16 + lr < a.m ? i * 16 + lr : a.m - 1) * (a.ldx / (int64_t)sizeof(S));
-    f32x4 acc[FM], low[FM];
+    for (int i = 0; i < FM; ++i) x[i] = x_row(lr, i);
+    f32x4 acc[FM][1], low[FM];
+    uint32_t lost = 0;  // (parts_of)
 #pragma unroll
-    for (int i = 0; i < FM; ++i) acc[i] = low[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < FM; ++i) acc[i][0] = low[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     const auto multiply = [&](const S (&ew)[8], const Pack<S, 8> (&ex)[FM]) {
         uint32_t pw[P][4], px[P][4];
-        parts_of<T, 8>(ew, pw);
+        parts_of<T, 8>(ew, pw, lost);
         u32x4 fw[P], fx[P];
 #pragma unroll
         for (int q = 0; q < P; ++q) fw[q] = u32x4{pw[q][0], pw[q][1], pw[q][2], pw[q][3]};
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            parts_of<T, 8>(ex[i].v, px);
+            parts_of<T, 8>(ex[i].v, px, lost);
 #pragma unroll
             for (int q = 0; q < P; ++q) fx[q] = u32x4{px[q][0], px[q][1], px[q][2], px[q][3]};
             if constexpr (P == 3) {
@@ -105,7 +111,7 @@ __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
                 low[i] = step_mma<M>(fw[1], fx[0], low[i]);
                 low[i] = step_mma<M>(fw[0], fx[1], low[i]);
             }
-            acc[i] = step_mma<M>(fw[0], fx[0], acc[i]);
+            acc[i][0] = step_mma<M>(fw[0], fx[0], acc[i][0]);
         }
     };
     const int64_t whole = a.k / 32;  // steps
@@ -137,8 +143,13 @@ __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
         }
         multiply(ew, ex);
     }
+    if constexpr (P == 3) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) part[wave][i][lane] = acc[i] + low[i];
+        for (int i = 0; i < FM; ++i) acc[i][0] += low[i];
+        if (__any(parts_lost(lost))) f32_again<16, true, false>(a.k, wave, x_row, 1, w_col, ldw, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) part[wave][i][lane] = acc[i][0];
     __syncthreads();
     if (wave >= FM) return;
     f32x4 sum = part[0][wave][lane];
