@@ -51,15 +51,6 @@ struct PartsAcc {
             for (int i = 0; i < FM; ++i) acc[i][j] = step_mma<TBF16>(fw[0], fx[i][0], acc[i][j]);
         }
     }
-    // The sums, in acc: of the parts, and what `again` makes of them where bits were lost.
-    template <class A>
-    __device__ __forceinline__ void join(A again) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] += low[i][j];
-        if (__any(parts_lost(lost))) again(acc);
-    }
 };
 
 // ---------------------------------------------------------------------------
@@ -129,17 +120,15 @@ __global__ __launch_bounds__(Z::THREADS, 3) void ffn_pipe_f32(FfnArgs a, int64_t
         });
     }
     __builtin_amdgcn_s_waitcnt(ffn_wait(0));  // no load into LDS outlives its wave
-    s.join([&](f32x4(&acc)[FM][FN]) {
-        const auto x = [&](int row, int i) {
-            const int64_t r = m0 + wm * TM + i * 16 + row;
-            return static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4);
-        };
-        const auto wr = [&](int row, int j) {
-            const int64_t r = n0 + wn * (TN / 2) + j % (FN / 2) * 16 + row;
-            return static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4);
-        };
-        f32_again<1, true, true>(a.k, 0, x, 1, wr, 1, acc);
-    });
+    const auto x_row = [&](int row, int i) {
+        const int64_t r = m0 + wm * TM + i * 16 + row;
+        return static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4);
+    };
+    const auto w_row = [&](int row, int j) {
+        const int64_t r = n0 + wn * (TN / 2) + j % (FN / 2) * 16 + row;
+        return static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4);
+    };
+    f32_join<1, true, true>(a.k, 0, parts_lost(s.lost), x_row, 1, w_row, 1, s.acc, s.low);
     const Out out{a};
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -226,17 +215,15 @@ __global__ __launch_bounds__(64 * KS, 2) void ffn_waves_f32(FfnArgs a, int64_t t
         for (int j = 0; j < FN; ++j) part(j < FN / 2 ? bw : bu, vow, at_w(j) + whole * 128, rw[j]);
         step(std::false_type{});
     }
-    s.join([&](f32x4(&acc)[FM][FN]) {
-        const auto x = [&](int row, int i) {
-            const int64_t r = m0 + i * 16 + row;
-            return static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4);
-        };
-        const auto w = [&](int row, int j) {
-            const int64_t r = n0 + j % (FN / 2) * 16 + row;
-            return static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4);
-        };
-        f32_again<KS, true, true>(a.k, kg, x, 1, w, 1, acc);
-    });
+    const auto x_row = [&](int row, int i) {
+        const int64_t r = m0 + i * 16 + row;
+        return static_cast<const float*>(a.x) + (r < a.m ? r : a.m - 1) * (a.ldx / 4);
+    };
+    const auto w_row = [&](int row, int j) {
+        const int64_t r = n0 + j % (FN / 2) * 16 + row;
+        return static_cast<const float*>(a.w) + ((r < a.n ? r : a.n - 1) + (j >= FN / 2 ? a.n : 0)) * (a.ldw / 4);
+    };
+    f32_join<KS, true, true>(a.k, kg, parts_lost(s.lost), x_row, 1, w_row, 1, s.acc, s.low);
     __shared__ f32x4 sums[KS][FM * FN][64];
 #pragma unroll
     for (int f = 0; f < FM * FN; ++f) sums[kg][f][lane] = s.acc[f / FN][f % FN];

@@ -130,9 +130,7 @@ __global__ __launch_bounds__(64 * KS, FM == 4 ? 1 : 2) void strided_f32(FfnArgs 
         step(std::false_type{});
     }
     __shared__ f32x4 sums[KS][FM * 4][64];
-#pragma unroll
-    for (int f = 0; f < FM * 4; ++f) acc[f / 4][f % 4] += low[f / 4][f % 4];
-    if (__any(parts_lost(lost))) f32_again<KS, !AT, false>(a.k, kg, x_row, ldx, w_col, ldw, acc);
+    f32_join<KS, !AT, false>(a.k, kg, parts_lost(lost), x_row, ldx, w_col, ldw, acc, low);
 #pragma unroll
     for (int f = 0; f < FM * 4; ++f) sums[kg][f][lane] = acc[f / 4][f % 4];
     __syncthreads();

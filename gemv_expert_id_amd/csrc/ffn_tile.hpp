@@ -7,8 +7,9 @@
 // out is below 2^-24 of a product. 16x16x32 bf16 takes 16 cycles, f32 instructions
 // 256 for the same tile: 96 for the six. The products of upper parts have an
 // accumulator of their own, so the small ones are not rounded away. Operands with bits
-// below 2^-133 (any below 2^-110) are noticed while they are parted, and the tile's sums
-// are then computed again by f32 instructions (f32_again). 16-bit operands are one part.
+// below 2^-133 (any below 2^-110) are noticed while they are parted; their sums, and those
+// with infinities, are computed again by f32 instructions (f32_join). 16-bit operands are
+// one part.
 //
 // A group of 4 waves (2 x 2) computes a tile of 32 FM x 32 FN, each wave SUB steps of
 // 32 elements of k an iteration; a block has KS groups, which take different steps
@@ -96,12 +97,15 @@ __device__ __forceinline__ void row_eight(const float* row, int64_t stride, int 
     }
 }
 
-// A wave's sums of FM x FN fragments again, by f32 instructions straight from memory, for
-// operands that parts do not hold, where that shows: what is lost of k products is less
-// than k 2^-133 (|x| + |w|), with the largest magnitudes of the two rows, and changes
-// nothing in a sum 2^24 times as large. (The few tiny values among ordinary ones, as
-// gradients behind a gate that is almost shut, cost a look at the rows, 1.5 to 5 times the
-// product; rows of tiny values take 2.5 to 8 times as long.)
+// The sums of a wave's FM x FN fragments, in acc, from those of upper parts and of the small
+// products; by f32 instructions straight from memory where parts do not give them:
+// - An infinity leaves NaN in the small products.
+// - `lost` says that parts lack bits. What is lost of k products is less than k 2^-133 (|x| +
+//   |w|), with the largest magnitudes of the two rows, and changes nothing in a sum 2^24 times
+//   as large. (A few tiny values among ordinary ones, as gradients behind a gate that is
+//   almost shut, cost a look at the rows, 1.5 to 5 times the product; rows of tiny values
+//   take 2.5 to 8 times as long.) A NaN may be an infinity times a lost value.
+// Each sum goes by its own rows: what others of the wave hold does not change it.
 //
 // `x(lr, i)` and `w(lr, j)` point to element 0 of row lr of a fragment, whose elements lie
 // together (XC, WC) or xs (ws) apart; the wave takes every KS-th step of 32 elements from
@@ -109,7 +113,21 @@ __device__ __forceinline__ void row_eight(const float* row, int64_t stride, int 
 // operands. (The lane is hidden from the compiler, which would otherwise hold the addresses
 // in registers all through the loop before.)
 template <int KS, bool XC, bool WC, int FM, int FN, class X, class W>
-__device__ __forceinline__ void f32_again(int64_t k, int kg, X x, int64_t xs, W w, int64_t ws, f32x4 (&acc)[FM][FN]) {
+__device__ __forceinline__ void f32_join(int64_t k, int kg, bool lost, X x, int64_t xs, W w, int64_t ws, f32x4 (&acc)[FM][FN],
+                                         const f32x4 (&low)[FM][FN]) {
+    uint64_t again = 0;  // the sums to compute, element e of fragment (i, j) at 4 (i FN + j) + e
+    bool nan = false;
+#pragma unroll
+    for (int f = 0; f < FM * FN * 4; ++f) nan |= __builtin_isnan(low[f / 4 / FN][f / 4 % FN][f % 4]);
+    if (__any(nan)) {
+#pragma unroll
+        for (int f = 0; f < FM * FN * 4; ++f)
+            if (__builtin_isnan(low[f / 4 / FN][f / 4 % FN][f % 4]) && __builtin_isinf(acc[f / 4 / FN][f / 4 % FN][f % 4]))
+                again |= 1ull << f;
+    }
+#pragma unroll
+    for (int f = 0; f < FM * FN; ++f) acc[f / FN][f % FN] += low[f / FN][f % FN];
+    if (!__any(lost || again)) return;
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int lr = lane & 15, lq = lane >> 4;
@@ -135,23 +153,25 @@ __device__ __forceinline__ void f32_again(int64_t k, int kg, X x, int64_t xs, W 
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, kWave));
         return __builtin_fmaxf(top, __shfl_xor(top, 32, kWave));
     };
-    const float least = (float)k * 0x1p-109f;
-    float tops[FM];
+    if (__any(lost)) {
+        const float least = (float)k * 0x1p-109f;
+        float tops[FM];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) tops[i] = row_top(x(lr, i), xs, std::bool_constant<XC>{});
-    bool shows = false;
+        for (int i = 0; i < FM; ++i) tops[i] = row_top(x(lr, i), xs, std::bool_constant<XC>{});
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const float top = row_top(w(lr, j), ws, std::bool_constant<WC>{});
+        for (int j = 0; j < FN; ++j) {
+            const float top = row_top(w(lr, j), ws, std::bool_constant<WC>{});
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float up = __shfl(top, 4 * lq + e, kWave);  // of the row of sum e
+            for (int e = 0; e < 4; ++e) {
+                const float up = __shfl(top, 4 * lq + e, kWave);  // of the row of sum e
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                shows |= __builtin_fabsf(acc[i][j][e]) < least * (tops[i] + up) && tops[i] > 0.f && up > 0.f;
+                for (int i = 0; i < FM; ++i)
+                    if (!(__builtin_fabsf(acc[i][j][e]) >= least * (tops[i] + up)) && tops[i] > 0.f && up > 0.f)
+                        again |= 1ull << (4 * (i * FN + j) + e);
+            }
         }
+        if (!__any(again != 0)) return;
     }
-    if (!__any(shows)) return;
     constexpr int JN = FN % 2 ? 1 : 2;  // fragments of w at a time
 #pragma unroll
     for (int j = 0; j < FN; j += JN) {
@@ -193,7 +213,10 @@ __device__ __forceinline__ void f32_again(int64_t k, int kg, X x, int64_t xs, W 
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int u = 0; u < JN; ++u) acc[i][j + u] = sum[i][u];
+            for (int u = 0; u < JN; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (again >> (4 * (i * FN + j + u) + e) & 1) acc[i][j + u][e] = sum[i][u][e];
     }
 }
 
@@ -429,19 +452,14 @@ __global__ __launch_bounds__(Z::THREADS, Z::KS > 1 ? Z::KS : 2) void ffn_tile(Ti
         __syncthreads();
     }
     if constexpr (P == 3) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] += low[i][j];
-        if (__syncthreads_or(parts_lost(a.lost | b.lost))) {
-            const auto x = [&](int r, int i) {
-                return static_cast<const float*>(t.a) + row_a(wm * TM + i * 16 + r) * (AK ? t.lda : 1);
-            };
-            const auto w = [&](int r, int j) {
-                return static_cast<const float*>(t.b) + row_b(wn * TN + j * 16 + r) * (BK ? t.ldb : 1);
-            };
-            f32_again<Z::KS, AK, BK>(t.k, kg, x, t.lda, w, t.ldb, acc);
-        }
+        const bool lost = __syncthreads_or(parts_lost(a.lost | b.lost));
+        const auto x = [&](int r, int i) {
+            return static_cast<const float*>(t.a) + row_a(wm * TM + i * 16 + r) * (AK ? t.lda : 1);
+        };
+        const auto w = [&](int r, int j) {
+            return static_cast<const float*>(t.b) + row_b(wn * TN + j * 16 + r) * (BK ? t.ldb : 1);
+        };
+        f32_join<Z::KS, AK, BK>(t.k, kg, lost, x, t.lda, w, t.ldb, acc, low);
     }
     if constexpr (Z::KS > 1) {
         f32x4* part = reinterpret_cast<f32x4*>(tile_lds);

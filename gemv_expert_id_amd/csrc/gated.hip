@@ -89,10 +89,10 @@ __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
     const S* x[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i) x[i] = x_row(lr, i);
-    f32x4 acc[FM][1], low[FM];
+    f32x4 acc[FM][1], low[FM][1];
     uint32_t lost = 0;  // (parts_of)
 #pragma unroll
-    for (int i = 0; i < FM; ++i) acc[i][0] = low[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < FM; ++i) acc[i][0] = low[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     const auto multiply = [&](const S (&ew)[8], const Pack<S, 8> (&ex)[FM]) {
         uint32_t pw[P][4], px[P][4];
         parts_of<T, 8>(ew, pw, lost);
@@ -105,11 +105,11 @@ __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
 #pragma unroll
             for (int q = 0; q < P; ++q) fx[q] = u32x4{px[q][0], px[q][1], px[q][2], px[q][3]};
             if constexpr (P == 3) {
-                low[i] = step_mma<M>(fw[2], fx[0], low[i]);
-                low[i] = step_mma<M>(fw[0], fx[2], low[i]);
-                low[i] = step_mma<M>(fw[1], fx[1], low[i]);
-                low[i] = step_mma<M>(fw[1], fx[0], low[i]);
-                low[i] = step_mma<M>(fw[0], fx[1], low[i]);
+                low[i][0] = step_mma<M>(fw[2], fx[0], low[i][0]);
+                low[i][0] = step_mma<M>(fw[0], fx[2], low[i][0]);
+                low[i][0] = step_mma<M>(fw[1], fx[1], low[i][0]);
+                low[i][0] = step_mma<M>(fw[1], fx[0], low[i][0]);
+                low[i][0] = step_mma<M>(fw[0], fx[1], low[i][0]);
             }
             acc[i][0] = step_mma<M>(fw[0], fx[0], acc[i][0]);
         }
@@ -144,9 +144,7 @@ __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
         multiply(ew, ex);
     }
     if constexpr (P == 3) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) acc[i][0] += low[i];
-        if (__any(parts_lost(lost))) f32_again<16, true, false>(a.k, wave, x_row, 1, w_col, ldw, acc);
+        f32_join<16, true, false>(a.k, wave, parts_lost(lost), x_row, 1, w_col, ldw, acc, low);
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) part[wave][i][lane] = acc[i][0];

@@ -610,10 +610,10 @@ typedef struct {
 
 /*
  * Forward: [G U] = x . w^T in f32, h = act(G) * U from the f32 sums, rounded
- * once. f32 operands may be multiplied in three bf16 parts: a sum that holds an
- * infinity is then NaN where it would be infinite. (Parts hold no bits below 2^-133; sums
- * in which that shows are computed again in f32, 2.5 to 8 times as slowly.) pre is
- * optional ({NULL, 0}): [G U] rounded to the dtype, for the backward pass.
+ * once. f32 operands may be multiplied in three bf16 parts; sums that these do not
+ * give, of infinities and of values below 2^-110, are computed again in f32, 2.5 to 8
+ * times as slowly. pre is optional ({NULL, 0}): [G U] rounded to the dtype, for the
+ * backward pass.
  */
 mm_status mm_gated(const mm_gated_params *params, mm_buf x, mm_buf w, mm_buf h, mm_buf pre,
                    void *stream, mm_receipt *receipt);
