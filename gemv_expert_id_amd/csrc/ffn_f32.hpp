@@ -58,7 +58,7 @@ struct PartsAcc {
 // 128 bytes are one step): LDS holds the raw 4 bytes an element, loads go there without
 // a register, and each wave parts the fragments that it reads. Blocks share a CU: one's
 // loads and barriers fall into the others' arithmetic. Bound by vector issue: parting is
-// 176 of the 211 vector instructions a wave issues for 24 matrix instructions.
+// 192 of the 227 vector instructions a wave issues for 24 matrix instructions.
 // ---------------------------------------------------------------------------
 #define MM_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 template <class Out, class Z>
@@ -261,16 +261,19 @@ hipError_t run_ffn_waves(const FfnArgs& a, hipStream_t s) {
 // tiles at a time on the 256 CUs; and what a round of them costs in us, for each
 // iteration and at its start. From 150 products of 65 to 4096 tokens in every form; the
 // one with the lowest sum of rounds is within 3% of the fastest in the mean (9% where
-// rows are not whole 16-byte chunks). Few tokens take f32 instructions, at 2/5 of the
-// rate of the six products but with nothing to part. Both sides of some borders, us:
-// 70 tokens by 1200 over 8000, thin 33.8, 32 x 32 57.3; 256 by the same, 32 x 64 86, thin
-// 98, 32 x 32 112; 70 by 2816 over 2048, thin 19.8, 32 x 64 25.3; 70 by 24000 over
-// 1000, 64 x 64 by four waves 47.8, 64 x 128 49.7; 400 by 22016 over 4096, 64 x 128 455, 64 x 64
-// through LDS 537, by four waves 575, 128 x 128 548; 509 by 2816 over 2048, 64 x 64
-// through LDS 53.6, by four waves 61.8, 128 x 128 124; 4096 by 8192 over 4096, 128 x 128
-// 1392, 64 x 64 through LDS 1756.
-// Bound by arithmetic from 512 tokens on: 4096 x 8192 over 4096 runs at 197 TFLOP/s, six
-// times that in the matrix units; 509 by 2816 over 2048 at 106, for 352 tiles of 512.
+// rows are not whole 16-byte chunks); measured before parting looked for lost bits, which
+// costs 64 x 64 by four waves up to a tenth and the others 1 to 7%. Few tokens take f32
+// instructions, at 2/5 of the rate of the six products but with nothing to part. Both sides
+// of some borders, us: 70 tokens by 1200 over 8000, thin 33.1, 32 x 32 57.6; 256 by the
+// same, thin 73.7, 32 x 64 86.3, 32 x 32 112; 70 by 2816 over 2048, thin 21.0, 32 x 64 24.9;
+// 70 by 24000 over 1000, 64 x 64 by four waves 48.1, through LDS 49.2, 64 x 128 51.9; 400
+// by 22016 over 4096, 64 x 128 506, 64 x 64 through LDS 571, by four waves 587, 128 x 128
+// 587; 509 by 2816 over 2048, 64 x 64 through LDS 58.9, by four waves 62.8, 128 x 128 126;
+// 4096 by 8192 over 4096, 128 x 128 1438, 64 x 64 through LDS 1804. Taken although slower:
+// by four waves, 64 x 64 through LDS beside it, 160 by 22016 over 4096 291 and 276, 160 by
+// 8192 over 11008 323 and 310, 1000 by 1200 over 8000 229 and 216.
+// Bound by arithmetic from 512 tokens on: 4096 x 8192 over 4096 runs at 191 TFLOP/s, six
+// times that in the matrix units; 509 by 2816 over 2048 at 100, for 352 tiles of 512.
 template <class Out>
 hipError_t run_ffn_f32(const FfnArgs& a, hipStream_t s, Launched* L) {
     const bool chunked = ffn_chunked(a, 4);

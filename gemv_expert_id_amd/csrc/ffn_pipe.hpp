@@ -198,8 +198,8 @@ __global__ __launch_bounds__(64 * TWaves) void ffn_thin(FfnArgs a, int tiles_m) 
 // The largest tile, 8 waves of 128 x 64, is bound by LDS and power together: a pair is
 // 2048 cycles of matrix instructions and, at 128 bytes a cycle, 1536 of fragment reads
 // and 512 of loads, at 1750 to 2050 MHz under this load. 8192 x 8192 over 8192: 808 us in
-// bf16 (1360 TFLOP/s), 461 in codes (2390 TOP/s). Few tiles are bound by memory: 48 tokens
-// by 22016 x 4096 bf16 take 43.5 us, 4.2 TB/s.
+// bf16 (1360 TFLOP/s), 466 in codes (2360 TOP/s). Few tiles are bound by memory: 48 tokens
+// by 22016 x 4096 bf16 take 41.4 us, 4.4 TB/s.
 //
 // XK, WK = false (16-bit gradients' products): the operand is stored with the
 // contraction along its rows, element (i, p) at p * ld + i. Its region holds the
@@ -483,10 +483,14 @@ inline bool ffn_chunked(const FfnArgs& a, int es) {
 }
 
 // 8 stages in LDS from 32 on, unless the last turn of the ring would be more than a
-// twelfth in vain or, of 32 tokens (12 KB a stage), CUs have more than a tile; 4 otherwise. us, 4 and 8: f16 1 by 8192 x 11008, 86 stages, 39.1
-// and 35.8; 1 by 1200 x 8000, 63, 10.7 and 7.8; f32 1 by 4096 x 8192, 128, 37.4 and 31.9;
-// codes 13 by 4099 x 11008, 43 in turns of 48, 11.3 and 13.2; 1 by 22016 x 4096, 16, 17.5 and
-// 20.2; f32 32 by 4096 x 8192, 45.8 and 36.7, by 22016 x 4096 91.5 and 104.9.
+// twelfth in vain or, of 32 tokens (12 KB a stage), CUs have more than a tile; 4 otherwise.
+// us, 4 and 8: f16 1 by 8192 rows, 16 stages 7.7 and 7.7, 24 10.0 and 9.8, 28 11.0 and
+// 11.2, 32 12.0 and 12.0, 40 14.3 and 14.1, 64 30.2 and 28.9, 86 38.8 and 36.0; 1 by 1200,
+// 24 5.1 and 5.2, 28 5.3 and 5.6, 32 6.7 and 5.7, 63 10.7 and 7.8; f32 16 by 4096, 24 7.5 and
+// 7.1, 32 8.7 and 8.3, 128 38.0 and 30.7; 1 by 22016, 32 35.4 and 36.4, 64 67.8 and 65.6;
+// codes 1 by 22016, 16 15.0 and 17.8, 32 35.0 and 34.0; 13 by 4099, 43 in turns of 48 11.4
+// and 13.2, but 32 8.0 and 9.9; f32 32 by 4096, 128 44.9 and 38.1, by 22016, 64 91.5 and
+// 104.9.
 template <class Out, int FM>
 hipError_t run_ffn_thin(const FfnArgs& a, hipStream_t s) {
     constexpr int XR = ThinShape<FM>::XR, WO = Out::kGated ? TRows / 2 : TRows, es = sizeof(typename Out::E::store_t);
@@ -529,13 +533,13 @@ hipError_t run_ffn_pipe_halves(const FfnArgs& a, hipStream_t s) {
 // CUs, and what a round of them costs in us, for each 128 bytes of k and at its
 // start. From 150 products of 1 to 8192 tokens in bf16 and codes, each in every form;
 // the form with the lowest sum of rounds is within 3% of the fastest one in the
-// mean. Both sides of some borders (us): 48 tokens by 22016 x 4096 bf16, 64 x 128
-// tiles 44.2, 64 x 64 49.7, 128 x 128 45.5; 512 by 2816 x 2048 codes, 64 x 128 9.3,
-// 64 x 64 10.2, 128 x 128 13.2; 1024 by 22016 x 4096 bf16, 256 x 128 179, 256 x 256
-// 214; 2048 by the same, 349 and 323; 32 by 1152 x 1792 bf16, 32 x 16 6.1, 64 x 64 7.8.
-// Up to 16 tokens take the thinnest: 1 by 22016 x 4096 f16 35.1, 64 x 128 38.3; 1 by
-// 8192 x 11008, 38.5, 64 x 64 51; the one loss found is 16 by 28672 x 4096 codes, 25.7
-// and 24.7.
+// mean. Both sides of some borders (us, all from one run): 48 tokens by 22016 x 4096
+// bf16, 64 x 128 tiles 43.9, 64 x 64 47.5, 128 x 128 45.1; 512 by 2816 x 2048 codes, 64 x
+// 128 9.4, 64 x 64 10.6, 128 x 128 13.0; 1024 by 22016 x 4096 bf16, 256 x 256 with its last
+// round in halves 173, 256 x 128 182; 2048 by the same, 329 and 354; 32 by 1152 x 1792
+// bf16, 32 x 16 5.4, 64 x 64 7.5. Up to 16 tokens take the thinnest: 1 by 22016 x 4096
+// f16 35.0, 64 x 128 38.6; 1 by 8192 x 11008, 35.1, 64 x 64 51.1; 16 by 28672 x 4096 codes,
+// 25.6, 64 x 64 26.0.
 struct FfnForm {
     int tokens, rows, at_a_time;
     float pair_us, round_us;

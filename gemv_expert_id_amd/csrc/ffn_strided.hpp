@@ -10,7 +10,7 @@
 // end repeat the last four (their sums are the same and are stored twice, or not at all).
 // Each of a block's KS waves computes the whole tile over every KS-th step of 32 of p;
 // the partial tiles meet in LDS at the end, summed in the order of the waves. Bound by
-// parting and multiplying in turn: 2000 x 4098 over 10000 144 TFLOP/s, 152 transposed.
+// parting and multiplying in turn: 2000 x 4098 over 10000 142 TFLOP/s, 145 transposed.
 #pragma once
 
 #include "ffn_f32.hpp"
@@ -160,10 +160,11 @@ hipError_t run_strided(const FfnArgs& a, hipStream_t s) {
 
 // The forms of f32 and what a round of their tiles costs in us, as for the rows of W
 // (ffn_f32.hpp). Both sides of some borders, us: dpre . w 70 x 4098 over 10000, 32 x 64
-// here 75, 64 x 64 here 134, 128 x 64 through LDS 146; 2000 x 4098 by the same, 64 x 64 here
-// 1140, 128 x 64 1426; 2000 x 8000 over 1200, 320 and 287; 600 x 500 over 8192, 32 x 64 57,
-// 16 x 64 80, 128 x 64 95; 16 x 8000 over 1200, 16 x 64 10.0, 32 x 64 12.8, 32 x 32 13.5.
-// dpre^T . x 2816 x 2048 over 2000, 64 x 64 here 159, 128 x 64 198; over 200, 43.9 and 33.7.
+// here 76.5, 16 x 64 122, 64 x 64 134, 32 x 32 through LDS 190; 2000 x 4098 by the same,
+// 64 x 64 here 1156, 32 x 64 1235, 128 x 64 through LDS 1449; 2000 x 8000 over 1200, 128 x
+// 64 287, 64 x 64 here 326; 600 x 500 over 8192, 32 x 64 58.9, 16 x 64 80.8, 64 x 64 109;
+// 16 x 8000 over 1200, 16 x 64 8.3, 32 x 64 10.8, 32 x 32 11.8. dpre^T . x 2816 x 2048 over
+// 2000, 64 x 64 here 169, 128 x 64 205; over 200, 42.7 and 29.3.
 template <bool AT>
 hipError_t run_f32_product(const FfnArgs& a, hipStream_t s) {
     const auto us = [&](int bm, int bn, int kt, int at_a_time, float step, float start) {

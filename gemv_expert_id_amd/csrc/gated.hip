@@ -65,11 +65,13 @@ __global__ __launch_bounds__(256) void gated_grad(FfnArgs a, int sh) {
 // contraction, read both operands straight into fragments, DEP steps in flight, and are
 // summed in order through LDS. A wave's lanes hold 8 rows of w at a column each, so w's
 // loads are single elements: 16 neighbours a row. Bound by the CU's own load path, for
-// few blocks share one contraction. us, here and in the narrowest tiles: f32 8 x 49 over
-// 21376 55.0 and 154.4, 16 x 1024 over 8198 32.1 and 60.9, 32 x 64 over 2000 11.1 and
-// 16.9, 32 x 130 over 600 9.8 and 7.4; bf16 8 x 49 over 21376 35.1 and 90.0, 16 x 4096
-// over 22016 120.7 and 124.8, 32 x 1024 over 8198 30.3 and 35.6, 32 x 256 over 4096 15.0
-// and 15.2, 16 x 1601 over 700 6.8 and 5.8.
+// few blocks share one contraction: 3.5 times what the bytes of w take, as are the forms
+// beside it. us, here and in the form that would be taken else: f32 8 x 49 over 21376 53.7
+// and 88.6, 16 x 1024 over 8198 29.0 and 36.4, 32 x 64 over 2000 8.8 and 9.7, 32 x 130 over
+// 600 7.8 and 4.7; bf16 8 x 49 over 21376 33.9 and 86.9, 16 x 4096 over 22016 119 and 122,
+// 32 x 1024 over 8198 28.4 and 33.8, 32 x 256 over 4096 12.4 and 13.9, 16 x 1601 over 700
+// 5.3 and 4.8. Taken although slower: 16 x 4096 over 8192 f16 40.3 and 32.0, over 4096
+// bf16 20.4 and 16.5.
 template <class T, int FM>
 __global__ __launch_bounds__(1024) void long_product(FfnArgs a) {
     using S = typename T::store_t;
@@ -188,15 +190,19 @@ hipError_t chunked_product(const GemmArgs& g, const FfnArgs& o, int64_t tiles, b
 
 }  // namespace
 
-// dpre . w (both as stored: NN) or dpre^T . x (TN). Products whose contraction the
-// pipelined GEMM takes whole go to it, and large TN ones of any contraction (it reads
-// zeros past the end), unless the tiles here leave fewer CUs idle in their last round;
-// others take the forms here: pipelined ones where rows hold whole 16-byte pieces and
-// 128 x 128 tiles are more than 64, tiles of any alignment else. us, f16, GEMM and here:
-// 4096 x 4096 over 4096, 111 and 129; 3001 x 2048 over 2816, 48.6 and 42.2, over 11008,
-// 177 and 136; 11008 x 2048 over 1024 transposed, 344 tiles of 256 x 256, 75.5 and 66.5,
-// 22016 x 4096 over 4096, 1376 tiles, 710 and 810;
-// 512 x 2048 over 2816, 64 tiles, any alignment 20.1, pipelined 22.4, GEMM 20.5.
+// dpre . w (both as stored: NN) or dpre^T . x (TN), of dpre as it was rounded: it is an
+// output that a caller keeps, and in 16 bits one matrix instruction takes it where two
+// parts would need two. That adds to the error: 0.0023 of the norm in bf16, where unrounded
+// dpre gives 0.0017 (the rounding of dx and dw themselves); 0.00029 and 0.00021 in f16.
+//
+// Products whose contraction the pipelined GEMM takes whole go to it, and large TN ones of
+// any contraction (it reads zeros past the end), unless the tiles here leave fewer CUs idle
+// in their last round; others take the forms here: pipelined ones where rows hold whole
+// 16-byte pieces and 128 x 128 tiles are more than 64, tiles of any alignment else. us,
+// f16, GEMM and here: 4096 x 4096 over 4096, 111 and 129; 3001 x 2048 over 2816, 48.6 and
+// 42.2, over 11008, 177 and 136; 11008 x 2048 over 1024 transposed, 344 tiles of 256 x 256,
+// 75.5 and 66.5, 22016 x 4096 over 4096, 1376 tiles, 710 and 810; 512 x 2048 over 2816, 64
+// tiles, any alignment 20.1, pipelined 22.4, GEMM 20.5.
 hipError_t launch_gated_product(const GemmArgs& g, hipStream_t s, Launched* L) {
     const auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const int64_t es = g.dtype == 0 ? 4 : 2;
