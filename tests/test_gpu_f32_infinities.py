@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import gemv_expert_id_amd as mm
-from test_gpu_f32_small import PRODUCTS, bound, products
+from test_gpu_f32_small import PRODUCTS, bound, near, products
 from test_gpu_ffn import F32_SHAPES, GATES, Rows, randn, stream
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,15 @@ def test_products(m, n, k):
         d = dpre.t.contiguous()
         same(dx.t, d, w.t().contiguous(), 2 * n, "dx")
         same(dw.t, d.t().contiguous(), x.t().contiguous(), m, "dw")
+
+
+@pytest.mark.parametrize("m,n,k", F32_SHAPES)
+def test_largest_numbers(m, n, k):
+    """The largest numbers of f32, as masks hold them, among ordinary ones: finite sums stay finite."""
+    top = torch.finfo(torch.float32).max
+    x, w = randn(1, m, k), (randn(2, 2 * n, k) * 2.0 ** -14).clamp(-2.0 ** -13, 2.0 ** -13)
+    x[::3, 0], x[1::3, k // 2], x[2::5, -1] = -top, top, -top
+    for pad in ((4, 1) if k % 4 == 0 else (1,)):
+        for a, b in ((x, w), (w[:1].expand(m, k).contiguous(), x[:1].expand(2 * n, k).contiguous())):
+            want, absolute = products(a, b)
+            near(forward(a, b, m, n, k, pad), want, bound(want, absolute, k), "pre")
