@@ -26,7 +26,7 @@
 //
 // Large f32 products: 4096 x 8192 over 4096 takes 1430 us, 192 TFLOP/s, 1150 of bf16
 // products. Matrix units are busy for 54% of the cycles, vector instructions issue in 46%,
-// LDS conflicts take 27%; the 128 x 128 tile holds 256 registers and spills 32 more. Rows
+// LDS conflicts take 27%; the 128 x 128 tile holds 256 registers and spills 35 more. Rows
 // of 16 bits that no pipelined form takes are bound by the staging through registers
 // (2000 x 4100 over 10000 bf16 344 us, 477 TFLOP/s).
 #pragma once
@@ -103,12 +103,14 @@ __device__ __forceinline__ void row_eight(const float* row, int64_t stride, int 
 // The sums of a wave's FM x FN fragments, in acc, from those of upper parts and of the small
 // products; by f32 instructions straight from memory where parts do not give them:
 // - An infinity leaves NaN in the small products.
-// - `lost` says that parts lack bits. What is lost of k products is less than k 2^-133 (|x| +
-//   |w|), with the largest magnitudes of the two rows, and changes nothing in a sum 2^24 times
-//   as large. (A few tiny values among ordinary ones, as gradients behind a gate that is
-//   almost shut, cost a look at the rows, 1.5 to 5 times the product; rows of tiny values
-//   take 2.5 to 8 times as long.) A NaN may be an infinity times a lost value.
-// Each sum goes by its own rows: what others of the wave hold does not change it.
+// - `lost` says that parts of some rows lack bits; a look at the rows finds them. What is
+//   lost of k products is less than k 2^-133 (|x| + |w|), with the largest magnitudes of the
+//   two rows, and changes nothing in a sum 2^24 times as large. (A few tiny values among
+//   ordinary ones, as gradients behind a gate that is almost shut, cost the look, 1.7 to 4
+//   times the product; rows of tiny values take 2.5 to 6.5 times as long.) A NaN may be an
+//   infinity times a lost value.
+// Each sum goes by its own rows: what others of the wave hold does not change it, and
+// neighbouring tiles that both store a sum store the same.
 //
 // `x(lr, i)` and `w(lr, j)` point to element 0 of row lr of a fragment, whose elements lie
 // together (XC, WC) or xs (ws) apart; the wave takes every KS-th step of 32 elements from
@@ -137,39 +139,56 @@ __device__ __forceinline__ void f32_join(int64_t k, int kg, bool lost, X x, int6
     const int64_t first = kg * 32 + 4 * lq, whole = k / 32, end = whole * 32;
     const bool tail = k % 32 && whole % KS == kg;
     const int valid = (int)(k - end) - 4 * lq;
-    // Largest magnitude of a row.
-    const auto row_top = [&](const float* row, int64_t stride, auto C_) {
+    // Largest magnitude of a row, and which of the 16 rows (bit lr) hold bits below 2^-133:
+    // numbers below 2^-110 that are no multiple of it.
+    struct Row {
+        float top;
+        uint32_t lack;
+    };
+    const auto look = [&](const float* row, int64_t stride, auto C_) {
         constexpr bool C = decltype(C_)::value;
         float top = 0.f, v[8];
+        bool lack = false;
+        const auto take = [&] {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = __builtin_fabsf(v[e]), units = a * 0x1p66f * 0x1p67f;
+                top = __builtin_fmaxf(top, a);
+                lack |= a < 0x1p-110f && units != __builtin_truncf(units);
+            }
+        };
         const float* p = row + first * (C ? 1 : stride);
 #pragma unroll 4
         for (int64_t s = kg * 32; s < end; s += 32 * KS, p += 32 * KS * (C ? 1 : stride)) {
             row_eight<C, false>(p, stride, 0, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(v[e]));
+            take();
         }
         if (tail) {
             row_eight<C, true>(row + (end + 4 * lq) * (C ? 1 : stride), stride, valid, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(v[e]));
+            take();
         }
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, kWave));
-        return __builtin_fmaxf(top, __shfl_xor(top, 32, kWave));
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32, kWave));
+        const uint64_t all = __ballot(lack);
+        const uint32_t half = (uint32_t)(all | all >> 32);
+        return Row{top, (half | half >> 16) & 0xFFFFu};
     };
     if (__any(lost)) {
         const float least = (float)k * 0x1p-109f;
-        float tops[FM];
+        Row rx[FM];
 #pragma unroll
-        for (int i = 0; i < FM; ++i) tops[i] = row_top(x(lr, i), xs, std::bool_constant<XC>{});
+        for (int i = 0; i < FM; ++i) rx[i] = look(x(lr, i), xs, std::bool_constant<XC>{});
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const float top = row_top(w(lr, j), ws, std::bool_constant<WC>{});
+            const Row rw = look(w(lr, j), ws, std::bool_constant<WC>{});
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float up = __shfl(top, 4 * lq + e, kWave);  // of the row of sum e
+                const int r = 4 * lq + e;  // the row of sum e
+                const float up = __shfl(rw.top, r, kWave);
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
-                    if (!(__builtin_fabsf(acc[i][j][e]) >= least * (tops[i] + up)) && tops[i] > 0.f && up > 0.f)
+                    if (((rx[i].lack >> lr | rw.lack >> r) & 1) && rx[i].top > 0.f && up > 0.f &&
+                        !(__builtin_fabsf(acc[i][j][e]) >= least * (rx[i].top + up)))
                         again |= 1ull << (4 * (i * FN + j) + e);
             }
         }

@@ -611,7 +611,7 @@ typedef struct {
 /*
  * Forward: [G U] = x . w^T in f32, h = act(G) * U from the f32 sums, rounded
  * once. f32 operands may be multiplied in three bf16 parts; sums that these do not
- * give, of infinities and of values below 2^-110, are computed again in f32, 2.5 to 8
+ * give, of infinities and of values below 2^-110, are computed again in f32, 2.5 to 6.5
  * times as slowly. pre is optional ({NULL, 0}): [G U] rounded to the dtype, for the
  * backward pass.
  */

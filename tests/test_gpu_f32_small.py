@@ -120,3 +120,48 @@ def test_small_recomputed(m, n, k):
         # of act(G), G tiny: its slope, 12 roundings (a sigmoid next to 1/2 and two products), and three below 2^-126
         e[:, n:] = dh.abs().double() * (ref.SLOPE * ep[:, :n] + 12 * U * ref.act(pre[:, :n], GATES[m % 2]).abs() + 3 * 2.0 ** -150)
         near(dpre.t, want, e + U * (want.abs() + e), "dpre")
+
+
+def with_lost(t):
+    """Values with bits below 2^-133 in every seventh row, one ordinary row of them."""
+    t = t.clone()
+    t[3::7] = scaled(77, *t.shape, -120)[3::7]
+    t[4::14, -1] = 2.0 ** -130 + 2.0 ** -140
+    return t
+
+
+@pytest.mark.parametrize("m,n,k", F32_SHAPES)
+def test_other_sums_keep_their_bits(m, n, k):
+    """Sums whose own operands the parts hold, ordinary ones and small ones, do not change with other rows and columns."""
+    for pad in ((4, 1) if k % 4 == 0 else (1,)):
+        x, w = randn(1, m, k), randn(2, 2 * n, k)
+        x[::2] *= 2.0 ** -103
+        x[::2] = (x[::2].view(torch.int32) & ~0xFF).view(torch.float32)  # 16 bits, from 2^-118 on above 2^-133
+        x[::2] = torch.where(x[::2].abs() < 2.0 ** -117, torch.zeros_like(x[::2]), x[::2])
+        first = None
+        for a, b in ((x, w), (with_lost(x), w), (x, with_lost(w))):
+            X, W = Rows(m, k, torch.float32, k + pad, value=a), Rows(2 * n, k, torch.float32, k + pad, value=b)
+            h, pre = Rows(m, n, torch.float32), Rows(m, 2 * n, torch.float32)
+            mm.mm_gated(mm.gated_params(0, m, n, k, ldx=X.ld, ldw=W.ld), X.buf, W.buf, h.buf, pre.buf, stream=stream())
+            first = pre.t if first is None else first
+            kept = (a == x).all(1)[:, None] & (b == w).all(1)[None]
+            assert torch.equal(pre.t[kept], first[kept]), "other sums have changed"
+
+
+@pytest.mark.parametrize("m,n,k", PRODUCTS)
+def test_other_gradients_keep_their_bits(m, n, k):
+    """As above for dx, by columns of w, and dw, by columns of x; a call gives the same bits again."""
+    pre, dh, x, w = randn(1, m, 2 * n), randn(2, m, n) * 2.0 ** -99, randn(3, m, k), randn(4, 2 * n, k)
+    outs = []
+    for a, b in ((x, w), (with_lost(x.t()).t().contiguous(), with_lost(w.t()).t().contiguous())):
+        for _ in range(2):
+            dpre, dx, dw = Rows(m, 2 * n, torch.float32), Rows(m, k, torch.float32), Rows(2 * n, k, torch.float32)
+            X, W = Rows(m, k, torch.float32, value=a), Rows(2 * n, k, torch.float32, value=b)
+            P, D = Rows(m, 2 * n, torch.float32, value=pre), Rows(m, n, torch.float32, value=dh)
+            mm.mm_gated_grad(mm.gated_params(0, m, n, k), X.buf, W.buf, P.buf, D.buf, dpre.buf, dx.buf, dw.buf, stream=stream())
+            outs.append((dx.t, dw.t, (b == w).all(0), (a == x).all(0)))
+    for i in range(0, 4, 2):
+        assert torch.equal(outs[i][0], outs[i + 1][0]) and torch.equal(outs[i][1], outs[i + 1][1]), "differs from call to call"
+    for i in (0, 1):
+        kept = outs[2][2 + i]
+        assert torch.equal(outs[0][i][:, kept], outs[2][i][:, kept]), "other columns have changed"
