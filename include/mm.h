@@ -12,7 +12,9 @@
  *   scratch.)
  * - Buffers are passed as mm_buf {ptr, bytes}: a device pointer and the
  *   number of bytes the caller vouches for from that pointer. Every call
- *   checks that the bytes it will touch lie inside [ptr, ptr + bytes).
+ *   checks that the bytes it will touch lie inside [ptr, ptr + bytes). (A load
+ *   of an odd number of 16-bit elements may take the rest of the aligned four
+ *   bytes that hold the last one; their value does not matter.)
  * - Fail-closed: each call validates everything on the host before it
  *   enqueues anything (mlx-native dense_matmul_id.rs, `dense_matmul_id`:
  *   every pipeline is resolved and every limit checked before encoding; test
